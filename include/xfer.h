@@ -272,6 +272,27 @@ int xfer_run_batch(xfer_conn* const* conns, const void* const* src, void* const*
 int xfer_run_messages(xfer_conn* c, const void* src, void* dst, const size_t* offsets,
                       const size_t* sizes, int n, void* stream);
 
+/* xfer_run_blocks: one transfer of n blocks named by two lists in DEVICE
+ * memory, in one launch: entry i moves block from[i] of the pool src (of
+ * src_blocks blocks of block_bytes) to block to[i] of the pool dst (of
+ * dst_blocks).  The lists may be the output of earlier work on the stream.
+ * Partition, steps, counters and FIFO bytes are those of xfer_run on the
+ * n * block_bytes bytes that the entries make up in order.
+ *   An entry with either id outside its pool (a padded list's -1) moves
+ *   nothing: it still counts in the partition, and the FIFO carries zeros
+ *   for it.  The ids in `to` that are inside must differ: channels reach
+ *   entries at different times, so what a block named twice holds afterwards
+ *   is a mix of both.
+ *   c            a SIMPLE (any FIFO) or ZEROCOPY_DIRECT connection.
+ *   block_bytes  a multiple of 16, at most 1 GiB.
+ *   src, dst     16-byte aligned; the pools must not overlap, and the lists
+ *                must not lie in dst.
+ * Errors: INVALID_ARG (other protocols, sizes outside these domains, NULL
+ * buffers or lists with n > 0, overlap, grid too large), STATE, HIP. */
+int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks, void* dst,
+                    size_t dst_blocks, size_t block_bytes, const int32_t* from,
+                    const int32_t* to, size_t n, void* stream);
+
 /* xfer_run_loop: iters messages of nbytes from src to dst back to back on
  * one connection in one launch (each message is a full transfer; dst holds
  * the last).  Measures per-message cost without launch overhead. */
@@ -322,6 +343,113 @@ int xfer_run_pingpong(xfer_conn* fwd, xfer_conn* rev, const void* a, void* b, vo
 int xfer_run_noalloc(int proto, int nchannels, int nslots, size_t slot_bytes,
                      const xfer_attr* attr, const void* src, void* dst, size_t nbytes,
                      uint32_t* status, void* stream);
+
+/* ----------------------------------------------------------------- cache
+ * A paged cache of a model's keys and values in 8 bits, whose blocks a
+ * connection moves as they are (xfer_run_blocks): the endpoint that ran a
+ * prompt stores into blocks, hands them over, and the endpoint that answers
+ * attends to them.
+ *
+ * A cache is a pool of `blocks` records of xfer_cache_block_bytes() bytes.  A
+ * record holds T = block_tokens tokens: for each of the H kv_heads the key
+ * codes [T][D] and the value codes [D][T] (D = head_dim; one byte each, e4m3),
+ * then float scales [H][2] (key, value), then zero to 127 bytes up to a
+ * multiple of 128.  A code stands for code * scale.  The scale of a block and
+ * head is a power of two 2^e, e >= -118, the smallest that brings the largest
+ * finite magnitude of its tokens to 448 or below.  Token t of a request sits
+ * in block table[t / T] at place t % T; its slot is block * T + t % T.
+ *
+ * These calls launch kernels on `stream` and return; they wait for nothing,
+ * allocate nothing, keep nothing between calls and may be captured into a
+ * graph.  They run on the current device, which must be that of the stream
+ * and the buffers.  They take no part in the launch order of transfers: their
+ * workgroups wait on nothing.  Strides are in elements. */
+typedef enum { XFER_BF16 = 0, XFER_FP16 = 1, XFER_FP32 = 2 } xfer_dtype;
+
+typedef struct {
+  int block_tokens; /* T: 16, 32 or 64 */
+  int kv_heads;     /* H: 1..1024 */
+  int head_dim;     /* D: 64, 96, 128, 192 or 256 */
+  int blocks;       /* in the pool; blocks * T <= 2^31 - 1 */
+} xfer_cache_shape;
+
+int xfer_cache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
+
+/* xfer_cache_plan: room for the next tokens of `batch` requests, from their
+ * lengths in device memory.  Request i has cached[i] tokens in the cache and
+ * adds added[i] (negative counts are taken as 0).  Its row of the table gets
+ * the blocks it needs beyond the ceil(cached[i] / T) it has: the next of
+ * free_blocks[0 .. nfree), requests in order, a request's blocks in order.
+ * The added tokens of all requests, in order, are the packed rows:
+ *   starts[batch + 1]   first row of each request, then their number
+ *   lengths[batch]      cached + added
+ *   slots[rows]         slot of each row's token; -1 where no block was left
+ *                       or the table is too narrow, and behind the last row
+ *   positions[rows]     the token's place in its request; -1 behind the last
+ *   counts[2]           new blocks the requests need (more than nfree: some
+ *                       got none), and tokens that they leave without a slot
+ * Entries of the table outside the new blocks stay as they are.  rows may
+ * exceed the packed rows (a padded batch) or fall short (the rest is cut).
+ * The sums of the lengths must stay below 2^31.  table_stride: elements from
+ * a request's row of table_width entries to the next. */
+int xfer_cache_plan(const int32_t* cached, const int32_t* added, int batch, int32_t* table,
+                    int64_t table_stride, int table_width, const int32_t* free_blocks, int nfree,
+                    int block_tokens, int32_t* slots, int32_t* positions, int rows,
+                    int32_t* starts, int32_t* lengths, int32_t* counts, void* stream);
+
+/* xfer_cache_store: rounds rows of keys and values into their slots.  key and
+ * value: [rows][H][D] with strides of a row and a head (the last dimension
+ * contiguous), of type dtype.  A slot outside the cache (a padded row's -1) is
+ * passed over.  A run of rows with consecutive slots in one block is stored
+ * together; a block whose run begins at place p > 0 already holds p tokens,
+ * keeps the larger of its scale and the run's, and has those tokens' codes
+ * rounded again where its scale grew.  Places behind the run stay as they are.
+ * A call may hold one run per block (as xfer_cache_plan lays them out); two
+ * runs into one block race for its scale.
+ *   Numbers are rounded to nearest even.  NaN and infinities are held as NaN
+ *   and do not count for the scale. */
+int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key, int64_t key_row,
+                     int64_t key_head, const void* value, int64_t value_row, int64_t value_head,
+                     int dtype, const int32_t* slots, int rows, void* stream);
+
+/* xfer_cache_attend: softmax(scale * q k^T) v of packed query rows over the
+ * cache.  Request b has the query rows starts[b] .. starts[b + 1) (of `rows`;
+ * the plan's starts) and lengths[b] tokens, which include those rows' own:
+ * row j of r sees the tokens 0 .. lengths[b] - r + j.  Head h of `heads` reads
+ * key/value head h / (heads / H).  A row that sees nothing gives 0 and a log
+ * sum of -infinity.  Tokens whose table entry lies outside the cache, and
+ * those past the table's width, are left out; what the cache holds behind a
+ * request's last token is not read into any result.  Rows of no request
+ * (behind the last, or before starts[0]) are left as they were.
+ * lse (or NULL): [rows][heads], the log of each row's sum of
+ * exp(scale * q k^T), with which results over parts of a context are joined.
+ * max_query, max_length: the largest number of query rows and of tokens of a
+ * request, where the host knows them; 0 where not.  They only shape the
+ * launch: results are right for any lengths.
+ * workspace: device memory of xfer_cache_attend_workspace() bytes for these
+ * arguments, 16-byte aligned, used by this call alone until it has run.
+ * Scores, sums and outputs are accumulated in float; the weights exp(...)
+ * are rounded to bfloat16 before they multiply the values. */
+typedef struct {
+  const void* query; /* [rows][heads][D], dtype BF16 or FP16 */
+  void* out;         /* [rows][heads][D], same dtype */
+  float* lse;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* starts;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t query_row, query_head, out_row, out_head, table_stride;
+  int batch, rows, heads, table_width;
+  int dtype; /* xfer_dtype */
+  float scale;
+  int max_query, max_length;
+} xfer_attend;
+
+int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const xfer_attend* args,
+                                size_t* bytes);
+int xfer_cache_attend(const xfer_cache_shape* shape, const void* cache, const xfer_attend* args,
+                      void* stream);
 
 /* --------------------------------------------------------------- inspect */
 /* Synchronous read of one channel's control words (lane 0 reported; the

@@ -1,0 +1,258 @@
+"""A paged cache of keys and values in 8 bits, whose blocks a connection moves.
+
+The endpoint that runs a prompt plans room for its tokens (plan_blocks), stores
+their keys and values (PagedCache.store) and sends the blocks
+(PagedCache.send); the endpoint that answers attends to them
+(PagedCache.attend).  Argument checks and marshalling only: the work is that of
+the library's HIP kernels (xfer_cache_* and xfer_run_blocks in include/xfer.h).
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from collections import namedtuple
+
+from . import xfer as X
+
+BlockPlan = namedtuple("BlockPlan", "slots positions starts lengths counts")
+BlockPlan.__doc__ = """Where the next tokens of a batch go (int32 tensors).
+
+slots[rows]: cache slot of each packed row, -1 where there is none; positions[rows]:
+the token's place in its request; starts[batch + 1]: first row of each request;
+lengths[batch]: tokens of each request with the new ones; counts[2]: new blocks
+needed, and tokens left without a slot."""
+
+BLOCK_TOKENS = (16, 32, 64)
+HEAD_DIMS = (64, 96, 128, 192, 256)
+
+
+def _tensor(t, what, dtypes, ndim, device):
+    """A GPU tensor of one of `dtypes` with `ndim` dimensions on `device` (None: any)."""
+    if not hasattr(t, "data_ptr"):
+        raise TypeError("%s: expected a torch tensor, got %s" % (what, type(t).__name__))
+    if not t.is_cuda:
+        raise ValueError("%s: tensor is not in GPU memory (device %s)" % (what, t.device))
+    if device is not None and t.device.index != device:
+        raise ValueError("%s: tensor is on cuda:%s, not on cuda:%d" % (what, t.device.index, device))
+    if t.dtype not in dtypes:
+        raise TypeError("%s: unsupported dtype %s" % (what, t.dtype))
+    if t.dim() != ndim:
+        raise ValueError("%s: expected %d dimensions, got shape %s" % (what, ndim, tuple(t.shape)))
+    return t
+
+
+def _list(t, what, n, device):
+    """A contiguous int32 tensor of n entries (None: any number)."""
+    import torch
+    _tensor(t, what, (torch.int32,), 1, device)
+    if n is not None and t.shape[0] != n:
+        raise ValueError("%s: expected %d entries, got %d" % (what, n, t.shape[0]))
+    if t.shape[0] > 1 and t.stride(0) != 1:
+        raise ValueError("%s: tensor is not contiguous" % what)
+    return t
+
+
+def _table(t, what, batch, device):
+    """A block table [batch, width]: any row stride of at least the width."""
+    import torch
+    _tensor(t, what, (torch.int32,), 2, device)
+    if t.shape[0] != batch:
+        raise ValueError("%s: expected %d rows, got %d" % (what, batch, t.shape[0]))
+    width = t.shape[1]
+    if (width > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) < width):
+        raise ValueError("%s: rows must be contiguous and not overlap" % what)
+    return t.stride(0) if batch > 1 else width, width
+
+
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    if device == torch.cuda.current_device():
+        X.check(fn(*args, X._stream_handle(stream)))
+    else:
+        with torch.cuda.device(device):
+            X.check(fn(*args, X._stream_handle(stream)))
+
+
+def _keep(stream, *tensors):
+    """Tensors made here and used on another stream than the current one stay
+    reserved until that stream has passed the call."""
+    if stream is None:
+        return
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if stream != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=None,
+                stream=None) -> BlockPlan:
+    """Room for the next tokens of a batch, worked out on the GPU.
+
+    Request i has cached[i] tokens and adds added[i]; its row of `table`
+    [batch, width] is extended in place by the blocks that it needs, taken from
+    `free` in order.  All int32 tensors.  rows: length of the packed rows'
+    outputs (the batch's added tokens, or more where it is padded).  out: a
+    BlockPlan to write into (a captured graph's), else new tensors."""
+    import torch
+    _list(cached, "plan_blocks: cached", None, None)
+    dev, batch = cached.device.index, cached.shape[0]
+    _list(added, "plan_blocks: added", batch, dev)
+    stride, width = _table(table, "plan_blocks: table", batch, dev)
+    _list(free, "plan_blocks: free", None, dev)
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError("plan_blocks: rows must not be negative")
+    sizes = (rows, rows, batch + 1, batch, 2)
+    if out is None:
+        out = BlockPlan(*(torch.empty(n, dtype=torch.int32, device=cached.device) for n in sizes))
+        _keep(stream, *out)
+    else:
+        for t, n, w in zip(out, sizes, BlockPlan._fields):
+            _list(t, "plan_blocks: out." + w, n, dev)
+    _call(dev, stream, X.lib().xfer_cache_plan, cached.data_ptr(), added.data_ptr(), batch,
+          table.data_ptr(), stride, width, free.data_ptr(), free.shape[0], int(block_tokens),
+          out.slots.data_ptr(), out.positions.data_ptr(), rows, out.starts.data_ptr(),
+          out.lengths.data_ptr(), out.counts.data_ptr())
+    return out
+
+
+class PagedCache:
+    """A pool of cache blocks in GPU memory: uint8 [blocks, block_bytes]."""
+
+    def __init__(self, blocks: int, block_tokens: int, kv_heads: int, head_dim: int, device=None,
+                 buffer=None):
+        """buffer: a contiguous uint8 tensor [blocks, block_bytes] to use, else zeros."""
+        import torch
+        self.blocks, self.block_tokens = int(blocks), int(block_tokens)
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        self._shape = X.xfer_cache_shape(self.block_tokens, self.kv_heads, self.head_dim,
+                                         self.blocks)
+        n = C.c_size_t()
+        X.check(X.lib().xfer_cache_block_bytes(C.byref(self._shape), C.byref(n)))
+        self.block_bytes = n.value
+        if buffer is None:
+            buffer = torch.zeros(self.blocks, self.block_bytes, dtype=torch.uint8,
+                                 device="cuda" if device is None else device)
+        _tensor(buffer, "PagedCache: buffer", (torch.uint8,), 2, None)
+        if tuple(buffer.shape) != (self.blocks, self.block_bytes):
+            raise ValueError("PagedCache: buffer must have shape (%d, %d), got %s"
+                             % (self.blocks, self.block_bytes, tuple(buffer.shape)))
+        if not buffer.is_contiguous() or buffer.data_ptr() % 16:
+            raise ValueError("PagedCache: buffer must be contiguous and 16-byte aligned")
+        self.buffer = buffer
+        self.device = buffer.device.index
+
+    def _view(self, dtype, shape, strides, at):
+        b = self.buffer.view(dtype)
+        return b.as_strided(shape, strides, b.storage_offset() + at)
+
+    def keys(self):
+        """Key codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view)."""
+        import torch
+        h, t, d = self.kv_heads, self.block_tokens, self.head_dim
+        return self._view(torch.float8_e4m3fn, (self.blocks, h, t, d),
+                          (self.block_bytes, 2 * t * d, d, 1), 0)
+
+    def values(self):
+        """Value codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view)."""
+        import torch
+        h, t, d = self.kv_heads, self.block_tokens, self.head_dim
+        return self._view(torch.float8_e4m3fn, (self.blocks, h, t, d),
+                          (self.block_bytes, 2 * t * d, 1, t), t * d)
+
+    def scales(self):
+        """Scales of keys and values, float32 [blocks, kv_heads, 2] (a view)."""
+        import torch
+        h, t, d = self.kv_heads, self.block_tokens, self.head_dim
+        return self._view(torch.float32, (self.blocks, h, 2), (self.block_bytes // 4, 2, 1),
+                          2 * h * t * d // 4)
+
+    def store(self, key, value, slots, stream=None) -> None:
+        """Stores rows of keys and values [rows, kv_heads, head_dim] (bfloat16,
+        float16 or float32; any strides of rows and heads) into their slots."""
+        import torch
+        kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        _tensor(key, "store: key", kinds, 3, self.device)
+        _tensor(value, "store: value", (key.dtype,), 3, self.device)
+        rows = key.shape[0]
+        for t, w in ((key, "key"), (value, "value")):
+            if tuple(t.shape) != (rows, self.kv_heads, self.head_dim):
+                raise ValueError("store: %s must have shape (%d, %d, %d), got %s"
+                                 % (w, rows, self.kv_heads, self.head_dim, tuple(t.shape)))
+            if t.stride(2) != 1:
+                raise ValueError("store: %s: the last dimension must be contiguous" % w)
+        _list(slots, "store: slots", rows, self.device)
+        _call(self.device, stream, X.lib().xfer_cache_store, C.byref(self._shape),
+              self.buffer.data_ptr(), key.data_ptr(), key.stride(0), key.stride(1),
+              value.data_ptr(), value.stride(0), value.stride(1), kinds[key.dtype],
+              slots.data_ptr(), rows)
+
+    def attend(self, query, table, lengths, starts, scale=None, out=None, lse=False, max_query=0,
+               max_length=0, stream=None):
+        """Attention of packed query rows [rows, heads, head_dim] (bfloat16 or
+        float16) over the cache; returns out, or (out, lse) with lse=True.
+
+        Request b has the rows starts[b] .. starts[b + 1) and lengths[b] tokens,
+        its rows' own included; row j of r sees tokens 0 .. lengths[b] - r + j.
+        table: int32 [batch, width].  scale: 1 / sqrt(head_dim) if None.
+        max_query, max_length: the batch's largest number of rows and of
+        tokens, where known; they shape the launch only.  Rows of no request
+        are left as they were (without `out`: undefined)."""
+        import torch
+        kinds = {torch.bfloat16: 0, torch.float16: 1}
+        _tensor(query, "attend: query", kinds, 3, self.device)
+        rows, heads, d = query.shape
+        if d != self.head_dim:
+            raise ValueError("attend: query has head_dim %d, the cache %d" % (d, self.head_dim))
+        if query.stride(2) != 1:
+            raise ValueError("attend: query: the last dimension must be contiguous")
+        _list(lengths, "attend: lengths", None, self.device)
+        batch = lengths.shape[0]
+        _list(starts, "attend: starts", batch + 1, self.device)
+        stride, width = _table(table, "attend: table", batch, self.device)
+        if out is None:
+            out = torch.empty(rows, heads, d, dtype=query.dtype, device=query.device)
+            _keep(stream, out)
+        else:
+            _tensor(out, "attend: out", (query.dtype,), 3, self.device)
+            if out.shape != query.shape or out.stride(2) != 1:
+                raise ValueError("attend: out must have the query's shape and a contiguous last "
+                                 "dimension")
+        sums = None
+        if lse is True:
+            sums = torch.empty(rows, heads, dtype=torch.float32, device=query.device)
+            _keep(stream, sums)
+        elif lse is not False and lse is not None:
+            sums = _tensor(lse, "attend: lse", (torch.float32,), 2, self.device)
+            if tuple(sums.shape) != (rows, heads) or not sums.is_contiguous():
+                raise ValueError("attend: lse must be contiguous of shape (%d, %d)" % (rows, heads))
+        a = X.xfer_attend(query.data_ptr(), out.data_ptr(),
+                          None if sums is None else sums.data_ptr(), table.data_ptr(),
+                          lengths.data_ptr(), starts.data_ptr(), None, 0, query.stride(0),
+                          query.stride(1), out.stride(0), out.stride(1), stride, batch, rows,
+                          heads, width, kinds[query.dtype],
+                          1.0 / math.sqrt(d) if scale is None else float(scale), int(max_query),
+                          int(max_length))
+        n = C.c_size_t()
+        L = X.lib()
+        X.check(L.xfer_cache_attend_workspace(C.byref(self._shape), C.byref(a), C.byref(n)))
+        if n.value:
+            work = torch.empty(n.value, dtype=torch.uint8, device=query.device)
+            _keep(stream, work)
+            a.workspace, a.workspace_bytes = work.data_ptr(), n.value
+        _call(self.device, stream, L.xfer_cache_attend, C.byref(self._shape),
+              self.buffer.data_ptr(), C.byref(a))
+        return out if sums is None else (out, sums)
+
+    def send(self, conn, dst, src_ids, dst_ids, stream=None) -> None:
+        """Moves block src_ids[i] of this cache to block dst_ids[i] of the cache
+        `dst` over a connection (Conn.run_blocks): int32 lists in GPU memory."""
+        mine = (self.block_tokens, self.kv_heads, self.head_dim)
+        other = (dst.block_tokens, dst.kv_heads, dst.head_dim)
+        if mine != other:
+            raise ValueError("send: blocks of shape %s cannot go into blocks of shape %s"
+                             % (mine, other))
+        conn.run_blocks(self.buffer, dst.buffer, self.block_bytes, src_ids, dst_ids, stream=stream)

@@ -52,6 +52,7 @@ struct xfer_conn {
   std::vector<uint64_t> add;     // per channel, steps a run adds (scratch of the run calls)
   int cap_one[2][2] = {{-1, -1}, {-1, -1}};  // resident capacity of a single-transfer
                                               // launch, by [aligned][debug]; -1 unknown
+  int cap_blocks[2] = {-1, -1};               // the same of a block transfer, by [debug]
 };
 
 static_assert(sizeof(xfer_trace_rec) == sizeof(xfer::TraceRec) &&
@@ -1019,6 +1020,66 @@ extern "C" int xfer_run_messages(xfer_conn* c, const void* src, void* dst, const
     for (const MsgDesc& m : msgs) lens.push_back(m.len);
     relay_job(c, std::move(lens), 1);
   }
+  commit_steps(c, add);
+  return XFER_OK;
+}
+
+extern "C" int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks, void* dst,
+                               size_t dst_blocks, size_t block_bytes, const int32_t* from,
+                               const int32_t* to, size_t n, void* stream) {
+  int rc = check_runnable(c, "xfer_run_blocks");
+  if (rc) return rc;
+  if (c->proto != XFER_PROTO_SIMPLE && c->proto != XFER_PROTO_ZEROCOPY_DIRECT)
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_run_blocks: the connection must be SIMPLE or ZEROCOPY_DIRECT");
+  if (block_bytes == 0 || block_bytes % 16 || block_bytes > (size_t(1) << 30))
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_run_blocks: block_bytes must be a multiple of 16, 16 bytes to 1 GiB");
+  if (src_blocks > 0x7FFFFFFFu || dst_blocks > 0x7FFFFFFFu || n > 0x7FFFFFFFu)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: at most 2^31 - 1 blocks and entries");
+  if (n == 0) return XFER_OK;
+  if (!src || !dst || !from || !to)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: NULL buffer or list with entries to move");
+  if (!aligned16(src) || !aligned16(dst) || (reinterpret_cast<uintptr_t>(from) & 3u) ||
+      (reinterpret_cast<uintptr_t>(to) & 3u))
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_run_blocks: pools must be 16-byte aligned, lists 4-byte aligned");
+  const size_t ns = src_blocks * block_bytes, nd = dst_blocks * block_bytes;
+  if (overlap(src, ns, dst, nd))
+    return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: the pools overlap");
+  if (overlap(dst, nd, from, n * 4) || overlap(dst, nd, to, n * 4))
+    return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: a list lies in the destination pool");
+  const uint64_t nbytes = uint64_t(n) * block_bytes;
+  std::vector<uint64_t>& add = c->add;
+  rc = plan_steps(c, nbytes, 1, add, "xfer_run_blocks");
+  if (rc) return rc;
+  DeviceGuard g(c->device);
+  const uint32_t total = grid_of(c, wgs_of(c));
+  const Variant v = variant_of(c, true);
+  rc = check_resident(c->device, v, 4, c->block, total, "xfer_run_blocks", &c->cap_blocks[v.debug]);
+  if (rc) return rc;
+  BlocksArgs args;
+  memset(&args, 0, sizeof(args));
+  args.conn = conn_args(c, src, dst, nbytes, 0);
+  args.from = from;
+  args.to = to;
+  args.block_bytes = block_bytes;
+  args.units = uint32_t(block_bytes / 16);
+  uint32_t log2d = 0;
+  while ((uint64_t(1) << log2d) < args.units) ++log2d;
+  args.shift = 28 + log2d;
+  args.magic = ((uint64_t(1) << args.shift) + args.units - 1) / args.units;
+  args.nfrom = uint32_t(src_blocks);
+  args.nto = uint32_t(dst_blocks);
+  args.timeout_ticks = c->timeout_ticks;
+  args.total_wgs = total;
+  args.xcd_remap = c->xcd_remap;
+  args.rx_wgs = rx_region_of(c);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e =
+      gate().run(c->device, s, [&] { return launch_blocks(v, args, c->block, s, c->coop); });
+  if (e != hipSuccess) return hip_fail(e, "xfer_run_blocks launch");
+  relay_job(c, {nbytes}, 1);
   commit_steps(c, add);
   return XFER_OK;
 }

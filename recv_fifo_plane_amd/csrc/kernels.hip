@@ -1175,10 +1175,9 @@ __device__ void zc_recv(const ConnArgs& A, uint32_t c, Side& sd, const RunArgs<M
 
 // Receiver of one lane of zero-copy direct, run by one thread: answer tail
 // with head until the launch's last step on the channel has landed.
-template <int SC, int ORD, int MAXB, int NMSG>
-__device__ void zcd_recv(const ConnArgs& A, uint32_t c, Side& sd, const RunArgs<MAXB, NMSG>& args,
-                         uint64_t ticks) {
-  const uint64_t end = sd.base + launch_steps(A, c, args);
+template <int SC, int ORD>
+__device__ void zcd_recv(const ConnArgs& A, Side& sd, uint64_t steps, uint64_t ticks) {
+  const uint64_t end = sd.base + steps;
   uint64_t done = sd.base;
   Deadline dl(ticks, A.status);
   while (done < end) {
@@ -1307,7 +1306,7 @@ __device__ void zero_copy_wg(const RunArgs<MAXB, NMSG>& args, Shared& sh) {
     if constexpr (PROTO == kProtoZC)
       zc_recv<SC, ORD, MAXB, NMSG>(A, c, sd, args, ticks);
     else
-      zcd_recv<SC, ORD, MAXB, NMSG>(A, c, sd, args, ticks);
+      zcd_recv<SC, ORD>(A, sd, launch_steps(A, c, args), ticks);
     return;
   }
   uint32_t pw = b - args.rx_wgs;
@@ -1389,6 +1388,347 @@ __global__ void __launch_bounds__(1024) run_kernel(RunArgs<MAXB, NMSG> args) {
     if constexpr (PROTO != kProtoSimple) {
       if (role == 0 && g0 != sd.base) ll_close<SC>(sd, g0);
     }
+  }
+}
+
+// ------------------------------------------------------------------- blocks
+// A transfer of blocks named by two lists in device memory: entry i moves
+// block from[i] of the source pool to block to[i] of the destination pool.
+// It is the transfer of the n * block_bytes bytes that the entries make up in
+// order, with the same partition, steps, counters and FIFO bytes; only the
+// addresses of the bytes at the two ends go through the lists.  Everything is
+// counted in units of 16 bytes, one vector: blocks, channel ranges and steps
+// are whole numbers of them.
+//
+// A wave's vectors of one unrolled access are 64 consecutive units, which lie
+// in one block, in two where a block ends among them, or in more where blocks
+// are shorter than 64 units.  The list entries of the first and last unit of
+// all kUnroll accesses are fetched by one load per wave, a lane each, ahead
+// of the payload; the block's base is then wave-uniform and sits in a buffer
+// descriptor of exactly the block's bytes, so the buffer unit bounds every
+// access.  An entry outside its pool gets an empty descriptor: its loads give
+// zeros and its stores nothing.  An entry counts only if both of its ids are
+// inside (list entries are checked against both pools at both ends), so a
+// block is never overwritten by the zeros of a missing one.
+struct BlockList {
+  const int32_t* from;
+  const int32_t* to;
+  uint64_t block_bytes;
+  uint64_t magic;     // ceil(2^shift / units of a block): exact division of a unit index < 2^27
+  uint32_t units;     // of a block
+  uint32_t shift;
+  uint32_t nfrom, nto;  // blocks in the pools
+};
+
+// The place of a step's chunk in the lists: its first entry, and the units
+// of that entry's block before the chunk.
+struct ListPos {
+  uint64_t entry;
+  uint32_t rem;
+};
+
+__device__ __forceinline__ ListPos list_pos(const BlockList& B, uint64_t off) {
+  const uint64_t e = off / B.block_bytes;
+  return ListPos{e, static_cast<uint32_t>((off - e * B.block_bytes) >> 4)};
+}
+
+// x / B.units for x < 2^27 + 2^26 (a chunk of at most 1 GiB from within a
+// block of at most 1 GiB), by the round-up method: magic = ceil(2^shift / d)
+// with shift = 28 + ceil(log2 d), so magic < 2^29 and the product < 2^57.
+__device__ __forceinline__ uint32_t entry_of(const BlockList& B, uint32_t x) {
+  return static_cast<uint32_t>((x * B.magic) >> B.shift);
+}
+
+// This wave's accesses of one batch: lane u (u < kUnroll) holds the entry of
+// access u's first unit, lane kUnroll + u that of its last, with its two ids
+// (-1 for both where either is outside its pool).
+struct BatchIds {
+  uint32_t entry;
+  int32_t from, to;
+};
+
+template <bool CYC>
+__device__ __forceinline__ uint32_t wave_unit(uint32_t w, uint32_t P, uint32_t u) {
+  const uint32_t t0 = threadIdx.x & ~63u;
+  if constexpr (CYC)
+    return (w + u * P) * blockDim.x + t0;
+  else
+    return u * blockDim.x + t0;
+}
+
+__device__ __forceinline__ void entry_ids(const BlockList& B, const ListPos& at, uint32_t e,
+                                          int32_t& from, int32_t& to) {
+  const int32_t f = B.from[at.entry + e], t = B.to[at.entry + e];
+  const bool ok = static_cast<uint32_t>(f) < B.nfrom && static_cast<uint32_t>(t) < B.nto;
+  from = ok ? f : -1;
+  to = ok ? t : -1;
+}
+
+// base, lim: the lane's units of the chunk.
+template <bool CYC>
+__device__ __forceinline__ BatchIds batch_ids(const BlockList& B, const ListPos& at, uint32_t base,
+                                              uint32_t lim, uint32_t u0, uint32_t w, uint32_t P) {
+  const uint32_t l = threadIdx.x & 63u, u = l % kUnroll;
+  BatchIds r{0u, -1, -1};
+  uint32_t x = wave_unit<CYC>(w, P, u0 + u);
+  if (l < 2u * kUnroll && x < lim) {
+    if (l >= kUnroll) x = min(x + 63u, lim - 1u);
+    r.entry = entry_of(B, at.rem + base + x);
+    entry_ids(B, at, r.entry, r.from, r.to);
+  }
+  return r;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rsrc(const BlockList& B,
+                                                             const uint8_t* pool, int32_t id) {
+  return make_rsrc(pool + (id < 0 ? 0 : static_cast<uint64_t>(id) * B.block_bytes),
+                   id < 0 ? 0u : static_cast<uint32_t>(B.block_bytes));
+}
+
+// Calls f(descriptor, byte offset in the block) for this lane's unit x of
+// access u, in the lanes of each block it meets in turn; every wave calls f
+// at least once per access (with an empty descriptor past the end).
+template <bool SRC, typename F>
+__device__ __forceinline__ void each_block(const BlockList& B, const ListPos& at,
+                                           const BatchIds& ids, uint32_t u, const uint8_t* pool,
+                                           uint32_t base, uint32_t x, uint32_t lim, F&& f) {
+  const uint32_t first = __builtin_amdgcn_readlane(ids.entry, u);
+  const uint32_t last = __builtin_amdgcn_readlane(ids.entry, kUnroll + u);
+  const int32_t id = __builtin_amdgcn_readlane(SRC ? ids.from : ids.to, u);
+  const uint32_t y = at.rem + base + x;
+  if (first == last) {  // a whole access inside one block (or past the end)
+    const uint32_t off = (x < lim ? y - first * B.units : B.units) << 4;
+    f(block_rsrc(B, pool, id), off);
+    return;
+  }
+  const uint32_t mine = x < lim ? entry_of(B, y) : 0xFFFFFFFFu;
+  for (uint32_t e = first; e <= last; ++e) {
+    int32_t ef, et;
+    if (e == first) {
+      ef = et = id;
+    } else if (e == last) {
+      ef = et = __builtin_amdgcn_readlane(SRC ? ids.from : ids.to, kUnroll + u);
+    } else {
+      entry_ids(B, at, e, ef, et);
+      ef = __builtin_amdgcn_readfirstlane(ef);
+      et = __builtin_amdgcn_readfirstlane(et);
+    }
+    if (mine == e) f(block_rsrc(B, pool, SRC ? ef : et), (y - e * B.units) << 4);
+  }
+}
+
+// The lane's units of a chunk of L bytes: first unit and count.
+template <bool CYC>
+__device__ __forceinline__ LaneSpan unit_span(uint32_t L, uint64_t S, uint32_t P, uint32_t w) {
+  const LaneSpan sp = lane_span<CYC>(L, S, P, w);
+  return LaneSpan{sp.base >> 4, sp.lim >> 4};
+}
+
+template <int LP, bool CYC>
+__device__ __forceinline__ void blocks_load(Batch& b, const BlockList& B, const ListPos& at,
+                                            const BatchIds& ids, const uint8_t* pool, LaneSpan sp,
+                                            uint32_t u0, uint32_t w, uint32_t P) {
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t x = wave_unit<CYC>(w, P, u0 + u) + (threadIdx.x & 63u);
+    each_block<true>(B, at, ids, u, pool, sp.base, x, sp.lim,
+                     [&](__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+                       b.r[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, LP);
+                     });
+  }
+}
+
+template <int SP, bool CYC>
+__device__ __forceinline__ void blocks_store(const Batch& b, const BlockList& B, const ListPos& at,
+                                             const BatchIds& ids, const uint8_t* pool, LaneSpan sp,
+                                             uint32_t u0, uint32_t w, uint32_t P) {
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t x = wave_unit<CYC>(w, P, u0 + u) + (threadIdx.x & 63u);
+    each_block<false>(B, at, ids, u, pool, sp.base, x, sp.lim,
+                      [&](__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+                        __builtin_amdgcn_raw_buffer_store_b128(b.r[u], rs, off, 0, SP);
+                      });
+  }
+}
+
+// Batches of a lane's share of a chunk.
+template <bool CYC>
+__device__ __forceinline__ bool batch_there(LaneSpan sp, uint32_t u0, uint32_t w, uint32_t P) {
+  return (CYC ? (w + u0 * P) * blockDim.x : u0 * blockDim.x) < sp.lim;
+}
+
+template <int SC, int ORD>
+__device__ bool blocks_send(const ConnArgs& A, const BlockList& B, uint32_t c, uint32_t w, Side& sd,
+                            uint64_t ticks, Shared& sh) {
+  using O = Order<SC, ORD>;
+  const uint64_t S = A.step_bytes;
+  for (uint64_t j = 0; j < sd.r.k; ++j) {
+    const uint64_t g = sd.base + j;
+    const uint32_t err = wait_credit<SC, ORD, true>(A, sd, g, ticks, sh);
+    if (!err && threadIdx.x == 0) trace_step(A, sd, g, 0, sd.seen);
+    if (!err) {
+      jitter(sd, g, 0);
+      const uint32_t L = chunk_len(sd, S, j);
+      const ListPos at = list_pos(B, sd.r.beg + j * S);
+      const LaneSpan sp = unit_span<false>(L, S, A.lanes, w);
+      const __amdgpu_buffer_rsrc_t rd = make_rsrc(slot_of(A, c, g) + sp.base * 16ull, sp.lim * 16u);
+      for (uint32_t u0 = 0; batch_there<false>(sp, u0, w, A.lanes); u0 += kUnroll) {
+        const BatchIds ids = batch_ids<false>(B, at, sp.base, sp.lim, u0, w, A.lanes);
+        Batch b;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) b.r[u] = u32x4{0u, 0u, 0u, 0u};
+        blocks_load<kPolNT, false>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          __builtin_amdgcn_raw_buffer_store_b128(b.r[u], rd, lane_vec<false>(w, A.lanes, u0 + u), 0,
+                                                 O::kShared);
+      }
+      O::release();
+    }
+    jitter(sd, g, 1);
+    if (wg_failed(sh, err, A)) return false;
+    if (threadIdx.x == 0) {
+      trace_step(A, sd, g, 1, g + 1);
+      st_u64<SC>(&sd.rx->tail, g + 1);
+    }
+  }
+  return true;
+}
+
+template <int SC, int ORD>
+__device__ bool blocks_recv(const ConnArgs& A, const BlockList& B, uint32_t c, uint32_t w, Side& sd,
+                            uint64_t ticks, Shared& sh) {
+  using O = Order<SC, ORD>;
+  const uint64_t S = A.step_bytes;
+  const uint64_t* ready = A.relay ? &A.ctrl_rx[static_cast<uint64_t>(c) * A.lanes].gtail : &sd.rx->tail;
+  for (uint64_t j = 0; j < sd.r.k; ++j) {
+    const uint64_t g = sd.base + j;
+    uint32_t err = 0;
+    if (sd.seen <= g) {
+      uint64_t t = 0;
+      err = wait_count<SC, true>(ready, 0, g, ticks, A.status, sh, t);
+      if (!err) {
+        O::acquire();
+        sd.seen = t;
+      }
+    }
+    if (!err && threadIdx.x == 0) trace_step(A, sd, g, 0, sd.seen);
+    if (!err) {
+      jitter(sd, g, 0);
+      const uint32_t L = chunk_len(sd, S, j);
+      const ListPos at = list_pos(B, sd.r.beg + j * S);
+      const LaneSpan sp = unit_span<false>(L, S, A.lanes, w);
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(slot_rx(A, c, g) + sp.base * 16ull, sp.lim * 16u);
+      for (uint32_t u0 = 0; batch_there<false>(sp, u0, w, A.lanes); u0 += kUnroll) {
+        const BatchIds ids = batch_ids<false>(B, at, sp.base, sp.lim, u0, w, A.lanes);
+        Batch b;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          b.r[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane_vec<false>(w, A.lanes, u0 + u), 0,
+                                                         O::kShared);
+        blocks_store<kPolNT, false>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
+      }
+      // The slot goes back once this wave's reads of it are complete: not
+      // every read feeds a store here (an entry outside its pool), so the
+      // wave waits for them.
+      O::release();
+    }
+    jitter(sd, g, 1);
+    if (wg_failed(sh, err, A)) return false;
+    if (threadIdx.x == 0) {
+      trace_step(A, sd, g, 1, g + 1);
+      st_u64<SC>(&sd.tx->head, g + 1);
+    }
+  }
+  return true;
+}
+
+// Zero-copy direct: every unit goes from its source block to its destination
+// block in one pass.
+template <int SC, int ORD>
+__device__ bool blocks_zcd_send(const ConnArgs& A, const BlockList& B, uint32_t w, Side& sd,
+                                Shared& sh) {
+  using O = Order<SC, ORD>;
+  const uint64_t S = A.step_bytes;
+  for (uint64_t j = 0; j < sd.r.k; ++j) {
+    const uint64_t g = sd.base + j;
+    if (threadIdx.x == 0) trace_step(A, sd, g, 0, sd.r.beg + j * S);
+    jitter(sd, g, 0);
+    const uint32_t L = chunk_len(sd, S, j);
+    const ListPos at = list_pos(B, sd.r.beg + j * S);
+    const LaneSpan sp = unit_span<true>(L, S, A.lanes, w);
+    for (uint32_t u0 = 0; batch_there<true>(sp, u0, w, A.lanes); u0 += kUnroll) {
+      const BatchIds ids = batch_ids<true>(B, at, sp.base, sp.lim, u0, w, A.lanes);
+      Batch b;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) b.r[u] = u32x4{0u, 0u, 0u, 0u};
+      blocks_load<kPolNT, true>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
+      blocks_store<O::kShared, true>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
+    }
+    O::release();
+    jitter(sd, g, 1);
+    if (wg_failed(sh, 0, A)) return false;
+    if (threadIdx.x == 0) {
+      trace_step(A, sd, g, 1, g + 1);
+      st_u64<SC>(&sd.rx->tail, g + 1);
+    }
+  }
+  return true;
+}
+
+// One transfer of blocks on one connection (SIMPLE or zero-copy direct), in
+// the workgroup layout of run_kernel.
+template <int PROTO, int SC, int ORD, bool DBG>
+__global__ void __launch_bounds__(1024) blocks_kernel(BlocksArgs args) {
+  __shared__ Shared sh;
+  if (threadIdx.x == 0) sh.err = 0;
+  __syncthreads();
+  const ConnArgs& A = args.conn;
+  const BlockList B{args.from,  args.to,    args.block_bytes, args.magic,
+                    args.units, args.shift, args.nfrom,       args.nto};
+  const uint64_t ticks = args.timeout_ticks;
+  if constexpr (PROTO == kProtoZCD) {
+    if (blockIdx.x < args.rx_wgs) {
+      const uint32_t nl = A.nch * A.lanes;
+      if (blockIdx.x >= zc_receiver_wgs(A.nch, A.lanes, blockDim.x)) return;
+      if (!claim_wg<DBG>(A, nl + blockIdx.x, sh)) return;
+      const uint32_t li = threadIdx.x % 64u;
+      const uint32_t t = (blockIdx.x * (blockDim.x / 64u) + threadIdx.x / 64u) * kRxLanesPerWave + li;
+      if (li >= kRxLanesPerWave || t >= nl || !((A.roles >> 1) & 1u)) return;
+      const uint32_t c = t / A.lanes;
+      Side sd = make_side<DBG, false>(A, c, t % A.lanes, false, SC);
+      if (sd.dead) return;
+      zcd_recv<SC, ORD>(A, sd, chan_range(A.nbytes, A.nch, c, A.step_bytes).k, ticks);
+      return;
+    }
+    uint32_t pw = blockIdx.x - args.rx_wgs;
+    if (args.xcd_remap) {
+      const uint32_t eighth = (args.total_wgs - args.rx_wgs) / 8u;
+      pw = (pw % 8u) * eighth + pw / 8u;
+    }
+    const uint32_t c = pw / A.lanes, w = pw % A.lanes;
+    if (c >= A.nch) return;
+    if (!claim_wg<DBG>(A, pw, sh)) return;
+    if (!(A.roles & 1u)) return;
+    Side sd = make_side<DBG>(A, c, w, true, SC);
+    if (sd.dead) return;
+    sd.r = chan_range(A.nbytes, A.nch, c, A.step_bytes);
+    blocks_zcd_send<SC, ORD>(A, B, w, sd, sh);
+  } else {
+    const uint32_t lw = logical_wg(args.xcd_remap, args.total_wgs);
+    const uint32_t pair = lw >> 1, role = lw & 1u;
+    const uint32_t c = pair / A.lanes, w = pair % A.lanes;
+    if (c >= A.nch) return;
+    if (!claim_wg<DBG>(A, lw, sh)) return;
+    if (!((A.roles >> role) & 1u)) return;
+    Side sd = make_side<DBG>(A, c, w, role == 0, SC);
+    if (sd.dead) return;
+    sd.r = chan_range(A.nbytes, A.nch, c, A.step_bytes);
+    if (role == 0)
+      blocks_send<SC, ORD>(A, B, c, w, sd, ticks, sh);
+    else
+      blocks_recv<SC, ORD>(A, B, c, w, sd, ticks, sh);
   }
 }
 
@@ -1534,6 +1874,29 @@ PingFn pick_ping(const Variant& v) {
                                       : pick_ping_sc<kProtoSimple>(v);
 }
 
+using BlocksFn = void (*)(BlocksArgs);
+
+template <int P, int SC, bool DBG>
+BlocksFn pick_blocks_ord(int ord) {
+  return ord == kOrdFenced ? blocks_kernel<P, SC, kOrdFenced, DBG>
+                           : blocks_kernel<P, SC, kOrdCoherent, DBG>;
+}
+
+template <int P, bool DBG>
+BlocksFn pick_blocks_sc(const Variant& v) {
+  return v.scope == kScopeSystem ? pick_blocks_ord<P, kScopeSystem, DBG>(v.ordering)
+                                 : pick_blocks_ord<P, kScopeAgent, DBG>(v.ordering);
+}
+
+template <int P>
+BlocksFn pick_blocks_dbg(const Variant& v) {
+  return v.debug ? pick_blocks_sc<P, true>(v) : pick_blocks_sc<P, false>(v);
+}
+
+BlocksFn pick_blocks(const Variant& v) {
+  return v.proto == kProtoZCD ? pick_blocks_dbg<kProtoZCD>(v) : pick_blocks_dbg<kProtoSimple>(v);
+}
+
 }  // namespace
 
 // hipLaunchKernel and hipLaunchCooperativeKernel report this launch's own
@@ -1561,6 +1924,11 @@ hipError_t launch_runB(const Variant& v, const RunBatch& a, int block, hipStream
 
 hipError_t launch_ping(const Variant& v, const PingArgs& a, int block, hipStream_t s, bool coop) {
   return launch(pick_ping(v), a, a.total_wgs, block, s, coop);
+}
+
+hipError_t launch_blocks(const Variant& v, const BlocksArgs& a, int block, hipStream_t s,
+                         bool coop) {
+  return launch(pick_blocks(v), a, a.total_wgs, block, s, coop);
 }
 
 // Whether the current device deals blocks to 8 XCDs in strict rotation on
@@ -1600,10 +1968,11 @@ hipError_t max_resident(const Variant& v, int kind, int block, int* wgs) {
   if (e != hipSuccess) return e;
   e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
   if (e != hipSuccess) return e;
-  // kind: 0 one transfer, 1 a batch, 2 the ping-pong, 3 a message list
+  // kind: 0 one transfer, 1 a batch, 2 the ping-pong, 3 a message list, 4 blocks
   const void* fn = kind == 0   ? reinterpret_cast<const void*>(pick_run<1, 1>(v))
                    : kind == 1 ? reinterpret_cast<const void*>(pick_run<16, 1>(v))
                    : kind == 3 ? reinterpret_cast<const void*>(pick_run<1, kMaxMsgs>(v))
+                   : kind == 4 ? reinterpret_cast<const void*>(pick_blocks(v))
                                : reinterpret_cast<const void*>(pick_ping(v));
   e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, block, 0);
   if (e != hipSuccess) return e;

@@ -136,6 +136,24 @@ struct PingArgs {
   uint32_t pad;
 };
 
+// A transfer of blocks named by device lists (xfer_run_blocks).  conn.nbytes
+// counts the bytes of all entries; units, magic and shift divide an index in
+// units of 16 bytes by a block's units (kernels.hip, entry_of).
+struct BlocksArgs {
+  ConnArgs conn;
+  const int32_t* from;
+  const int32_t* to;
+  uint64_t block_bytes;
+  uint64_t magic;
+  uint32_t units, shift;
+  uint32_t nfrom, nto;
+  uint64_t timeout_ticks;
+  uint32_t total_wgs;
+  uint32_t xcd_remap;
+  uint32_t rx_wgs;  // zero-copy direct: receiver workgroups
+  uint32_t pad;
+};
+
 // Workgroups of one connection's launch.  SIMPLE and LL: a producer and a
 // consumer workgroup per lane.  Both zero-copy protocols: a producer
 // workgroup per lane, and receiver workgroups in which the first
@@ -193,9 +211,11 @@ hipError_t launch_runB(const Variant& v, const RunBatch& a, int block, hipStream
                        bool coop = false);
 hipError_t launch_ping(const Variant& v, const PingArgs& a, int block, hipStream_t s,
                        bool coop = false);
+hipError_t launch_blocks(const Variant& v, const BlocksArgs& a, int block, hipStream_t s,
+                         bool coop = false);
 // Workgroups of `block` threads the device can hold resident at once for
 // the variant's kernel of launch kind 0 (one transfer), 1 (a batch of
-// connections), 2 (the ping-pong) or 3 (a message list).
+// connections), 2 (the ping-pong), 3 (a message list) or 4 (blocks).
 hipError_t max_resident(const Variant& v, int kind, int block, int* wgs);
 // Whether the current device deals a launch's blocks to 8 XCDs in strict
 // rotation on every stream (the kernels may then place blocks by XCD id).

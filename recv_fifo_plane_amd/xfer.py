@@ -83,6 +83,21 @@ class xfer_chan_state(C.Structure):
     ]
 
 
+class xfer_cache_shape(C.Structure):
+    _fields_ = [("block_tokens", C.c_int), ("kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("blocks", C.c_int)]
+
+
+class xfer_attend(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("query", "out", "lse", "table", "lengths", "starts",
+                                           "workspace")]
+                + [("workspace_bytes", C.c_size_t)]
+                + [(n, C.c_int64) for n in ("query_row", "query_head", "out_row", "out_head",
+                                            "table_stride")]
+                + [(n, C.c_int) for n in ("batch", "rows", "heads", "table_width", "dtype")]
+                + [("scale", C.c_float), ("max_query", C.c_int), ("max_length", C.c_int)])
+
+
 class xfer_setup_op(C.Structure):
     _fields_ = [("kind", C.c_int), ("peer", C.c_int), ("channel", C.c_int)]
 
@@ -102,9 +117,19 @@ SIGNATURES = {
     "xfer_run_loop": (C.c_int, [_vp, _vp, _vp, C.c_size_t, C.c_int, _vp]),
     "xfer_run_messages": (C.c_int, [_vp, _vp, _vp, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t),
                                     C.c_int, _vp]),
+    "xfer_run_blocks": (C.c_int, [_vp, _vp, C.c_size_t, _vp, C.c_size_t, C.c_size_t, _vp, _vp,
+                                  C.c_size_t, _vp]),
     "xfer_run_pingpong": (C.c_int, [_vp, _vp, _vp, _vp, _vp, C.c_size_t, C.c_int, _vp]),
     "xfer_run_noalloc": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_size_t, C.POINTER(xfer_attr),
                                    _vp, _vp, C.c_size_t, _vp, _vp]),
+    "xfer_cache_block_bytes": (C.c_int, [C.POINTER(xfer_cache_shape), C.POINTER(C.c_size_t)]),
+    "xfer_cache_plan": (C.c_int, [_vp, _vp, C.c_int, _vp, C.c_int64, C.c_int, _vp, C.c_int, C.c_int,
+                                  _vp, _vp, C.c_int, _vp, _vp, _vp, _vp]),
+    "xfer_cache_store": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, _vp, C.c_int64, C.c_int64, _vp,
+                                   C.c_int64, C.c_int64, C.c_int, _vp, C.c_int, _vp]),
+    "xfer_cache_attend_workspace": (C.c_int, [C.POINTER(xfer_cache_shape), C.POINTER(xfer_attend),
+                                              C.POINTER(C.c_size_t)]),
+    "xfer_cache_attend": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, C.POINTER(xfer_attend), _vp]),
     "xfer_conn_query": (C.c_int, [_vp, C.c_int, C.POINTER(xfer_chan_state)]),
     "xfer_conn_fifo": (C.c_int, [_vp, C.c_int, C.POINTER(_vp), C.POINTER(C.c_size_t)]),
     "xfer_conn_read_fifo": (C.c_int, [_vp, C.c_int, _vp, C.c_size_t]),
@@ -224,6 +249,17 @@ def _buf(buf, nbytes: int, device: int | None, what: str) -> int:
     return int(buf.data_ptr())
 
 
+def _extent(buf, size: int, given, what: str) -> int:
+    """How many items of `size` bytes a buffer holds: of a tensor, or as given."""
+    if given is not None:
+        if int(given) < 0:
+            raise ValueError("%s: negative count" % what)
+        return int(given)
+    if not hasattr(buf, "numel"):
+        raise ValueError("%s: an address needs its count" % what)
+    return buf.numel() * buf.element_size() // size
+
+
 class Conn:
     """One connection (xfer_conn).  Destroy it only after its streams are idle."""
 
@@ -291,6 +327,32 @@ class Conn:
         offs = (C.c_size_t * max(n, 1))(*offs_l)
         szs = (C.c_size_t * max(n, 1))(*szs_l)
         check(lib().xfer_run_messages(self._h, s, d, offs, szs, n, _stream_handle(stream)))
+
+    def run_blocks(self, src, dst, block_bytes: int, src_ids, dst_ids, src_blocks=None,
+                   dst_blocks=None, n=None, stream=None) -> None:
+        """Moves block src_ids[i] of src to block dst_ids[i] of dst for every i.
+
+        src, dst: pools of blocks of block_bytes; src_ids, dst_ids: int32 lists
+        in device memory.  The pools' block counts and the number of entries
+        follow from tensors and are given for raw addresses."""
+        size = int(block_bytes)
+        if size <= 0:
+            raise ValueError("run_blocks: block_bytes must be positive")
+        sb, db = (_extent(x, size, k, "run_blocks: " + w) for x, k, w in
+                  ((src, src_blocks, "src"), (dst, dst_blocks, "dst")))
+        ns, nd = (_extent(x, 4, n, "run_blocks: " + w) for x, w in
+                  ((src_ids, "src_ids"), (dst_ids, "dst_ids")))
+        if ns != nd:
+            raise ValueError("run_blocks: %d source ids for %d destination ids" % (ns, nd))
+        for x, w in ((src_ids, "src_ids"), (dst_ids, "dst_ids")):
+            if hasattr(x, "dtype") and not str(x.dtype).endswith("int32"):
+                raise TypeError("run_blocks: %s must be int32, got %s" % (w, x.dtype))
+        s = _buf(src, sb * size, self.device, "run_blocks: src")
+        d = _buf(dst, db * size, self.device, "run_blocks: dst")
+        f = _buf(src_ids, ns * 4, self.device, "run_blocks: src_ids")
+        t = _buf(dst_ids, nd * 4, self.device, "run_blocks: dst_ids")
+        check(lib().xfer_run_blocks(self._h, s, sb, d, db, size, f, t, ns,
+                                    _stream_handle(stream)))
 
     def query(self, channel: int) -> dict:
         st = xfer_chan_state()
