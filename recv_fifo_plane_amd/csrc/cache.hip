@@ -314,81 +314,462 @@ struct AttendArgs {
   const int32_t* table;
   const int32_t* lengths;
   const int32_t* starts;
+  float* part;   // [rows * heads][nsplit][D] unnormalised sums of the splits
+  float* stats;  // [rows * heads][nsplit][2] their maxima and sums of weights
   int64_t query_row, query_head, out_row, out_head, table_stride;
   int32_t batch, rows, heads, width;
-  float scale;
+  uint32_t group;         // query heads of one key/value head
+  uint32_t nsplit;        // splits of the tokens
+  uint32_t split_chunks;  // chunks of a split
+  float scale2;           // scale * log2(e): weights are powers of two
   Shape s;
 };
 
-constexpr int kAttendThreads = 256;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Row n of request b sees the tokens 0 .. length_b - (rows of b) + its place.
-// One workgroup per row and head, tokens in chunks of a thread each, with a
-// running maximum m and sum l: o = sum p v / l, p = exp(score - m).
 template <typename E>
-__global__ void __launch_bounds__(kAttendThreads) attend_kernel(AttendArgs A) {
-  __shared__ float s_q[256], s_p[kAttendThreads], s_red[kAttendThreads / 64];
-  __shared__ int64_t s_block[kAttendThreads];
-  const int32_t n = blockIdx.x;
-  const uint32_t hq = blockIdx.y, T = A.s.T, D = A.s.D, tid = threadIdx.x;
-  const uint32_t h = hq / (A.heads / A.s.H);
-  int lo = 0, hi = A.batch;  // last request that starts at or before n
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (A.starts[mid] <= n) lo = mid; else hi = mid;
-  }
-  const int32_t r0 = A.starts[lo], r1 = A.starts[lo + 1];
-  if (n < r0 || n >= r1) return;  // a row of no request
-  const int64_t len = min<int64_t>(max(A.lengths[lo], 0), static_cast<int64_t>(A.width) * T);
-  const int64_t seen = min<int64_t>(len, static_cast<int64_t>(A.lengths[lo]) - (r1 - r0) + (n - r0) + 1);
-  const E* q = static_cast<const E*>(A.query) + n * A.query_row + hq * A.query_head;
-  if (tid < D) s_q[tid] = static_cast<float>(q[tid]);
-  float m = -INFINITY, l = 0.0f, acc = 0.0f;
-  for (int64_t t0 = 0; t0 < seen; t0 += kAttendThreads) {
-    const int64_t t = t0 + tid;
-    int64_t block = -1;
-    if (t < seen) {
-      const int32_t id = A.table[lo * A.table_stride + t / T];
-      if (static_cast<uint32_t>(id) < A.s.blocks) block = id;
+struct Vec8;
+template <>
+struct Vec8<bf16_t> {
+  typedef bf16x8 type;
+};
+template <>
+struct Vec8<fp16_t> {
+  typedef fp16x8 type;
+};
+
+// Eight e4m3 codes times scale, exactly (a power of two, in range).
+__device__ __forceinline__ void widen(uint32_t lo, uint32_t hi, float scale, bf16x8& r) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  r = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ void widen(uint32_t lo, uint32_t hi, float scale, fp16x8& r) {
+  const fp16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
+  const fp16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
+  const fp16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
+  const fp16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
+  r = fp16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(fp16x8 a, fp16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+constexpr int kAttendWaves = 4;
+constexpr int kChunk = 64;  // tokens a wave takes at once
+
+// The rows of one request and key/value head that a workgroup computes.
+struct RowTile {
+  int64_t start;  // first packed row of the request
+  int64_t ahead;  // tokens before its first row's own (negative: rows that see nothing)
+  int32_t seen;   // tokens that the tile's last row sees
+  uint32_t rows;  // rows times group
+};
+
+__device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uint32_t first,
+                                            uint32_t tile_rows) {
+  RowTile r;
+  r.start = A.starts[b];
+  const int64_t queries = static_cast<int64_t>(A.starts[b + 1]) - r.start, length = A.lengths[b];
+  const int64_t held = min<int64_t>(length, static_cast<int64_t>(A.width) * A.s.T);
+  r.ahead = length - queries;
+  r.rows = static_cast<uint32_t>(max<int64_t>(0, min<int64_t>(queries, A.rows)) * A.group);
+  const uint32_t last = min(r.rows, first + tile_rows);
+  r.seen = 0;
+  if (last > first)
+    r.seen = static_cast<int32_t>(
+        max<int64_t>(0, min<int64_t>(held, r.ahead + (last - 1) / A.group + 1)));
+  return r;
+}
+
+// Splits that the tokens of a tile take (at least one: it writes the rows).
+__device__ __forceinline__ uint32_t splits_of(const AttendArgs& A, int32_t seen) {
+  const uint32_t chunks = (static_cast<uint32_t>(seen) + kChunk - 1) / kChunk;
+  return max(1u, min((chunks + A.split_chunks - 1) / A.split_chunks, A.nsplit));
+}
+
+// Row i of a request and key/value head is query row i / group, head i %
+// group of the group.  A workgroup computes NR tiles of 16 rows of one request
+// and key/value head over one split of the tokens: its waves take chunks of 64
+// tokens in turn, each with a running maximum m, sum l and accumulator of its
+// own, and join them at the end.
+//
+// Both products run on the 16x16x32 matrix instruction with the cache's codes
+// as the left operand, straight from the loads: no shared memory, no
+// transposing.  S^T = K Q^T takes 16 tokens by 16 rows a time.  In its result
+// lane (g, n) = (lane / 16, lane % 16) holds row n and the tile's lines 4g + r,
+// so which token sits at line 4g + r of tile t is chosen as 16g + 4t + r: over
+// the four tiles of a chunk a lane then holds the sixteen consecutive tokens
+// 16g .. 16g + 15 of its row.  Those are what O^T = V^T P^T wants from it: its
+// right operand takes eight consecutive tokens of row n from lane (g, n), and
+// its left operand eight consecutive tokens of dim 16e + n, which the cache
+// holds together as V^T.  Sixteen tokens never pass a block's end, so a lane
+// has one block, one key scale and one value scale per chunk: the key scale
+// goes into the scores' multiplier, the value scale into the widening of the
+// codes to bfloat16, where both are exact.
+//
+// Weights are rounded to bfloat16 whatever the query's type: code times scale
+// needs its range, and the error (2^-9 of each weight, at random) stays below
+// the output's own rounding for bfloat16 and near it for float16.
+template <typename E, int D, int NR>
+__global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A) {
+  typedef typename Vec8<E>::type E8;
+  constexpr int KL = D / 32;  // eight-byte loads of a key line
+  constexpr int DT = D / 16;  // tiles of dims
+  constexpr int kPad = D + 4;
+  __shared__ float s_acc[kAttendWaves][16][kPad];
+  __shared__ float s_m[kAttendWaves][NR * 16], s_l[kAttendWaves][NR * 16];
+  const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H, sp = blockIdx.z;
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, g = lane >> 4;
+  const uint32_t T = A.s.T;
+  const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
+  for (uint32_t first = blockIdx.y * NR * 16;; first += gridDim.y * NR * 16) {
+    const RowTile rt = row_tile(A, b, first, NR * 16);
+    if (first >= rt.rows) return;
+    const uint32_t used = splits_of(A, rt.seen);
+    if (sp >= used) continue;
+    const uint32_t c0 = sp * A.split_chunks;
+    uint32_t c1 = (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk;
+    if (sp + 1 < used) c1 = min(c1, c0 + A.split_chunks);
+
+    // Queries: lane (g, n) holds row n's dims 32j + 8g .. + 7.
+    E8 q[NR][KL];
+    int32_t limit[NR];       // last token that the row sees
+    int32_t least = rt.seen;  // the first of them
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const uint32_t i = first + x * 16 + n;
+      const int64_t j = i / A.group, row = rt.start + j;
+      const bool there = i < rt.rows && row >= 0 && row < A.rows;
+      limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
+      const E* p = static_cast<const E*>(A.query) + row * A.query_row +
+                   static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
+#pragma unroll
+      for (int k = 0; k < KL; ++k) {
+        E8 v = {};
+        if (there) __builtin_memcpy(&v, p + 32 * k + 8 * g, 16);
+        q[x][k] = v;
+      }
+      least = min(least, limit[x]);
     }
-    __syncthreads();
-    float x = -INFINITY;
-    if (block >= 0) {
-      const uint8_t* k = A.cache + A.s.key_at(block, h) + (t % T) * D;
-      const float ks = *reinterpret_cast<const float*>(A.cache + A.s.scales_at(block, h));
-      x = 0.0f;
-      for (uint32_t d = 0; d < D; ++d) x += s_q[d] * value_of(k[d]);
-      x *= ks * A.scale;
+    for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+
+    float m[NR], l[NR];
+    f32x4 acc[NR][DT];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    s_block[tid] = block;
-    float top = x;
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if ((tid & 63u) == 0) s_red[tid >> 6] = top;
-    __syncthreads();
-    for (int w = 0; w < kAttendThreads / 64; ++w) top = fmaxf(top, s_red[w]);
-    top = fmaxf(m, top);
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float keep = expf(m - base);
-    m = top;
-    const float p = block >= 0 ? expf(x - base) : 0.0f;
-    s_p[tid] = p;
-    __syncthreads();
-    l *= keep;
-    acc *= keep;
-    const int cnt = static_cast<int>(min<int64_t>(kAttendThreads, seen - t0));
-    for (int i = 0; i < cnt; ++i) {
-      if (s_block[i] < 0) continue;
-      l += s_p[i];
-      if (tid < D) {
-        const uint8_t* v = A.cache + A.s.value_at(s_block[i], h);
-        const float vs = *reinterpret_cast<const float*>(A.cache + A.s.scales_at(s_block[i], h) + 4);
-        acc += s_p[i] * value_of(v[tid * T + (t0 + i) % T]) * vs;
+
+    for (uint32_t c = c0 + wave; c < c1; c += kAttendWaves) {
+      const int32_t t0 = static_cast<int32_t>(c * kChunk);
+      // This lane's block as a holder of scores and values (tokens 16g ..),
+      // and as a loader of key lines (line n is token 16 (n / 4) + 4t + n % 4).
+      // (t0 + 63 passes 2^31 only past every request's tokens, so these compare as unsigned)
+      const uint32_t tg = t0 + 16 * g, tk = t0 + 16 * (n >> 2), seen_all = rt.seen;
+      int32_t bg = tg < seen_all ? table[tg / T] : -1;
+      int32_t bk = tk < seen_all ? table[tk / T] : -1;
+      if (static_cast<uint32_t>(bg) >= A.s.blocks) bg = -1;
+      if (static_cast<uint32_t>(bk) >= A.s.blocks) bk = -1;
+      const uint8_t* kp = A.cache + A.s.key_at(max(bk, 0), h) + (tk % T + (n & 3u)) * D + 8 * g;
+      const uint8_t* vp = A.cache + A.s.value_at(max(bg, 0), h) + n * T + tg % T;
+      const float* sc = reinterpret_cast<const float*>(A.cache + A.s.scales_at(max(bg, 0), h));
+      const float ks = bg < 0 ? 1.0f : sc[0], vs = bg < 0 ? 1.0f : sc[1];
+      u32x2 kc[4][KL];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < KL; ++k)
+          kc[t][k] = *reinterpret_cast<const u32x2*>(kp + 4 * t * D + 32 * k);
+      u32x4 vc[DT];
+#pragma unroll
+      for (int e = 0; e < DT; ++e) vc[e] = *reinterpret_cast<const u32x4*>(vp + 16 * e * T);
+
+      f32x4 s[NR][4];
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < KL; ++k) {
+          E8 a;
+          widen(kc[t][k][0], kc[t][k][1], 1.0f, a);
+#pragma unroll
+          for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, q[x][k], s[x][t]);
+        }
+
+      const bool whole = t0 <= least - (kChunk - 1) && __ballot(bg < 0) == 0;
+      const float mul = ks * A.scale2;
+      bf16x8 p[NR][2];
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        // (of this lane's sixteen tokens; a lane's tokens are past no limit or start below 2^31)
+        const int32_t seen = bg < 0 ? 0 : limit[x] - static_cast<int32_t>(tg) + 1;
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float v = s[x][t][r] * mul;
+            if (!whole && 4 * t + r >= seen) v = -INFINITY;
+            s[x][t][r] = v;
+            top = fmaxf(top, v);
+          }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        top = fmaxf(top, m[x]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float keep = __builtin_amdgcn_exp2f(m[x] - base);
+        m[x] = top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = __builtin_amdgcn_exp2f(s[x][t][r] - base);
+            sum += w;
+            p[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w);
+          }
+        l[x] = l[x] * keep + sum;
+        if (__ballot(keep != 1.0f) != 0) {
+#pragma unroll
+          for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+        }
+      }
+
+      bool nan_codes = false;
+      if (!whole) {
+        // Codes of tokens that no row sees are cleared: they may be anything,
+        // and 0 times NaN is NaN.
+        const int32_t held = bg < 0 ? 0 : rt.seen - static_cast<int32_t>(tg);
+        uint32_t nans = 0;
+#pragma unroll
+        for (int e = 0; e < DT; ++e)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int left = held - 4 * w;
+            vc[e][w] &= left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+            nans |= (vc[e][w] & 0x7F7F7F7Fu) + 0x01010101u;
+          }
+        nan_codes = __ballot((nans & 0x80808080u) != 0) != 0;
+      }
+#pragma unroll
+      for (int e = 0; e < DT; ++e) {
+        bf16x8 a, z;
+        if (nan_codes) {
+          // A NaN among the others reaches the rows that see its token and no
+          // other: it is taken out and counted for them by a product of its own.
+          uint32_t is[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            is[w] = (((vc[e][w] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
+            vc[e][w] &= ~(is[w] * 0xFFu);
+          }
+          widen(is[0] * 0x38u, is[1] * 0x38u, 1.0f, a);  // (0x38 is 1)
+          widen(is[2] * 0x38u, is[3] * 0x38u, 1.0f, z);
+#pragma unroll
+          for (int x = 0; x < NR; ++x) {
+            const int32_t seen = bg < 0 ? 0 : limit[x] - static_cast<int32_t>(tg) + 1;
+            bf16x8 lo, hi;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              lo[i] = static_cast<bf16_t>(i < seen ? 1.0f : 0.0f);
+              hi[i] = static_cast<bf16_t>(i + 8 < seen ? 1.0f : 0.0f);
+            }
+            const f32x4 hit = mfma(z, hi, mfma(a, lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (hit[r] != 0.0f) acc[x][e][r] = NAN;
+          }
+        }
+        widen(vc[e][0], vc[e][1], vs, a);
+        widen(vc[e][2], vc[e][3], vs, z);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+          acc[x][e] = mfma(a, p[x][0], acc[x][e]);
+          acc[x][e] = mfma(z, p[x][1], acc[x][e]);
+        }
       }
     }
+
+    // Join the waves.
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      l[x] += __shfl_xor(l[x], 16);
+      l[x] += __shfl_xor(l[x], 32);
+      if (g == 0) {
+        s_m[wave][x * 16 + n] = m[x];
+        s_l[wave][x * 16 + n] = l[x];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      float top = s_m[0][x * 16 + n];
+      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, s_m[w][x * 16 + n]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      const float f = __builtin_amdgcn_exp2f(m[x] - base);
+#pragma unroll
+      for (int e = 0; e < DT; ++e)
+        *reinterpret_cast<f32x4*>(&s_acc[wave][n][16 * e + 4 * g]) = acc[x][e] * f;
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
+        const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + x * 16 + r;
+        const int64_t row = rt.start + ri / A.group;
+        if (ri >= rt.rows || row < 0 || row >= A.rows) continue;
+        float top = s_m[0][x * 16 + r], sum = 0.0f;
+        for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, s_m[w][x * 16 + r]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = 0; w < kAttendWaves; ++w) {
+          sum += s_l[w][x * 16 + r] * __builtin_amdgcn_exp2f(s_m[w][x * 16 + r] - base);
+          o += *reinterpret_cast<const f32x4*>(&s_acc[w][r][d]);
+        }
+        const uint32_t head = h * A.group + ri % A.group;
+        const int64_t at = row * A.heads + head;
+        if (used == 1) {
+          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+          E v[4];
+          for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+          __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + d, v, 8);
+          if (d == 0 && A.lse)
+            A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<f32x4*>(A.part + (at * A.nsplit + sp) * D + d) = o;
+          if (d == 0) {
+            A.stats[(at * A.nsplit + sp) * 2] = top;
+            A.stats[(at * A.nsplit + sp) * 2 + 1] = sum;
+          }
+        }
+      }
+      __syncthreads();
+    }
   }
-  E* o = static_cast<E*>(A.out) + n * A.out_row + hq * A.out_head;
-  if (tid < D) o[tid] = static_cast<E>(l != 0.0f ? acc / l : 0.0f);
-  if (tid == 0 && A.lse) A.lse[static_cast<int64_t>(n) * A.heads + hq] = m + logf(l);
+}
+
+constexpr int kJoinThreads = 256;
+
+// Joins the splits of the rows that took more than one: a wave per row and
+// head, splits in order, so the result does not depend on when they ran.
+template <typename E, int D, int NR>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 64) + (threadIdx.x >> 6);
+  const int64_t row = at / A.heads;
+  if (row >= A.rows) return;
+  const uint32_t head = static_cast<uint32_t>(at % A.heads), lane = threadIdx.x & 63u;
+  int lo = 0, hi = A.batch;  // the last request that starts at or before the row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (A.starts[mid] <= row)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int64_t j = row - A.starts[lo];
+  if (j < 0 || row >= A.starts[lo + 1]) return;
+  const uint32_t i = static_cast<uint32_t>(j) * A.group + head % A.group;
+  const RowTile rt = row_tile(A, lo, i / (NR * 16) * (NR * 16), NR * 16);
+  const uint32_t used = splits_of(A, rt.seen);
+  if (used == 1) return;
+  const float* st = A.stats + at * A.nsplit * 2;
+  float top = -INFINITY;
+  for (uint32_t s = 0; s < used; ++s) top = fmaxf(top, st[2 * s]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  constexpr int kPer = (D + 63) / 64;
+  float o[kPer] = {}, sum = 0.0f;
+  for (uint32_t s = 0; s < used; ++s) {
+    const float f = __builtin_amdgcn_exp2f(st[2 * s] - base);
+    sum += st[2 * s + 1] * f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (k * 64 + lane < D) o[k] += A.part[(at * A.nsplit + s) * D + k * 64 + lane] * f;
+  }
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  E* out = static_cast<E*>(A.out) + row * A.out_row + head * A.out_head;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (k * 64 + lane < D) out[k * 64 + lane] = static_cast<E>(o[k] * inv);
+  if (lane == 0 && A.lse) A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
+
+using AttendFn = void (*)(AttendArgs);
+struct AttendKernels {
+  AttendFn attend, join;
+};
+
+template <typename E, int D, int NR>
+AttendKernels attend_of() {
+  return AttendKernels{attend_kernel<E, D, NR>, join_kernel<E, D, NR>};
+}
+
+template <typename E, int D>
+AttendKernels pick_attend_rows(int nr) {
+  if constexpr (D <= 128) {
+    if (nr == 2) return attend_of<E, D, 2>();
+  }
+  return attend_of<E, D, 1>();
+}
+
+template <typename E>
+AttendKernels pick_attend(uint32_t d, int nr) {
+  switch (d) {
+    case 64: return pick_attend_rows<E, 64>(nr);
+    case 96: return pick_attend_rows<E, 96>(nr);
+    case 128: return pick_attend_rows<E, 128>(nr);
+    case 192: return pick_attend_rows<E, 192>(nr);
+    default: return pick_attend_rows<E, 256>(nr);
+  }
+}
+
+// The launch of a call: row tiles of a workgroup, and splits.
+struct AttendPlan {
+  int nr;
+  uint32_t tiles, nsplit, split_chunks;
+};
+
+AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
+  AttendPlan p;
+  const int64_t group = q.heads / int(s.H);
+  int64_t most = q.max_query ? std::min(q.max_query, q.rows) : q.rows;
+  if (!q.max_query && q.rows <= q.batch) most = 1;
+  const int64_t rows = most * group;
+  p.nr = rows <= 16 || s.D > 128 ? 1 : 2;
+  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.nr * 16 - 1) / (p.nr * 16)));
+  const int64_t width = int64_t(q.table_width) * s.T;
+  const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
+  const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
+  // Splits until the launch has about 1024 workgroups, each of at least four chunks a wave.
+  const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
+  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, wgs));
+  const int64_t least = 4 * kAttendWaves;
+  p.split_chunks = uint32_t(std::max<int64_t>(least, (chunks + want - 1) / want));
+  p.nsplit = uint32_t(std::min<int64_t>(64, (chunks + p.split_chunks - 1) / p.split_chunks));
+  return p;
+}
+
+size_t attend_part_bytes(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
+  return p.nsplit == 1 ? 0 : size_t(q.rows) * size_t(q.heads) * p.nsplit * s.D * sizeof(float);
+}
+size_t attend_work_bytes(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
+  return p.nsplit == 1 ? 0
+                       : attend_part_bytes(s, q, p) +
+                             size_t(q.rows) * size_t(q.heads) * p.nsplit * 2 * sizeof(float);
 }
 
 // ------------------------------------------------------------------ checks
@@ -528,7 +909,7 @@ extern "C" int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const 
   const int rc = attend_args(shape, q, "xfer_cache_attend_workspace", &s);
   if (rc) return rc;
   if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_cache_attend_workspace: NULL bytes");
-  *bytes = 0;
+  *bytes = attend_work_bytes(s, *q, attend_plan(s, *q));
   return XFER_OK;
 }
 
@@ -561,12 +942,28 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
   a.rows = q->rows;
   a.heads = q->heads;
   a.width = q->table_width;
-  a.scale = q->scale;
-  const dim3 grid(uint32_t(q->rows), uint32_t(q->heads));
+  a.group = uint32_t(q->heads) / a.s.H;
+  a.scale2 = q->scale * 1.44269504088896341f;
+  const AttendPlan p = attend_plan(a.s, *q);
+  a.nsplit = p.nsplit;
+  a.split_chunks = p.split_chunks;
+  const size_t need = attend_work_bytes(a.s, *q, p);
+  if (need && (!q->workspace || q->workspace_bytes < need || !aligned(q->workspace, 16)))
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_cache_attend: the workspace must hold xfer_cache_attend_workspace() bytes, "
+                "16-byte aligned");
+  a.part = static_cast<float*>(q->workspace);
+  a.stats = need ? a.part + attend_part_bytes(a.s, *q, p) / sizeof(float) : nullptr;
+  const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr)
+                                                : pick_attend<fp16_t>(a.s.D, p.nr);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = q->dtype == XFER_BF16
-                           ? launch(attend_kernel<bf16_t>, a, grid, kAttendThreads, s)
-                           : launch(attend_kernel<fp16_t>, a, grid, kAttendThreads, s);
+  hipError_t e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles, p.nsplit),
+                        kAttendWaves * 64, s);
   if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
+  if (p.nsplit > 1) {
+    const int64_t waves = int64_t(q->rows) * q->heads, per = kJoinThreads / 64;
+    e = launch(k.join, a, dim3(uint32_t((waves + per - 1) / per)), kJoinThreads, s);
+    if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
+  }
   return XFER_OK;
 }

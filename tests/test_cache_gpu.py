@@ -439,6 +439,19 @@ def test_attend_not_finite():
     assert np.isnan(got[1, 2:, 9]).all() and np.isnan(got[1]).sum() == 2
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attend_nan_of_unseen_tokens(dtype):
+    """A NaN stored for a token reaches the rows that see it, not the earlier ones of its tile."""
+    def edit(q, c, t):
+        c.v[t[0, 1], 0, 9, 5] = 127       # token 25 of 40, whose rows are tokens 20 .. 39
+        c.k[t[0, 2], 1, 1, 3] = 255       # token 33
+        c.v[t[1, 6], 1, 0, 100] = 255     # token 96 of 130
+    got, lse = check_attend([40, 130], [20, 60], 16, 2, 3, 128, dtype, seed=8, edit=edit)
+    assert not np.isnan(got[:5, :3]).any() and np.isnan(got[5:20, :3, 5]).all()
+    assert not np.isnan(got[:13, 3:]).any() and np.isnan(got[13:20, 3:]).all()
+    assert np.isnan(got[46:, 3:, 100]).all() and not np.isnan(got[20:46]).any()
+
+
 def test_attend_nothing():
     ref = new_pool(4, 16, 2, 64, 1)
     gpu = gpu_cache(ref)
