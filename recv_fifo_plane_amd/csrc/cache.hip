@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "xfer.h"
 
@@ -44,6 +45,7 @@ hipError_t launch(Fn fn, const Args& a, dim3 grid, int block, hipStream_t s) {
 struct Shape {
   uint64_t block_bytes;
   uint32_t T, H, D, blocks;
+  uint32_t log2T;
   __device__ uint64_t key_at(uint32_t block, uint32_t h) const {
     return block * block_bytes + static_cast<uint64_t>(2u * h) * T * D;
   }
@@ -390,6 +392,8 @@ __device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uin
   if (last > first)
     r.seen = static_cast<int32_t>(
         max<int64_t>(0, min<int64_t>(held, r.ahead + (last - 1) / A.group + 1)));
+  r.seen = __builtin_amdgcn_readfirstlane(r.seen);  // (the same in every lane)
+  r.rows = __builtin_amdgcn_readfirstlane(r.rows);
   return r;
 }
 
@@ -397,6 +401,191 @@ __device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uin
 __device__ __forceinline__ uint32_t splits_of(const AttendArgs& A, int32_t seen) {
   const uint32_t chunks = (static_cast<uint32_t>(seen) + kChunk - 1) / kChunk;
   return max(1u, min((chunks + A.split_chunks - 1) / A.split_chunks, A.nsplit));
+}
+
+// A lane's blocks in a chunk: as the holder of scores and values of tokens
+// 16g .. (-1: none), and as a loader of key lines (line n is token 16 (n / 4) +
+// 4t + n % 4; any block where there is none).
+struct Place {
+  int32_t mine, line;
+  // (seen > 0; the entries of tokens past it are those of the last)
+  __device__ __forceinline__ void look(const AttendArgs& A, const int32_t* table, uint32_t t0,
+                                       uint32_t seen, uint32_t g, uint32_t n) {
+    mine = table[min(t0 + 16 * g, seen - 1) >> A.s.log2T];
+    line = table[min(t0 + 16 * (n >> 2), seen - 1) >> A.s.log2T];
+  }
+  __device__ __forceinline__ void settle(const AttendArgs& A, uint32_t t0, uint32_t seen, uint32_t g) {
+    if (static_cast<uint32_t>(mine) >= A.s.blocks || t0 + 16 * g >= seen) mine = -1;
+    if (static_cast<uint32_t>(line) >= A.s.blocks) line = 0;
+  }
+};
+
+// The dims of lane group g in step k of 32: sixteen-byte loads of the keys
+// serve two steps where D allows.
+template <int D>
+__device__ __forceinline__ uint32_t key_dim(uint32_t k, uint32_t g) {
+  if constexpr (D % 64 == 0)
+    return 64 * (k / 2) + 16 * g + 8 * (k % 2);
+  else
+    return 32 * k + 8 * g;
+}
+
+// Workgroups a CU is to hold: bounds the registers of a lane.
+constexpr int attend_resident(int d, int nr) {
+  return nr == 1 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1);
+}
+
+template <bool ONCE, typename V>
+__device__ __forceinline__ V fetch(const uint8_t* p) {
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else
+    return *reinterpret_cast<const V*>(p);
+}
+
+template <int D, bool ONCE>
+struct Keys {
+  static constexpr bool kWide = D % 64 == 0;
+  u32x4 w[4][kWide ? D / 64 : 1];
+  u32x2 d[4][kWide ? 1 : D / 32];
+  __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
+                                       uint32_t g, uint32_t n) {
+    const uint32_t tk = t0 + 16 * (n >> 2);
+    const uint8_t* p = A.cache + A.s.key_at(at.line, h) +
+                       ((tk & (A.s.T - 1)) + (n & 3u)) * D + (kWide ? 16 : 8) * g;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+          w[t][j] = fetch<ONCE, u32x4>(p + 4 * t * D + 64 * j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          d[t][j] = fetch<ONCE, u32x2>(p + 4 * t * D + 32 * j);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t lo(int t, int k) const {
+    if constexpr (kWide)
+      return w[t][k / 2][k % 2 * 2];
+    else
+      return d[t][k][0];
+  }
+  __device__ __forceinline__ uint32_t hi(int t, int k) const {
+    if constexpr (kWide)
+      return w[t][k / 2][k % 2 * 2 + 1];
+    else
+      return d[t][k][1];
+  }
+};
+
+// NaN for each of the dims d .. d + 3 in which one of the tokens t0 .. last
+// has a NaN code, 0 for the others.  Rarely run, so it is a plain loop.
+__device__ __forceinline__ f32x4 seen_nans(const AttendArgs& A, const int32_t* table,
+                                                       uint32_t h, int32_t t0, int32_t last,
+                                                       uint32_t d) {
+  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma clang loop unroll(disable)
+  for (int32_t t = t0; t <= last; ++t) {
+    const int32_t id = table[t >> A.s.log2T];
+    if (static_cast<uint32_t>(id) >= A.s.blocks) continue;
+    const uint8_t* v = A.cache + A.s.value_at(id, h) + (t & (A.s.T - 1));
+#pragma clang loop unroll(disable)
+    for (uint32_t k = 0; k < 4; ++k)
+      if ((v[static_cast<uint64_t>(d + k) * A.s.T] & 0x7F) == 0x7F) r[k] = NAN;
+  }
+  return r;
+}
+
+// The weights of a chunk's scores and their product with the values.  MASK:
+// some row does not see some token of the chunk.
+template <bool MASK, bool TWO, int DT, int NR>
+__device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f32x4 (&acc)[NR][DT],
+                                      float (&m)[NR], float (&l)[NR], const u32x4 (&vc)[DT],
+                                      const int32_t (&limit)[NR], float mul, float vs,
+                                      int32_t seen_all, int32_t tg, int32_t bg,
+                                      const int32_t* table, uint32_t h, int32_t t0, uint32_t g) {
+  bf16x8 p[NR][2], p2[NR][2];
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const int32_t seen = bg < 0 ? 0 : limit[x] - tg + 1;  // of this lane's sixteen tokens
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v = s[x][t][r] * mul;
+        if (MASK && 4 * t + r >= seen) v = -INFINITY;
+        s[x][t][r] = v;
+        top = fmaxf(top, v);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    top = fmaxf(top, m[x]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float keep = __builtin_amdgcn_exp2f(m[x] - base);
+    m[x] = top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w = __builtin_amdgcn_exp2f(s[x][t][r] - base);
+        sum += w;
+        const bf16_t first = static_cast<bf16_t>(w);
+        p[x][t >> 1][(t & 1) * 4 + r] = first;
+        if constexpr (TWO)
+          p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
+      }
+    l[x] = l[x] * keep + sum;
+#pragma unroll
+    for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+  }
+  // Codes of tokens that no row sees are cleared: they may be anything, and 0
+  // times NaN is NaN.
+  uint32_t mask[4];
+  if constexpr (MASK) {
+    const int32_t held = bg < 0 ? 0 : seen_all - tg;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int left = held - 4 * w;
+      mask[w] = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < DT; ++e) {
+    u32x4 v = vc[e];
+    if constexpr (MASK) {
+      u32x4 nan;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v[w] &= mask[w];
+        nan[w] = (((v[w] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
+      }
+      if (__ballot((nan[0] | nan[1] | nan[2] | nan[3]) != 0) != 0) {
+        // A NaN among the others reaches the rows that see its token and no
+        // other: it is taken out here and looked for again in memory.
+#pragma unroll
+        for (int w = 0; w < 4; ++w) v[w] &= ~(nan[w] * 0xFFu);
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+          acc[x][e] += seen_nans(A, table, h, t0, min(t0 + kChunk - 1, limit[x]), 16 * e + 4 * g);
+      }
+    }
+    bf16x8 a, z;
+    widen(v[0], v[1], vs, a);
+    widen(v[2], v[3], vs, z);
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      acc[x][e] = mfma(a, p[x][0], acc[x][e]);
+      acc[x][e] = mfma(z, p[x][1], acc[x][e]);
+      if constexpr (TWO) {
+        acc[x][e] = mfma(a, p2[x][0], acc[x][e]);
+        acc[x][e] = mfma(z, p2[x][1], acc[x][e]);
+      }
+    }
+  }
 }
 
 // Row i of a request and key/value head is query row i / group, head i %
@@ -419,19 +608,23 @@ __device__ __forceinline__ uint32_t splits_of(const AttendArgs& A, int32_t seen)
 // goes into the scores' multiplier, the value scale into the widening of the
 // codes to bfloat16, where both are exact.
 //
-// Weights are rounded to bfloat16 whatever the query's type: code times scale
-// needs its range, and the error (2^-9 of each weight, at random) stays below
-// the output's own rounding for bfloat16 and near it for float16.
-template <typename E, int D, int NR>
-__global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A) {
+// Weights are bfloat16 whatever the query's type: code times scale needs its
+// range.  Rounding them is off by up to 2^-8 of each weight, at random; that is
+// below the output's own rounding for bfloat16 queries.  For float16 it would
+// be above, so there a weight goes in two parts, the rounded one and the
+// rounded rest (off by 2^-16), at one more product each.
+template <typename E, int D, int NR, bool ONCE>
+__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
   typedef typename Vec8<E>::type E8;
-  constexpr int KL = D / 32;  // eight-byte loads of a key line
+  constexpr int KL = D / 32;  // steps of 32 dims
   constexpr int DT = D / 16;  // tiles of dims
+  constexpr bool kTwo = __is_same(E, fp16_t);  // weights in two parts
   constexpr int kPad = D + 4;
   __shared__ float s_acc[kAttendWaves][16][kPad];
   __shared__ float s_m[kAttendWaves][NR * 16], s_l[kAttendWaves][NR * 16];
   const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H, sp = blockIdx.z;
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, n = lane & 15u, g = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
   const uint32_t T = A.s.T;
   const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
   for (uint32_t first = blockIdx.y * NR * 16;; first += gridDim.y * NR * 16) {
@@ -443,7 +636,7 @@ __global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A)
     uint32_t c1 = (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk;
     if (sp + 1 < used) c1 = min(c1, c0 + A.split_chunks);
 
-    // Queries: lane (g, n) holds row n's dims 32j + 8g .. + 7.
+    // Queries: lane (g, n) holds row n's dims in the order of its key loads.
     E8 q[NR][KL];
     int32_t limit[NR];       // last token that the row sees
     int32_t least = rt.seen;  // the first of them
@@ -458,12 +651,13 @@ __global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A)
 #pragma unroll
       for (int k = 0; k < KL; ++k) {
         E8 v = {};
-        if (there) __builtin_memcpy(&v, p + 32 * k + 8 * g, 16);
+        if (there) __builtin_memcpy(&v, p + key_dim<D>(k, g), 16);
         q[x][k] = v;
       }
       least = min(least, limit[x]);
     }
     for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+    least = __builtin_amdgcn_readfirstlane(least);
 
     float m[NR], l[NR];
     f32x4 acc[NR][DT];
@@ -475,29 +669,30 @@ __global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A)
       for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    for (uint32_t c = c0 + wave; c < c1; c += kAttendWaves) {
+    // A chunk's keys are loaded while the chunk before is still at its
+    // weights and values, and its table entries one step earlier.
+    const uint32_t seen_all = __builtin_amdgcn_readfirstlane(rt.seen);
+    Keys<D, ONCE> keys;
+    Place at, next;
+    if (c0 + wave < c1) {
+      const uint32_t t0 = (c0 + wave) * kChunk;
+      at.look(A, table, t0, seen_all, g, n);
+      at.settle(A, t0, seen_all, g);
+      keys.load(A, at, t0, h, g, n);
+    }
+    uint32_t c = c0 + wave;
+    auto step = [&](auto masked) {
       const int32_t t0 = static_cast<int32_t>(c * kChunk);
-      // This lane's block as a holder of scores and values (tokens 16g ..),
-      // and as a loader of key lines (line n is token 16 (n / 4) + 4t + n % 4).
-      // (t0 + 63 passes 2^31 only past every request's tokens, so these compare as unsigned)
-      const uint32_t tg = t0 + 16 * g, tk = t0 + 16 * (n >> 2), seen_all = rt.seen;
-      int32_t bg = tg < seen_all ? table[tg / T] : -1;
-      int32_t bk = tk < seen_all ? table[tk / T] : -1;
-      if (static_cast<uint32_t>(bg) >= A.s.blocks) bg = -1;
-      if (static_cast<uint32_t>(bk) >= A.s.blocks) bk = -1;
-      const uint8_t* kp = A.cache + A.s.key_at(max(bk, 0), h) + (tk % T + (n & 3u)) * D + 8 * g;
-      const uint8_t* vp = A.cache + A.s.value_at(max(bg, 0), h) + n * T + tg % T;
+      const uint32_t tg = t0 + 16 * g, ahead = t0 + kAttendWaves * kChunk;
+      next.look(A, table, ahead, seen_all, g, n);
+      const int32_t bg = at.mine;
+      const uint8_t* vp = A.cache + A.s.value_at(max(bg, 0), h) + n * T + (tg & (T - 1));
       const float* sc = reinterpret_cast<const float*>(A.cache + A.s.scales_at(max(bg, 0), h));
-      const float ks = bg < 0 ? 1.0f : sc[0], vs = bg < 0 ? 1.0f : sc[1];
-      u32x2 kc[4][KL];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int k = 0; k < KL; ++k)
-          kc[t][k] = *reinterpret_cast<const u32x2*>(kp + 4 * t * D + 32 * k);
+      float ks = sc[0], vs = sc[1];
       u32x4 vc[DT];
 #pragma unroll
-      for (int e = 0; e < DT; ++e) vc[e] = *reinterpret_cast<const u32x4*>(vp + 16 * e * T);
+      for (int e = 0; e < DT; ++e) vc[e] = fetch<ONCE, u32x4>(vp + 16 * e * T);
+      __builtin_amdgcn_sched_barrier(0);
 
       f32x4 s[NR][4];
 #pragma unroll
@@ -509,104 +704,24 @@ __global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A)
 #pragma unroll
         for (int k = 0; k < KL; ++k) {
           E8 a;
-          widen(kc[t][k][0], kc[t][k][1], 1.0f, a);
+          widen(keys.lo(t, k), keys.hi(t, k), 1.0f, a);
 #pragma unroll
           for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, q[x][k], s[x][t]);
         }
-
-      const bool whole = t0 <= least - (kChunk - 1) && __ballot(bg < 0) == 0;
-      const float mul = ks * A.scale2;
-      bf16x8 p[NR][2];
-#pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        // (of this lane's sixteen tokens; a lane's tokens are past no limit or start below 2^31)
-        const int32_t seen = bg < 0 ? 0 : limit[x] - static_cast<int32_t>(tg) + 1;
-        float top = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float v = s[x][t][r] * mul;
-            if (!whole && 4 * t + r >= seen) v = -INFINITY;
-            s[x][t][r] = v;
-            top = fmaxf(top, v);
-          }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        top = fmaxf(top, m[x]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float keep = __builtin_amdgcn_exp2f(m[x] - base);
-        m[x] = top;
-        float sum = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float w = __builtin_amdgcn_exp2f(s[x][t][r] - base);
-            sum += w;
-            p[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w);
-          }
-        l[x] = l[x] * keep + sum;
-        if (__ballot(keep != 1.0f) != 0) {
-#pragma unroll
-          for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
-        }
-      }
-
-      bool nan_codes = false;
-      if (!whole) {
-        // Codes of tokens that no row sees are cleared: they may be anything,
-        // and 0 times NaN is NaN.
-        const int32_t held = bg < 0 ? 0 : rt.seen - static_cast<int32_t>(tg);
-        uint32_t nans = 0;
-#pragma unroll
-        for (int e = 0; e < DT; ++e)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int left = held - 4 * w;
-            vc[e][w] &= left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-            nans |= (vc[e][w] & 0x7F7F7F7Fu) + 0x01010101u;
-          }
-        nan_codes = __ballot((nans & 0x80808080u) != 0) != 0;
-      }
-#pragma unroll
-      for (int e = 0; e < DT; ++e) {
-        bf16x8 a, z;
-        if (nan_codes) {
-          // A NaN among the others reaches the rows that see its token and no
-          // other: it is taken out and counted for them by a product of its own.
-          uint32_t is[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            is[w] = (((vc[e][w] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
-            vc[e][w] &= ~(is[w] * 0xFFu);
-          }
-          widen(is[0] * 0x38u, is[1] * 0x38u, 1.0f, a);  // (0x38 is 1)
-          widen(is[2] * 0x38u, is[3] * 0x38u, 1.0f, z);
-#pragma unroll
-          for (int x = 0; x < NR; ++x) {
-            const int32_t seen = bg < 0 ? 0 : limit[x] - static_cast<int32_t>(tg) + 1;
-            bf16x8 lo, hi;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              lo[i] = static_cast<bf16_t>(i < seen ? 1.0f : 0.0f);
-              hi[i] = static_cast<bf16_t>(i + 8 < seen ? 1.0f : 0.0f);
-            }
-            const f32x4 hit = mfma(z, hi, mfma(a, lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}));
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (hit[r] != 0.0f) acc[x][e][r] = NAN;
-          }
-        }
-        widen(vc[e][0], vc[e][1], vs, a);
-        widen(vc[e][2], vc[e][3], vs, z);
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          acc[x][e] = mfma(a, p[x][0], acc[x][e]);
-          acc[x][e] = mfma(z, p[x][1], acc[x][e]);
-        }
-      }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+      next.settle(A, ahead, seen_all, g);
+      if (c + kAttendWaves < c1) keys.load(A, next, ahead, h, g, n);
+      __builtin_amdgcn_sched_barrier(0);
+      if (bg < 0) ks = vs = 1.0f;  // (of a block that is not the request's: anything)
+      weigh<decltype(masked)::value, kTwo, DT, NR>(A, s, acc, m, l, vc, limit, ks * A.scale2, vs,
+                                                   seen_all, tg, bg, table, h, t0, g);
+      at = next;
+      c += kAttendWaves;
+    };
+    // Chunks that every row sees whole, up to the first that is not; then the rest.
+    const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
+    while (c < whole && __ballot(at.mine < 0) == 0) step(std::false_type());
+    while (c < c1) step(std::true_type());
 
     // Join the waves.
 #pragma unroll
@@ -665,14 +780,17 @@ __global__ void __launch_bounds__(kAttendWaves * 64) attend_kernel(AttendArgs A)
 
 constexpr int kJoinThreads = 256;
 
-// Joins the splits of the rows that took more than one: a wave per row and
-// head, splits in order, so the result does not depend on when they ran.
+// Joins the splits of the rows that took more than one: a workgroup per row
+// and head, D / 4 threads wide, whose groups of threads take the splits in
+// turn and are then added in order, so the result does not depend on when the
+// splits ran.
 template <typename E, int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 64) + (threadIdx.x >> 6);
-  const int64_t row = at / A.heads;
-  if (row >= A.rows) return;
-  const uint32_t head = static_cast<uint32_t>(at % A.heads), lane = threadIdx.x & 63u;
+  constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide;
+  __shared__ f32x4 s_o[kGroups][kWide];
+  __shared__ float s_sum[kGroups];
+  const int64_t row = blockIdx.x;
+  const uint32_t head = blockIdx.y, tid = threadIdx.x, grp = tid / kWide, d = tid % kWide;
   int lo = 0, hi = A.batch;  // the last request that starts at or before the row
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -687,25 +805,34 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
   const RowTile rt = row_tile(A, lo, i / (NR * 16) * (NR * 16), NR * 16);
   const uint32_t used = splits_of(A, rt.seen);
   if (used == 1) return;
+  const int64_t at = row * A.heads + head;
   const float* st = A.stats + at * A.nsplit * 2;
   float top = -INFINITY;
-  for (uint32_t s = 0; s < used; ++s) top = fmaxf(top, st[2 * s]);
+  for (uint32_t s = tid & 63u; s < used; s += 64) top = fmaxf(top, st[2 * s]);
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
   const float base = top == -INFINITY ? 0.0f : top;
-  constexpr int kPer = (D + 63) / 64;
-  float o[kPer] = {}, sum = 0.0f;
-  for (uint32_t s = 0; s < used; ++s) {
-    const float f = __builtin_amdgcn_exp2f(st[2 * s] - base);
-    sum += st[2 * s + 1] * f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (k * 64 + lane < D) o[k] += A.part[(at * A.nsplit + s) * D + k * 64 + lane] * f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  float sum = 0.0f;
+  if (grp < kGroups) {
+    for (uint32_t s = grp; s < used; s += kGroups) {
+      const float f = __builtin_amdgcn_exp2f(st[2 * s] - base);
+      sum += st[2 * s + 1] * f;
+      o += *reinterpret_cast<const f32x4*>(A.part + (at * A.nsplit + s) * D + 4 * d) * f;
+    }
+    s_o[grp][d] = o;
+    if (d == 0) s_sum[grp] = sum;
+  }
+  __syncthreads();
+  if (tid >= kWide) return;
+  for (uint32_t k = 1; k < kGroups; ++k) {
+    o += s_o[k][d];
+    sum += s_sum[k];
   }
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  E* out = static_cast<E*>(A.out) + row * A.out_row + head * A.out_head;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    if (k * 64 + lane < D) out[k * 64 + lane] = static_cast<E>(o[k] * inv);
-  if (lane == 0 && A.lse) A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+  E v[4];
+  for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+  __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
+  if (d == 0 && A.lse) A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 using AttendFn = void (*)(AttendArgs);
@@ -713,27 +840,23 @@ struct AttendKernels {
   AttendFn attend, join;
 };
 
-template <typename E, int D, int NR>
-AttendKernels attend_of() {
-  return AttendKernels{attend_kernel<E, D, NR>, join_kernel<E, D, NR>};
-}
-
 template <typename E, int D>
-AttendKernels pick_attend_rows(int nr) {
+AttendKernels pick_attend_rows(int nr, bool once) {
   if constexpr (D <= 128) {
-    if (nr == 2) return attend_of<E, D, 2>();
+    if (nr == 2) return {attend_kernel<E, D, 2, false>, join_kernel<E, D, 2>};
   }
-  return attend_of<E, D, 1>();
+  if (once) return {attend_kernel<E, D, 1, true>, join_kernel<E, D, 1>};
+  return {attend_kernel<E, D, 1, false>, join_kernel<E, D, 1>};
 }
 
 template <typename E>
-AttendKernels pick_attend(uint32_t d, int nr) {
+AttendKernels pick_attend(uint32_t d, int nr, bool once) {
   switch (d) {
-    case 64: return pick_attend_rows<E, 64>(nr);
-    case 96: return pick_attend_rows<E, 96>(nr);
-    case 128: return pick_attend_rows<E, 128>(nr);
-    case 192: return pick_attend_rows<E, 192>(nr);
-    default: return pick_attend_rows<E, 256>(nr);
+    case 64: return pick_attend_rows<E, 64>(nr, once);
+    case 96: return pick_attend_rows<E, 96>(nr, once);
+    case 128: return pick_attend_rows<E, 128>(nr, once);
+    case 192: return pick_attend_rows<E, 192>(nr, once);
+    default: return pick_attend_rows<E, 256>(nr, once);
   }
 }
 
@@ -759,7 +882,8 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, wgs));
   const int64_t least = 4 * kAttendWaves;
   p.split_chunks = uint32_t(std::max<int64_t>(least, (chunks + want - 1) / want));
-  p.nsplit = uint32_t(std::min<int64_t>(64, (chunks + p.split_chunks - 1) / p.split_chunks));
+  p.split_chunks = uint32_t(std::max<int64_t>(p.split_chunks, (chunks + 255) / 256));
+  p.nsplit = uint32_t((chunks + p.split_chunks - 1) / p.split_chunks);
   return p;
 }
 
@@ -789,6 +913,7 @@ int shape_of(const xfer_cache_shape* g, const char* who, Shape* out) {
     return fail(XFER_ERR_INVALID_ARG,
                 std::string(who) + ": blocks must be >= 1 and hold at most 2^31 - 1 tokens");
   out->T = uint32_t(g->block_tokens);
+  out->log2T = out->T == 16 ? 4 : out->T == 32 ? 5 : 6;
   out->H = uint32_t(g->kv_heads);
   out->D = uint32_t(g->head_dim);
   out->blocks = uint32_t(g->blocks);
@@ -892,6 +1017,8 @@ int attend_args(const xfer_cache_shape* shape, const xfer_attend* q, const char*
   if (q->heads < 1 || q->heads > 16 * kMaxHeads || q->heads % shape->kv_heads)
     return fail(XFER_ERR_INVALID_ARG,
                 std::string(who) + ": heads must be a multiple of kv_heads, at most 16384");
+  if (int64_t(q->rows) * q->heads > 0x7FFFFFFFll)
+    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": rows * heads must stay below 2^31");
   if (q->dtype != XFER_BF16 && q->dtype != XFER_FP16)
     return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": dtype must be BF16 or FP16");
   if (!(q->scale > 0.0f) || !(q->scale <= 3.402823466e38f))
@@ -954,15 +1081,15 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
                 "16-byte aligned");
   a.part = static_cast<float*>(q->workspace);
   a.stats = need ? a.part + attend_part_bytes(a.s, *q, p) / sizeof(float) : nullptr;
-  const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr)
-                                                : pick_attend<fp16_t>(a.s.D, p.nr);
+  const bool once = p.tiles == 1;  // no other workgroup reads the same tokens
+  const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr, once)
+                                                : pick_attend<fp16_t>(a.s.D, p.nr, once);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles, p.nsplit),
                         kAttendWaves * 64, s);
   if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
   if (p.nsplit > 1) {
-    const int64_t waves = int64_t(q->rows) * q->heads, per = kJoinThreads / 64;
-    e = launch(k.join, a, dim3(uint32_t((waves + per - 1) / per)), kJoinThreads, s);
+    e = launch(k.join, a, dim3(uint32_t(q->rows), uint32_t(q->heads)), kJoinThreads, s);
     if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
   }
   return XFER_OK;

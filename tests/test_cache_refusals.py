@@ -57,6 +57,9 @@ def _attend(**kw):
 @pytest.mark.parametrize("kw", [dict(batch=-1), dict(rows=-1), dict(table_width=-1),
                                 dict(table_stride=3), dict(heads=0), dict(heads=3),
                                 dict(heads=1 << 17), dict(dtype=2), dict(dtype=-1),
+                                dict(rows=1 << 29, heads=4), dict(workspace_bytes=0, table_width=1 << 20, table_stride=1 << 20),
+                                dict(workspace=None, table_width=1 << 20, table_stride=1 << 20),
+                                dict(workspace=P + 8, table_width=1 << 20, table_stride=1 << 20),
                                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
                                 dict(scale=float("nan")), dict(max_query=-1), dict(max_length=-1),
                                 dict(query=None), dict(out=None), dict(table=None),
