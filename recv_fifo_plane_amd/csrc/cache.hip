@@ -308,6 +308,19 @@ __global__ void __launch_bounds__(kStoreThreads) store_kernel(StoreArgs A) {
 }
 
 // ------------------------------------------------------------------ attend
+// A tile of rows whose tokens several workgroups share, from w on to `last`.
+struct Begun {
+  int32_t request;  // -1: there is none
+  uint32_t tile, last, pad;
+};
+
+// The same value in every lane, known to the compiler as such.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 |
+         uniform(static_cast<uint32_t>(v));
+}
+
 struct AttendArgs {
   const uint8_t* cache;
   const void* query;
@@ -316,13 +329,14 @@ struct AttendArgs {
   const int32_t* table;
   const int32_t* lengths;
   const int32_t* starts;
-  float* part;   // [rows * heads][nsplit][D] unnormalised sums of the splits
-  float* stats;  // [rows * heads][nsplit][2] their maxima and sums of weights
+  // A launch whose workgroups share the tokens out evenly (flat > 0):
+  Begun* begun;     // [flat] the tile that a workgroup begins and does not finish
+  float* part;      // [workgroups][2][tile rows][D] sums of weighted values of begun tiles
+  float* stats;     // [workgroups][2][tile rows][2] their maxima and sums of weights
   int64_t query_row, query_head, out_row, out_head, table_stride;
   int32_t batch, rows, heads, width;
   uint32_t group;         // query heads of one key/value head
-  uint32_t nsplit;        // splits of the tokens
-  uint32_t split_chunks;  // chunks of a split
+  uint32_t flat;          // workgroups of one key/value head, 0: one per tile of rows
   float scale2;           // scale * log2(e): weights are powers of two
   Shape s;
 };
@@ -379,6 +393,12 @@ struct RowTile {
   uint32_t rows;  // rows times group
 };
 
+// Rows of request b that there are (a start below 0 has none).
+__device__ __forceinline__ uint32_t rows_of(const AttendArgs& A, uint32_t b) {
+  const int64_t start = A.starts[b], end = min<int64_t>(A.starts[b + 1], A.rows);
+  return start < 0 || end <= start ? 0u : static_cast<uint32_t>(end - start) * A.group;
+}
+
 __device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uint32_t first,
                                             uint32_t tile_rows) {
   RowTile r;
@@ -386,7 +406,7 @@ __device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uin
   const int64_t queries = static_cast<int64_t>(A.starts[b + 1]) - r.start, length = A.lengths[b];
   const int64_t held = min<int64_t>(length, static_cast<int64_t>(A.width) * A.s.T);
   r.ahead = length - queries;
-  r.rows = static_cast<uint32_t>(max<int64_t>(0, min<int64_t>(queries, A.rows)) * A.group);
+  r.rows = rows_of(A, b);
   const uint32_t last = min(r.rows, first + tile_rows);
   r.seen = 0;
   if (last > first)
@@ -397,10 +417,18 @@ __device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uin
   return r;
 }
 
-// Splits that the tokens of a tile take (at least one: it writes the rows).
-__device__ __forceinline__ uint32_t splits_of(const AttendArgs& A, int32_t seen) {
-  const uint32_t chunks = (static_cast<uint32_t>(seen) + kChunk - 1) / kChunk;
-  return max(1u, min((chunks + A.split_chunks - 1) / A.split_chunks, A.nsplit));
+// Request b's tiles of rows and, for each of them, units of work: chunks of
+// its tokens (one at least, so that every row is written).  A tile that sees
+// fewer tokens has units that hold nothing.
+struct Units {
+  uint32_t tiles, chunks;
+  __device__ uint64_t all() const { return static_cast<uint64_t>(tiles) * chunks; }
+};
+
+__device__ __forceinline__ Units units_of(const AttendArgs& A, uint32_t b, uint32_t tile_rows) {
+  const int64_t held = min<int64_t>(A.lengths[b], static_cast<int64_t>(A.width) * A.s.T);
+  const uint32_t chunks = (static_cast<uint32_t>(max<int64_t>(1, held)) + kChunk - 1) / kChunk;
+  return Units{(rows_of(A, b) + tile_rows - 1) / tile_rows, chunks};
 }
 
 // A lane's blocks in a chunk: as the holder of scores and values of tokens
@@ -430,17 +458,34 @@ __device__ __forceinline__ uint32_t key_dim(uint32_t k, uint32_t g) {
     return 32 * k + 8 * g;
 }
 
-// Workgroups a CU is to hold: bounds the registers of a lane.
-constexpr int attend_resident(int d, int nr) {
-  return nr == 1 ? (d <= 64 ? 3 : d <= 128 ? 2 : 1) : (d <= 64 ? 2 : 1);
-}
-
 template <bool ONCE, typename V>
 __device__ __forceinline__ V fetch(const uint8_t* p) {
   if constexpr (ONCE)
     return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
   else
     return *reinterpret_cast<const V*>(p);
+}
+
+// A chunk's value codes and the scales of the lane's block.
+template <int D, bool ONCE>
+struct Values {
+  u32x4 w[D / 16];
+  float key_scale, value_scale;
+  __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
+                                       uint32_t g, uint32_t n) {
+    const uint32_t block = max(at.mine, 0), T = A.s.T;
+    const uint8_t* p = A.cache + A.s.value_at(block, h) + n * T + ((t0 + 16 * g) & (T - 1));
+    const float* s = reinterpret_cast<const float*>(A.cache + A.s.scales_at(block, h));
+    key_scale = s[0];
+    value_scale = s[1];
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) w[e] = fetch<ONCE, u32x4>(p + 16 * e * T);
+  }
+};
+
+// Workgroups a CU is to hold: bounds the registers of a lane.
+constexpr int attend_resident(int d, int nr) {
+  return nr == 2 ? (d <= 96 ? 2 : 1) : d == 64 ? 3 : d <= 128 ? 2 : 1;
 }
 
 template <int D, bool ONCE>
@@ -504,8 +549,7 @@ template <bool MASK, bool TWO, int DT, int NR>
 __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f32x4 (&acc)[NR][DT],
                                       float (&m)[NR], float (&l)[NR], const u32x4 (&vc)[DT],
                                       const int32_t (&limit)[NR], float mul, float vs,
-                                      int32_t seen_all, int32_t tg, int32_t bg,
-                                      const int32_t* table, uint32_t h, int32_t t0, uint32_t g) {
+                                      int32_t seen_all, int32_t tg, int32_t bg, uint32_t& nans) {
   bf16x8 p[NR][2], p2[NR][2];
 #pragma unroll
   for (int x = 0; x < NR; ++x) {
@@ -563,14 +607,12 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
         v[w] &= mask[w];
         nan[w] = (((v[w] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
       }
-      if (__ballot((nan[0] | nan[1] | nan[2] | nan[3]) != 0) != 0) {
-        // A NaN among the others reaches the rows that see its token and no
-        // other: it is taken out here and looked for again in memory.
+      // A NaN among the others reaches the rows that see its token and no
+      // other: it is taken out here and looked for again in memory at the end.
 #pragma unroll
-        for (int w = 0; w < 4; ++w) v[w] &= ~(nan[w] * 0xFFu);
-#pragma unroll
-        for (int x = 0; x < NR; ++x)
-          acc[x][e] += seen_nans(A, table, h, t0, min(t0 + kChunk - 1, limit[x]), 16 * e + 4 * g);
+      for (int w = 0; w < 4; ++w) {
+        nans |= nan[w];
+        v[w] &= ~(nan[w] * 0xFFu);
       }
     }
     bf16x8 a, z;
@@ -613,51 +655,80 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // below the output's own rounding for bfloat16 queries.  For float16 it would
 // be above, so there a weight goes in two parts, the rounded one and the
 // rounded rest (off by 2^-16), at one more product each.
+template <int D, int NR>
+struct AttendShared {
+  u32x4 q[NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
+  float acc[kAttendWaves][16][D + 4];
+  float m[kAttendWaves][NR * 16], l[kAttendWaves][NR * 16];
+};
+
+// The rows first .. first + 16 NR - 1 of request b and key/value head h over
+// the chunks c0 .. c1 - 1, by a workgroup.  part null: these are all the
+// tokens, and the rows are written; else their sums go to part and stats.
 template <typename E, int D, int NR, bool ONCE>
-__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
+__device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D, NR>& sh, uint32_t b,
+                                            uint32_t h, uint32_t first, uint32_t c0, uint32_t c1,
+                                            float* part, float* stats) {
   typedef typename Vec8<E>::type E8;
   constexpr int KL = D / 32;  // steps of 32 dims
   constexpr int DT = D / 16;  // tiles of dims
   constexpr bool kTwo = __is_same(E, fp16_t);  // weights in two parts
-  constexpr int kPad = D + 4;
-  __shared__ float s_acc[kAttendWaves][16][kPad];
-  __shared__ float s_m[kAttendWaves][NR * 16], s_l[kAttendWaves][NR * 16];
-  const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H, sp = blockIdx.z;
   const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
-  const uint32_t T = A.s.T;
   const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
-  for (uint32_t first = blockIdx.y * NR * 16;; first += gridDim.y * NR * 16) {
+  {
     const RowTile rt = row_tile(A, b, first, NR * 16);
-    if (first >= rt.rows) return;
-    const uint32_t used = splits_of(A, rt.seen);
-    if (sp >= used) continue;
-    const uint32_t c0 = sp * A.split_chunks;
-    uint32_t c1 = (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk;
-    if (sp + 1 < used) c1 = min(c1, c0 + A.split_chunks);
+    c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
 
-    // Queries: lane (g, n) holds row n's dims in the order of its key loads.
-    E8 q[NR][KL];
-    int32_t limit[NR];       // last token that the row sees
+    // The first chunk's table entries, then its keys and values, are asked for
+    // before anything is waited for: each is a trip to memory.
+    const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen));
+    uint32_t c = c0 + wave, nans = 0;
+    Keys<D, ONCE> keys;
+    Values<D, ONCE> vals;
+    Place at, next;
+    constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
+    if (c < c1) {
+      at.look(A, table, c * kChunk, seen_all, g, n);
+      next.look(A, table, c * kChunk + kNext, seen_all, g, n);
+    }
+
+    // Queries: lane (g, n) takes row n's dims in the order of its key loads.
+    // They wait in shared memory, the same for every wave, which frees the
+    // registers that decide how many waves a CU holds.
+    constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
+    int32_t limit[NR];        // last token that the row sees
     int32_t least = rt.seen;  // the first of them
+    u32x4 q[NR][QL];
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const uint32_t i = first + x * 16 + n;
       const int64_t j = i / A.group, row = rt.start + j;
-      const bool there = i < rt.rows && row >= 0 && row < A.rows;
+      const bool there = i < rt.rows;
       limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
       const E* p = static_cast<const E*>(A.query) + row * A.query_row +
                    static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
 #pragma unroll
-      for (int k = 0; k < KL; ++k) {
-        E8 v = {};
-        if (there) __builtin_memcpy(&v, p + key_dim<D>(k, g), 16);
-        q[x][k] = v;
+      for (int k = 0; k < QL; ++k) {
+        q[x][k] = u32x4{0u, 0u, 0u, 0u};
+        const uint32_t step = wave + k * kAttendWaves;
+        if (there && step < KL) __builtin_memcpy(&q[x][k], p + key_dim<D>(step, g), 16);
       }
       least = min(least, limit[x]);
     }
+    if (c < c1) {
+      at.settle(A, c * kChunk, seen_all, g);
+      keys.load(A, at, c * kChunk, h, g, n);
+      vals.load(A, at, c * kChunk, h, g, n);
+    }
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int k = 0; k < QL; ++k)
+        if (wave + k * kAttendWaves < KL) sh.q[x][wave + k * kAttendWaves][lane] = q[x][k];
     for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
     least = __builtin_amdgcn_readfirstlane(least);
+    __syncthreads();
 
     float m[NR], l[NR];
     f32x4 acc[NR][DT];
@@ -669,59 +740,55 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
       for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // A chunk's keys are loaded while the chunk before is still at its
-    // weights and values, and its table entries one step earlier.
-    const uint32_t seen_all = __builtin_amdgcn_readfirstlane(rt.seen);
-    Keys<D, ONCE> keys;
-    Place at, next;
-    if (c0 + wave < c1) {
-      const uint32_t t0 = (c0 + wave) * kChunk;
-      at.look(A, table, t0, seen_all, g, n);
-      at.settle(A, t0, seen_all, g);
-      keys.load(A, at, t0, h, g, n);
-    }
-    uint32_t c = c0 + wave;
+    // A chunk's keys are loaded while the chunk before is still at its weights
+    // and values, its values as soon as those are done.  Loads return in the
+    // order they were asked for, so its table entries come a step earlier yet,
+    // ahead of the values of the chunk before: waiting for them waits for no
+    // codes.  The last step loads too (the last block again, near at hand): a
+    // branch around the loads would make every wait after it one for all of
+    // them.
     auto step = [&](auto masked) {
       const int32_t t0 = static_cast<int32_t>(c * kChunk);
-      const uint32_t tg = t0 + 16 * g, ahead = t0 + kAttendWaves * kChunk;
-      next.look(A, table, ahead, seen_all, g, n);
+      const uint32_t tg = t0 + 16 * g, ahead = t0 + kNext;
       const int32_t bg = at.mine;
-      const uint8_t* vp = A.cache + A.s.value_at(max(bg, 0), h) + n * T + (tg & (T - 1));
-      const float* sc = reinterpret_cast<const float*>(A.cache + A.s.scales_at(max(bg, 0), h));
-      float ks = sc[0], vs = sc[1];
-      u32x4 vc[DT];
-#pragma unroll
-      for (int e = 0; e < DT; ++e) vc[e] = fetch<ONCE, u32x4>(vp + 16 * e * T);
-      __builtin_amdgcn_sched_barrier(0);
-
       f32x4 s[NR][4];
 #pragma unroll
       for (int x = 0; x < NR; ++x)
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int k = 0; k < KL; ++k) {
+        E8 b8[NR];
 #pragma unroll
-        for (int k = 0; k < KL; ++k) {
+        for (int x = 0; x < NR; ++x) b8[x] = __builtin_bit_cast(E8, sh.q[x][k][lane]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
           E8 a;
           widen(keys.lo(t, k), keys.hi(t, k), 1.0f, a);
 #pragma unroll
-          for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, q[x][k], s[x][t]);
+          for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[x], s[x][t]);
         }
+      }
       __builtin_amdgcn_sched_barrier(0);
       next.settle(A, ahead, seen_all, g);
-      if (c + kAttendWaves < c1) keys.load(A, next, ahead, h, g, n);
+      keys.load(A, next, ahead, h, g, n);
       __builtin_amdgcn_sched_barrier(0);
-      if (bg < 0) ks = vs = 1.0f;  // (of a block that is not the request's: anything)
-      weigh<decltype(masked)::value, kTwo, DT, NR>(A, s, acc, m, l, vc, limit, ks * A.scale2, vs,
-                                                   seen_all, tg, bg, table, h, t0, g);
+      // (the scales of a block that is not the request's: anything)
+      const float ks = bg < 0 ? 1.0f : vals.key_scale, vs = bg < 0 ? 1.0f : vals.value_scale;
+      weigh<decltype(masked)::value, kTwo, DT, NR>(A, s, acc, m, l, vals.w, limit, ks * A.scale2, vs,
+                                                   seen_all, tg, bg, nans);
+      __builtin_amdgcn_sched_barrier(0);
       at = next;
+      next.look(A, table, ahead + kNext, seen_all, g, n);
+      vals.load(A, at, ahead, h, g, n);
       c += kAttendWaves;
     };
     // Chunks that every row sees whole, up to the first that is not; then the rest.
     const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
     while (c < whole && __ballot(at.mine < 0) == 0) step(std::false_type());
+    const uint32_t rest = c;
     while (c < c1) step(std::true_type());
+    const bool any_nan = __ballot(nans != 0) != 0;
 
     // Join the waves.
 #pragma unroll
@@ -729,36 +796,45 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
       l[x] += __shfl_xor(l[x], 16);
       l[x] += __shfl_xor(l[x], 32);
       if (g == 0) {
-        s_m[wave][x * 16 + n] = m[x];
-        s_l[wave][x * 16 + n] = l[x];
+        sh.m[wave][x * 16 + n] = m[x];
+        sh.l[wave][x * 16 + n] = l[x];
       }
     }
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      float top = s_m[0][x * 16 + n];
-      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, s_m[w][x * 16 + n]);
+      float top = sh.m[0][x * 16 + n];
+      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
       const float base = top == -INFINITY ? 0.0f : top;
       const float f = __builtin_amdgcn_exp2f(m[x] - base);
 #pragma unroll
       for (int e = 0; e < DT; ++e)
-        *reinterpret_cast<f32x4*>(&s_acc[wave][n][16 * e + 4 * g]) = acc[x][e] * f;
+        *reinterpret_cast<f32x4*>(&sh.acc[wave][n][16 * e + 4 * g]) = acc[x][e] * f;
+      if (any_nan) {
+#pragma clang loop unroll(disable)
+        for (uint32_t i = 0; i < DT * ((c1 - rest + kAttendWaves - 1) / kAttendWaves); ++i) {
+          const uint32_t d = 16 * (i % DT) + 4 * g;
+          const int32_t t0 = (rest + i / DT * kAttendWaves) * kChunk;
+          f32x4* o = reinterpret_cast<f32x4*>(&sh.acc[wave][n][d]);
+          *o += seen_nans(A, table, h, t0, min(t0 + kChunk - 1, limit[x]), d);
+        }
+      }
       __syncthreads();
       for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
         const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + x * 16 + r;
         const int64_t row = rt.start + ri / A.group;
-        if (ri >= rt.rows || row < 0 || row >= A.rows) continue;
-        float top = s_m[0][x * 16 + r], sum = 0.0f;
-        for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, s_m[w][x * 16 + r]);
+        if (ri >= rt.rows) continue;
+        float top = sh.m[0][x * 16 + r], sum = 0.0f;
+        for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + r]);
         const float base = top == -INFINITY ? 0.0f : top;
         f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int w = 0; w < kAttendWaves; ++w) {
-          sum += s_l[w][x * 16 + r] * __builtin_amdgcn_exp2f(s_m[w][x * 16 + r] - base);
-          o += *reinterpret_cast<const f32x4*>(&s_acc[w][r][d]);
+          sum += sh.l[w][x * 16 + r] * __builtin_amdgcn_exp2f(sh.m[w][x * 16 + r] - base);
+          o += *reinterpret_cast<const f32x4*>(&sh.acc[w][r][d]);
         }
         const uint32_t head = h * A.group + ri % A.group;
         const int64_t at = row * A.heads + head;
-        if (used == 1) {
+        if (part == nullptr) {
           const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
           E v[4];
           for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
@@ -766,10 +842,10 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
           if (d == 0 && A.lse)
             A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
         } else {
-          *reinterpret_cast<f32x4*>(A.part + (at * A.nsplit + sp) * D + d) = o;
+          *reinterpret_cast<f32x4*>(part + (x * 16 + r) * D + d) = o;
           if (d == 0) {
-            A.stats[(at * A.nsplit + sp) * 2] = top;
-            A.stats[(at * A.nsplit + sp) * 2 + 1] = sum;
+            stats[(x * 16 + r) * 2] = top;
+            stats[(x * 16 + r) * 2 + 1] = sum;
           }
         }
       }
@@ -778,75 +854,161 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
   }
 }
 
+// One workgroup per tile of rows and key/value head.
+template <typename E, int D, int NR, bool ONCE>
+__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
+  __shared__ AttendShared<D, NR> sh;
+  const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H;
+  for (uint32_t y = blockIdx.y;; y += gridDim.y) {
+    if (y >= units_of(A, b, NR * 16).tiles) return;
+    attend_rows<E, D, NR, ONCE>(A, sh, b, h, y * NR * 16, 0, ~0u, nullptr, nullptr);
+  }
+}
+
+// The chunks of all requests and tiles in one line, cut into equal shares for
+// as many workgroups per key/value head as the GPU holds: requests of very
+// different lengths, or few long ones, keep every CU busy to the end.  A
+// workgroup writes the tiles that lie whole in its share and leaves the sums
+// of at most two others, the first and the last, to join_kernel.  Every
+// workgroup sums up the requests' units for itself.
+template <typename E, int D, int NR, bool ONCE>
+__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_flat_kernel(AttendArgs A) {
+  constexpr uint32_t kThreads = kAttendWaves * 64, kRows = NR * 16;
+  __shared__ AttendShared<D, NR> sh;
+  __shared__ uint64_t s_pre[kThreads], s_wave[kAttendWaves];
+  const uint32_t h = blockIdx.x % A.s.H, w = blockIdx.x / A.s.H, tid = threadIdx.x;
+  const uint32_t batch = A.batch, seg = (batch + kThreads - 1) / kThreads;
+  const uint32_t b0 = min(batch, tid * seg), b1 = min(batch, b0 + seg);
+  uint64_t sum = 0;
+  for (uint32_t b = b0; b < b1; ++b) sum += units_of(A, b, kRows).all();
+  uint64_t run = sum;  // inclusive over the wave's lanes
+  for (uint32_t d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up(static_cast<unsigned long long>(run), d);
+    if ((tid & 63u) >= d) run += o;
+  }
+  if ((tid & 63u) == 63u) s_wave[tid >> 6] = run;
+  __syncthreads();
+  uint64_t pre = run - sum, all = 0;
+  for (uint32_t k = 0; k < kAttendWaves; ++k) {
+    if (k < (tid >> 6)) pre += s_wave[k];
+    all += s_wave[k];
+  }
+  s_pre[tid] = pre;
+  __syncthreads();
+  all = uniform(all);
+  const uint64_t flat = min<uint64_t>(A.flat, all);  // (so every share holds a unit)
+  if (h == 0 && tid == 0) A.begun[w].request = -1;
+  if (w >= flat) return;
+  const uint64_t lo = all * w / flat, hi = all * (w + 1) / flat;
+  uint32_t first = 0, last = kThreads;  // the last segment that begins at or before lo
+  while (last - first > 1) {
+    const uint32_t mid = (first + last) / 2;
+    if (s_pre[mid] <= lo)
+      first = mid;
+    else
+      last = mid;
+  }
+  uint32_t b = uniform(first) * seg;
+  uint64_t u = lo, at = uniform(s_pre[first]);  // the unit to do, the request's first
+  Units q = units_of(A, b, kRows);
+  for (;;) {
+    while (at + q.all() <= u && b + 1 < batch) {  // (u < all: a request with units follows)
+      at = uniform(at + q.all());
+      q = units_of(A, ++b, kRows);
+    }
+    q.chunks = uniform(q.chunks);
+    const uint32_t y = uniform(static_cast<uint32_t>((u - at) / q.chunks));
+    const uint64_t begin = at + static_cast<uint64_t>(y) * q.chunks, end = begin + q.chunks;
+    const uint64_t to = min(hi, end);
+    const bool whole = begin >= lo && end <= hi;
+    if (end > hi && begin >= lo && h == 0 && tid == 0)
+      A.begun[w] = Begun{static_cast<int32_t>(b), y, static_cast<uint32_t>((end * flat - 1) / all), 0};
+    const uint32_t slot = (blockIdx.x * 2 + (begin >= lo ? 1 : 0)) * kRows;
+    attend_rows<E, D, NR, ONCE>(A, sh, b, h, y * kRows, static_cast<uint32_t>(u - begin),
+                                static_cast<uint32_t>(to - begin),
+                                whole ? nullptr : A.part + static_cast<uint64_t>(slot) * D,
+                                A.stats + slot * 2);
+    u = to;
+    if (u == hi) return;
+  }
+}
+
 constexpr int kJoinThreads = 256;
 
-// Joins the splits of the rows that took more than one: a workgroup per row
-// and head, D / 4 threads wide, whose groups of threads take the splits in
-// turn and are then added in order, so the result does not depend on when the
-// splits ran.
+// Joins the sums of the tiles that several workgroups shared: workgroup (w, h)
+// that of the tile which share w begins and later ones go on with, D / 4
+// threads for a row, the shares in order, so the result does not depend on
+// when they were done.
 template <typename E, int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
-  constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide;
-  __shared__ f32x4 s_o[kGroups][kWide];
-  __shared__ float s_sum[kGroups];
-  const int64_t row = blockIdx.x;
-  const uint32_t head = blockIdx.y, tid = threadIdx.x, grp = tid / kWide, d = tid % kWide;
-  int lo = 0, hi = A.batch;  // the last request that starts at or before the row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (A.starts[mid] <= row)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int64_t j = row - A.starts[lo];
-  if (j < 0 || row >= A.starts[lo + 1]) return;
-  const uint32_t i = static_cast<uint32_t>(j) * A.group + head % A.group;
-  const RowTile rt = row_tile(A, lo, i / (NR * 16) * (NR * 16), NR * 16);
-  const uint32_t used = splits_of(A, rt.seen);
-  if (used == 1) return;
-  const int64_t at = row * A.heads + head;
-  const float* st = A.stats + at * A.nsplit * 2;
-  float top = -INFINITY;
-  for (uint32_t s = tid & 63u; s < used; s += 64) top = fmaxf(top, st[2 * s]);
-  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const float base = top == -INFINITY ? 0.0f : top;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  float sum = 0.0f;
-  if (grp < kGroups) {
-    for (uint32_t s = grp; s < used; s += kGroups) {
-      const float f = __builtin_amdgcn_exp2f(st[2 * s] - base);
-      sum += st[2 * s + 1] * f;
-      o += *reinterpret_cast<const f32x4*>(A.part + (at * A.nsplit + s) * D + 4 * d) * f;
+  constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide, kRows = NR * 16;
+  const uint32_t w = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % kWide;
+  const Begun t = A.begun[w];
+  if (t.request < 0 || tid >= kGroups * kWide) return;
+  const uint32_t rows = rows_of(A, t.request);
+  const int64_t start = A.starts[t.request];
+  {
+    const uint32_t r = blockIdx.z * kGroups + tid / kWide, i = t.tile * kRows + r;
+    if (r >= kRows || i >= rows) return;
+    // the first share's second place, the later ones' first
+    const uint64_t p0 = (static_cast<uint64_t>(w * A.s.H + h) * 2 + 1) * kRows + r;
+    const uint64_t step = 2ull * A.s.H * kRows, p1 = p0 - kRows + step;
+    float top = -INFINITY, sum = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr uint32_t kTake = 8;  // shares taken together: their loads are in flight at once
+    for (uint32_t k0 = 0; k0 <= t.last - w; k0 += kTake) {
+      float m[kTake], l[kTake];
+      f32x4 v[kTake];
+#pragma unroll
+      for (uint32_t k = 0; k < kTake; ++k) {
+        const bool there = k0 + k <= t.last - w;
+        const uint64_t p = k0 + k == 0 || !there ? p0 : p1 + (k0 + k - 1) * step;
+        m[k] = there ? A.stats[p * 2] : -INFINITY;
+        l[k] = there ? A.stats[p * 2 + 1] : 0.0f;
+        v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (there) v[k] = *reinterpret_cast<const f32x4*>(A.part + p * D + 4 * d);
+      }
+      const float was = top;
+#pragma unroll
+      for (uint32_t k = 0; k < kTake; ++k) top = fmaxf(top, m[k]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      const float keep = __builtin_amdgcn_exp2f(was - base);
+      sum *= keep;
+      o *= keep;
+#pragma unroll
+      for (uint32_t k = 0; k < kTake; ++k) {
+        const float f = __builtin_amdgcn_exp2f(m[k] - base);
+        sum += l[k] * f;
+        o += v[k] * f;
+      }
     }
-    s_o[grp][d] = o;
-    if (d == 0) s_sum[grp] = sum;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    const int64_t row = start + i / A.group;
+    const uint32_t head = h * A.group + i % A.group;
+    E v[4];
+    for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+    __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
+    if (d == 0 && A.lse)
+      A.lse[row * A.heads + head] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
   }
-  __syncthreads();
-  if (tid >= kWide) return;
-  for (uint32_t k = 1; k < kGroups; ++k) {
-    o += s_o[k][d];
-    sum += s_sum[k];
-  }
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  E v[4];
-  for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
-  __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
-  if (d == 0 && A.lse) A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 using AttendFn = void (*)(AttendArgs);
 struct AttendKernels {
-  AttendFn attend, join;
+  AttendFn attend, flat, join;
 };
+
+template <typename E, int D, int NR, bool ONCE>
+AttendKernels attend_of() {
+  return {attend_kernel<E, D, NR, ONCE>, attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
+}
 
 template <typename E, int D>
 AttendKernels pick_attend_rows(int nr, bool once) {
   if constexpr (D <= 128) {
-    if (nr == 2) return {attend_kernel<E, D, 2, false>, join_kernel<E, D, 2>};
+    if (nr == 2) return attend_of<E, D, 2, false>();
   }
-  if (once) return {attend_kernel<E, D, 1, true>, join_kernel<E, D, 1>};
-  return {attend_kernel<E, D, 1, false>, join_kernel<E, D, 1>};
+  return once ? attend_of<E, D, 1, true>() : attend_of<E, D, 1, false>();
 }
 
 template <typename E>
@@ -860,10 +1022,11 @@ AttendKernels pick_attend(uint32_t d, int nr, bool once) {
   }
 }
 
-// The launch of a call: row tiles of a workgroup, and splits.
+// The launch of a call: row tiles of a workgroup, and how the work is shared.
 struct AttendPlan {
   int nr;
-  uint32_t tiles, nsplit, split_chunks;
+  uint32_t tiles;  // of a request
+  uint32_t flat;   // AttendArgs::flat
 };
 
 AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
@@ -877,23 +1040,34 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
-  // Splits until the launch has about 1024 workgroups, each of at least four chunks a wave.
+  // Sharing costs a second launch and about 8 us; it pays where few workgroups
+  // would be left with long requests.  Measured at 8 key/value heads of 128,
+  // group 4, one workgroup per tile against shared (us): 1 request of 1024
+  // tokens 14 / 16, of 2048 21 / 17, of 16384 120 / 23; 32 requests of 2048
+  // 31 / 38, of 4096 52 / 60, of 410 .. 4096 42 / 38, of 8192 95 / 104, of 820 ..
+  // 8192 75 / 56; 128 requests of 410 .. 4096 106 / 106.
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
-  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, wgs));
-  const int64_t least = 4 * kAttendWaves;
-  p.split_chunks = uint32_t(std::max<int64_t>(least, (chunks + want - 1) / want));
-  p.split_chunks = uint32_t(std::max<int64_t>(p.split_chunks, (chunks + 255) / 256));
-  p.nsplit = uint32_t((chunks + p.split_chunks - 1) / p.split_chunks);
+  p.flat = 0;
+  if (chunks >= (wgs <= 128 ? 24 : 64)) {
+    // As many workgroups as are resident at once on 256 CUs, eight chunks each at least.
+    const int64_t resident = 256 * attend_resident(int(s.D), p.nr);
+    p.flat = uint32_t(std::max<int64_t>(
+        1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
+  }
   return p;
 }
 
-size_t attend_part_bytes(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
-  return p.nsplit == 1 ? 0 : size_t(q.rows) * size_t(q.heads) * p.nsplit * s.D * sizeof(float);
-}
-size_t attend_work_bytes(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
-  return p.nsplit == 1 ? 0
-                       : attend_part_bytes(s, q, p) +
-                             size_t(q.rows) * size_t(q.heads) * p.nsplit * 2 * sizeof(float);
+// The workspace: the begun tiles, their sums and the sums' statistics.
+struct AttendWork {
+  size_t begun, part, stats;
+  size_t all() const { return begun + part + stats; }
+};
+
+AttendWork attend_work(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
+  if (!p.flat) return AttendWork{0, 0, 0};
+  const size_t tiles = size_t(p.flat) * s.H * 2 * size_t(p.nr) * 16;
+  return AttendWork{size_t(p.flat) * sizeof(Begun), tiles * s.D * sizeof(float),
+                    tiles * 2 * sizeof(float)};
 }
 
 // ------------------------------------------------------------------ checks
@@ -1036,7 +1210,7 @@ extern "C" int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const 
   const int rc = attend_args(shape, q, "xfer_cache_attend_workspace", &s);
   if (rc) return rc;
   if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_cache_attend_workspace: NULL bytes");
-  *bytes = attend_work_bytes(s, *q, attend_plan(s, *q));
+  *bytes = attend_work(s, *q, attend_plan(s, *q)).all();
   return XFER_OK;
 }
 
@@ -1072,25 +1246,30 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
   a.group = uint32_t(q->heads) / a.s.H;
   a.scale2 = q->scale * 1.44269504088896341f;
   const AttendPlan p = attend_plan(a.s, *q);
-  a.nsplit = p.nsplit;
-  a.split_chunks = p.split_chunks;
-  const size_t need = attend_work_bytes(a.s, *q, p);
-  if (need && (!q->workspace || q->workspace_bytes < need || !aligned(q->workspace, 16)))
+  a.flat = p.flat;
+  const AttendWork work = attend_work(a.s, *q, p);
+  if (p.flat && (!q->workspace || q->workspace_bytes < work.all() || !aligned(q->workspace, 16)))
     return fail(XFER_ERR_INVALID_ARG,
                 "xfer_cache_attend: the workspace must hold xfer_cache_attend_workspace() bytes, "
                 "16-byte aligned");
-  a.part = static_cast<float*>(q->workspace);
-  a.stats = need ? a.part + attend_part_bytes(a.s, *q, p) / sizeof(float) : nullptr;
+  uint8_t* mem = static_cast<uint8_t*>(q->workspace);
+  a.begun = reinterpret_cast<Begun*>(mem);
+  a.part = reinterpret_cast<float*>(mem + work.begun);
+  a.stats = reinterpret_cast<float*>(mem + work.begun + work.part);
   const bool once = p.tiles == 1;  // no other workgroup reads the same tokens
   const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr, once)
                                                 : pick_attend<fp16_t>(a.s.D, p.nr, once);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles, p.nsplit),
-                        kAttendWaves * 64, s);
-  if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
-  if (p.nsplit > 1) {
-    e = launch(k.join, a, dim3(uint32_t(q->rows), uint32_t(q->heads)), kJoinThreads, s);
-    if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
+  hipError_t e;
+  if (!p.flat) {
+    e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles), kAttendWaves * 64, s);
+  } else {
+    e = launch(k.flat, a, dim3(p.flat * a.s.H), kAttendWaves * 64, s);
+    if (e == hipSuccess) {
+      const uint32_t rows = uint32_t(kJoinThreads) / (a.s.D / 4);  // of a join workgroup
+      e = launch(k.join, a, dim3(p.flat, a.s.H, (uint32_t(p.nr) * 16 + rows - 1) / rows), kJoinThreads, s);
+    }
   }
+  if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
   return XFER_OK;
 }
