@@ -26,6 +26,19 @@ BLOCK_TOKENS = (16, 32, 64)
 HEAD_DIMS = (64, 96, 128, 192, 256)
 
 
+_KINDS = {}  # torch dtypes of rows to xfer_dtype, filled at the first call
+_INT32 = None
+
+
+def _kinds():
+    global _INT32
+    if not _KINDS:
+        import torch
+        _KINDS.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        _INT32 = torch.int32
+    return _KINDS
+
+
 def _tensor(t, what, dtypes, ndim, device):
     """A GPU tensor of one of `dtypes` with `ndim` dimensions on `device` (None: any)."""
     if not hasattr(t, "data_ptr"):
@@ -42,36 +55,51 @@ def _tensor(t, what, dtypes, ndim, device):
 
 
 def _list(t, what, n, device):
-    """A contiguous int32 tensor of n entries (None: any number)."""
-    import torch
-    _tensor(t, what, (torch.int32,), 1, device)
-    if n is not None and t.shape[0] != n:
-        raise ValueError("%s: expected %d entries, got %d" % (what, n, t.shape[0]))
-    if t.shape[0] > 1 and t.stride(0) != 1:
+    """Address of a contiguous int32 tensor of n entries (None: any number)."""
+    _tensor(t, what, (_INT32,), 1, device)
+    have = t.shape[0]
+    if n is not None and have != n:
+        raise ValueError("%s: expected %d entries, got %d" % (what, n, have))
+    if have > 1 and t.stride(0) != 1:
         raise ValueError("%s: tensor is not contiguous" % what)
-    return t
+    return t.data_ptr()
 
 
 def _table(t, what, batch, device):
-    """A block table [batch, width]: any row stride of at least the width."""
-    import torch
-    _tensor(t, what, (torch.int32,), 2, device)
-    if t.shape[0] != batch:
-        raise ValueError("%s: expected %d rows, got %d" % (what, batch, t.shape[0]))
-    width = t.shape[1]
-    if (width > 1 and t.stride(1) != 1) or (batch > 1 and t.stride(0) < width):
+    """Address, row stride and width of a block table [batch, width]: any row
+    stride of at least the width."""
+    _tensor(t, what, (_INT32,), 2, device)
+    have, width = t.shape
+    if have != batch:
+        raise ValueError("%s: expected %d rows, got %d" % (what, batch, have))
+    stride = t.stride(0) if batch > 1 else width
+    if (width > 1 and t.stride(1) != 1) or stride < width:
         raise ValueError("%s: rows must be contiguous and not overlap" % what)
-    return t.stride(0) if batch > 1 else width, width
+    return t.data_ptr(), stride, width
+
+
+def _rows(t, what, dtypes, device, rows, heads, dim):
+    """Address and strides of rows [rows, heads, dim] with a contiguous last dimension."""
+    _tensor(t, what, dtypes, 3, device)
+    if t.shape != (rows, heads, dim):
+        raise ValueError("%s must have shape (%d, %d, %d), got %s"
+                         % (what, rows, heads, dim, tuple(t.shape)))
+    row, head, last = t.stride()
+    if last != 1:
+        raise ValueError("%s: the last dimension must be contiguous" % what)
+    return t.data_ptr(), row, head
 
 
 def _call(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
     import torch
     if device == torch.cuda.current_device():
-        X.check(fn(*args, X._stream_handle(stream)))
+        rc = fn(*args, X._stream_handle(stream))
     else:
         with torch.cuda.device(device):
-            X.check(fn(*args, X._stream_handle(stream)))
+            rc = fn(*args, X._stream_handle(stream))
+    if rc:
+        X.check(rc)
 
 
 def _keep(stream, *tensors):
@@ -87,6 +115,11 @@ def _keep(stream, *tensors):
             t.record_stream(stream)
 
 
+def _empty(like, shape, dtype):
+    import torch
+    return torch.empty(shape, dtype=getattr(torch, dtype), device=like.device)
+
+
 def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=None,
                 stream=None) -> BlockPlan:
     """Room for the next tokens of a batch, worked out on the GPU.
@@ -96,26 +129,25 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
     `free` in order.  All int32 tensors.  rows: length of the packed rows'
     outputs (the batch's added tokens, or more where it is padded).  out: a
     BlockPlan to write into (a captured graph's), else new tensors."""
-    import torch
-    _list(cached, "plan_blocks: cached", None, None)
+    _kinds()
+    at_cached = _list(cached, "plan_blocks: cached", None, None)
     dev, batch = cached.device.index, cached.shape[0]
-    _list(added, "plan_blocks: added", batch, dev)
-    stride, width = _table(table, "plan_blocks: table", batch, dev)
-    _list(free, "plan_blocks: free", None, dev)
+    at_added = _list(added, "plan_blocks: added", batch, dev)
+    at_table, stride, width = _table(table, "plan_blocks: table", batch, dev)
+    at_free = _list(free, "plan_blocks: free", None, dev)
     rows = int(rows)
     if rows < 0:
         raise ValueError("plan_blocks: rows must not be negative")
     sizes = (rows, rows, batch + 1, batch, 2)
     if out is None:
-        out = BlockPlan(*(torch.empty(n, dtype=torch.int32, device=cached.device) for n in sizes))
-        _keep(stream, *out)
-    else:
-        for t, n, w in zip(out, sizes, BlockPlan._fields):
-            _list(t, "plan_blocks: out." + w, n, dev)
-    _call(dev, stream, X.lib().xfer_cache_plan, cached.data_ptr(), added.data_ptr(), batch,
-          table.data_ptr(), stride, width, free.data_ptr(), free.shape[0], int(block_tokens),
-          out.slots.data_ptr(), out.positions.data_ptr(), rows, out.starts.data_ptr(),
-          out.lengths.data_ptr(), out.counts.data_ptr())
+        buf = cached.new_empty(sum(sizes))
+        _keep(stream, buf)
+        out = BlockPlan(*buf.split(sizes))
+    slots, positions, starts, lengths, counts = (
+        _list(t, "plan_blocks: out", n, dev) for t, n in zip(out, sizes))
+    _call(dev, stream, X.lib().xfer_cache_plan, at_cached, at_added, batch, at_table, stride, width,
+          at_free, free.shape[0], int(block_tokens), slots, positions, rows, starts, lengths,
+          counts)
     return out
 
 
@@ -144,6 +176,7 @@ class PagedCache:
             raise ValueError("PagedCache: buffer must be contiguous and 16-byte aligned")
         self.buffer = buffer
         self.device = buffer.device.index
+        self._ref, self._base = C.byref(self._shape), buffer.data_ptr()
 
     def _view(self, dtype, shape, strides, at):
         b = self.buffer.view(dtype)
@@ -173,22 +206,16 @@ class PagedCache:
     def store(self, key, value, slots, stream=None) -> None:
         """Stores rows of keys and values [rows, kv_heads, head_dim] (bfloat16,
         float16 or float32; any strides of rows and heads) into their slots."""
-        import torch
-        kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        kinds = _kinds()
         _tensor(key, "store: key", kinds, 3, self.device)
-        _tensor(value, "store: value", (key.dtype,), 3, self.device)
-        rows = key.shape[0]
-        for t, w in ((key, "key"), (value, "value")):
-            if tuple(t.shape) != (rows, self.kv_heads, self.head_dim):
-                raise ValueError("store: %s must have shape (%d, %d, %d), got %s"
-                                 % (w, rows, self.kv_heads, self.head_dim, tuple(t.shape)))
-            if t.stride(2) != 1:
-                raise ValueError("store: %s: the last dimension must be contiguous" % w)
-        _list(slots, "store: slots", rows, self.device)
-        _call(self.device, stream, X.lib().xfer_cache_store, C.byref(self._shape),
-              self.buffer.data_ptr(), key.data_ptr(), key.stride(0), key.stride(1),
-              value.data_ptr(), value.stride(0), value.stride(1), kinds[key.dtype],
-              slots.data_ptr(), rows)
+        rows, dtype = key.shape[0], key.dtype
+        k, k_row, k_head = _rows(key, "store: key", kinds, self.device, rows, self.kv_heads,
+                                 self.head_dim)
+        v, v_row, v_head = _rows(value, "store: value", (dtype,), self.device, rows, self.kv_heads,
+                                 self.head_dim)
+        at = _list(slots, "store: slots", rows, self.device)
+        _call(self.device, stream, X.lib().xfer_cache_store, self._ref, self._base, k, k_row, k_head,
+              v, v_row, v_head, kinds[dtype], at, rows)
 
     def attend(self, query, table, lengths, starts, scale=None, out=None, lse=False, max_query=0,
                max_length=0, stream=None):
@@ -201,50 +228,44 @@ class PagedCache:
         max_query, max_length: the batch's largest number of rows and of
         tokens, where known; they shape the launch only.  Rows of no request
         are left as they were (without `out`: undefined)."""
-        import torch
-        kinds = {torch.bfloat16: 0, torch.float16: 1}
+        kinds = _kinds()
         _tensor(query, "attend: query", kinds, 3, self.device)
         rows, heads, d = query.shape
-        if d != self.head_dim:
-            raise ValueError("attend: query has head_dim %d, the cache %d" % (d, self.head_dim))
-        if query.stride(2) != 1:
-            raise ValueError("attend: query: the last dimension must be contiguous")
-        _list(lengths, "attend: lengths", None, self.device)
+        dtype = query.dtype
+        if kinds[dtype] == 2:
+            raise TypeError("attend: query: unsupported dtype %s" % dtype)
+        q, q_row, q_head = _rows(query, "attend: query", kinds, self.device, rows, heads,
+                                 self.head_dim)
+        at_lengths = _list(lengths, "attend: lengths", None, self.device)
         batch = lengths.shape[0]
-        _list(starts, "attend: starts", batch + 1, self.device)
-        stride, width = _table(table, "attend: table", batch, self.device)
+        at_starts = _list(starts, "attend: starts", batch + 1, self.device)
+        at_table, stride, width = _table(table, "attend: table", batch, self.device)
         if out is None:
-            out = torch.empty(rows, heads, d, dtype=query.dtype, device=query.device)
+            out = query.new_empty((rows, heads, d))
             _keep(stream, out)
-        else:
-            _tensor(out, "attend: out", (query.dtype,), 3, self.device)
-            if out.shape != query.shape or out.stride(2) != 1:
-                raise ValueError("attend: out must have the query's shape and a contiguous last "
-                                 "dimension")
+        o, o_row, o_head = _rows(out, "attend: out", (dtype,), self.device, rows, heads, d)
         sums = None
         if lse is True:
-            sums = torch.empty(rows, heads, dtype=torch.float32, device=query.device)
+            sums = _empty(query, (rows, heads), "float32")
             _keep(stream, sums)
         elif lse is not False and lse is not None:
-            sums = _tensor(lse, "attend: lse", (torch.float32,), 2, self.device)
+            sums = _tensor(lse, "attend: lse", [t for t, k in kinds.items() if k == 2], 2, self.device)
             if tuple(sums.shape) != (rows, heads) or not sums.is_contiguous():
                 raise ValueError("attend: lse must be contiguous of shape (%d, %d)" % (rows, heads))
-        a = X.xfer_attend(query.data_ptr(), out.data_ptr(),
-                          None if sums is None else sums.data_ptr(), table.data_ptr(),
-                          lengths.data_ptr(), starts.data_ptr(), None, 0, query.stride(0),
-                          query.stride(1), out.stride(0), out.stride(1), stride, batch, rows,
-                          heads, width, kinds[query.dtype],
+        a = X.xfer_attend(q, o, None if sums is None else sums.data_ptr(), at_table, at_lengths,
+                          at_starts, None, 0, q_row, q_head, o_row, o_head, stride, batch, rows,
+                          heads, width, kinds[dtype],
                           1.0 / math.sqrt(d) if scale is None else float(scale), int(max_query),
                           int(max_length))
-        n = C.c_size_t()
-        L = X.lib()
-        X.check(L.xfer_cache_attend_workspace(C.byref(self._shape), C.byref(a), C.byref(n)))
+        n, ref, lib = C.c_size_t(), C.byref(a), X.lib()
+        rc = lib.xfer_cache_attend_workspace(self._ref, ref, C.byref(n))
+        if rc:
+            X.check(rc)
         if n.value:
-            work = torch.empty(n.value, dtype=torch.uint8, device=query.device)
+            work = _empty(query, (n.value,), "uint8")
             _keep(stream, work)
             a.workspace, a.workspace_bytes = work.data_ptr(), n.value
-        _call(self.device, stream, L.xfer_cache_attend, C.byref(self._shape),
-              self.buffer.data_ptr(), C.byref(a))
+        _call(self.device, stream, lib.xfer_cache_attend, self._ref, self._base, ref)
         return out if sums is None else (out, sums)
 
     def send(self, conn, dst, src_ids, dst_ids, stream=None) -> None:

@@ -215,11 +215,16 @@ struct StoreArgs {
   int64_t key_row, key_head, value_row, value_head;  // strides in elements
   const int32_t* slots;
   int32_t rows;
+  uint32_t tile, wg_heads;  // rows whose runs, and heads, a workgroup looks after
   Shape s;
 };
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16_t;
 typedef _Float16 fp16_t;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
 
 // Smallest power of two, 2^-118 at least, that brings amax (finite) to 448 =
 // 1.75 * 2^8 or below.  amax = (1 + m / 2^23) * 2^(x - 127) from its bits; a
@@ -251,59 +256,321 @@ __device__ __forceinline__ float value_of(uint8_t c) {
   return __builtin_amdgcn_cvt_f32_fp8(c, 0);
 }
 
-constexpr int kStoreThreads = 128;
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Element j of eight packed in words.
+template <typename E>
+__device__ __forceinline__ float element(const uint32_t* w, uint32_t j) {
+  if constexpr (sizeof(E) == 4) {
+    return __uint_as_float(w[j]);
+  } else {
+    const uint16_t b = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
+    return static_cast<float>(__builtin_bit_cast(E, b));
+  }
+}
+
+// Bits of the 16-bit types' infinity: the magnitudes' bits are ordered as they
+// are, those that are not finite last.
+template <typename E>
+constexpr uint32_t infinity_bits() {
+  return __is_same(E, bf16_t) ? 0x7F80u : 0x7C00u;
+}
+
+// Groups of four places that a wave holds at once.
+constexpr uint32_t store_groups(int d, int t) {
+  const uint32_t fit = d <= 64 ? 8 : d <= 128 ? 4 : 2, all = t / 4;
+  return fit < all ? fit : all;
+}
+
+constexpr int kStoreWaves = 4;
+
+__device__ __forceinline__ float wave_max(float x) {
+  for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
+  return x;
+}
+
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
+// The codes of elements 4q .. 4q + 3 of eight packed in words, divided by
+// scale (a power of two), the first lowest.  The conversion divides and rounds
+// to nearest even in one step.
+template <typename E>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t* w, uint32_t q, float scale) {
+  i16x2 r = {0, 0};
+  if constexpr (__is_same(E, bf16_t)) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[2 * q]), scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, w[2 * q + 1]), scale, true);
+  } else if constexpr (__is_same(E, fp16_t)) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(fp16x2, w[2 * q]), scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(fp16x2, w[2 * q + 1]), scale, true);
+  } else {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[4 * q]), __uint_as_float(w[4 * q + 1]), scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(w[4 * q + 2]), __uint_as_float(w[4 * q + 3]), scale, true);
+  }
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// NaN in the places of a word of codes whose elements are not finite.
+template <typename E>
+__device__ __forceinline__ uint32_t with_nans(uint32_t codes, const uint32_t* w, uint32_t q) {
+#pragma unroll
+  for (uint32_t j = 0; j < 4; ++j)
+    if (!(fabsf(element<E>(w, 4 * q + j)) <= 3.402823466e38f))
+      codes = (codes & ~(0xFFu << (8 * j))) | 0x7Fu << (8 * j);
+  return codes;
+}
+
+// Byte j of the four words, as word j.
+__device__ __forceinline__ void transpose(const uint32_t (&w)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
 
 // A run is the rows that fall into one block: consecutive slots that do not
-// pass its end.  The workgroup of a run's first row and one head finds the
-// largest magnitude of the run's keys (values), settles the block's scale,
-// rounds the earlier tokens' codes again if it grew and writes the run's.
-template <typename E>
-__global__ void __launch_bounds__(kStoreThreads) store_kernel(StoreArgs A) {
-  __shared__ float s_max[kStoreThreads / 64];
-  const int32_t n = blockIdx.x;
-  const uint32_t h = blockIdx.y, T = A.s.T, D = A.s.D, tid = threadIdx.x;
-  const int32_t slot = A.slots[n];
-  if (slot < 0 || static_cast<uint32_t>(slot) / T >= A.s.blocks) return;
-  const uint32_t block = static_cast<uint32_t>(slot) / T, off = static_cast<uint32_t>(slot) % T;
-  if (off > 0 && n > 0 && A.slots[n - 1] == slot - 1) return;
-  uint32_t cnt = 1;
-  while (n + static_cast<int32_t>(cnt) < A.rows && off + cnt < T &&
-         A.slots[n + cnt] == slot + static_cast<int32_t>(cnt))
-    ++cnt;
-  for (int side = 0; side < 2; ++side) {
-    const E* src = side ? static_cast<const E*>(A.value) + n * A.value_row + h * A.value_head
-                        : static_cast<const E*>(A.key) + n * A.key_row + h * A.key_head;
-    const int64_t row = side ? A.value_row : A.key_row;
-    uint8_t* codes = A.cache + (side ? A.s.value_at(block, h) : A.s.key_at(block, h));
-    float* held = reinterpret_cast<float*>(A.cache + A.s.scales_at(block, h)) + side;
-    const uint32_t st = side ? 1u : D, sd = side ? T : 1u;  // code strides of a token and a dim
-    float amax = 0.0f;
-    for (uint32_t i = tid; i < cnt * D; i += kStoreThreads)
-      amax = fmaxf(amax, finite_abs(static_cast<float>(src[(i / D) * row + i % D])));
-    for (int d = 1; d < 64; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
-    __syncthreads();
-    if ((tid & 63u) == 0) s_max[tid >> 6] = amax;
-    __syncthreads();
-    for (int w = 0; w < kStoreThreads / 64; ++w) amax = fmaxf(amax, s_max[w]);
-    float scale = scale_of(amax);
-    if (off > 0) {
-      const float was = *held;
-      if (scale > was) {
-        const float f = was * power_inverse(scale);
-        for (uint32_t i = tid; i < off * D; i += kStoreThreads) {
-          uint8_t* c = codes + (i / D) * st + (i % D) * sd;
-          *c = code_of(value_of(*c) * f);
-        }
-      } else {
-        scale = was;
-      }
+// pass its end, places off .. end - 1, from row n on.  The keys or the values of
+// one run and head are an item: its largest magnitude is found, the block's
+// scale settled, the earlier tokens' codes rounded again if the scale grew, and
+// the run's written.
+//
+// A lane holds four consecutive places of a block times eight dims (col): the
+// keys go out as eight bytes per place, the values, which the cache holds
+// transposed, as a word of four places per dim.  64 / (D / 8) groups of four
+// places fit a wave at once (TG): a pass.  WV waves take an item, each its share
+// of the block's passes, and exchange their magnitudes through shared memory
+// (every wave of the workgroup must then be in the same call).  With several
+// waves the rows of 16-bit types stay in registers between the two looks at
+// them; one wave loads them again, which its short runs bear.
+template <typename E, int D, int T, int WV>
+__device__ __forceinline__ void store_item(const StoreArgs& A, float* s_max, int32_t n, uint32_t block,
+                                           uint32_t off, uint32_t end, uint32_t h, uint32_t side) {
+  constexpr uint32_t W = D / 8;
+  constexpr uint32_t TG = store_groups(D, T), P = T / (4 * TG) / WV;
+  constexpr bool kKeep = P == 1 || (sizeof(E) == 2 && WV > 1);
+  constexpr uint32_t kSpan = 4 * TG;  // places of a pass
+  struct Row8 {
+    uint32_t w[2 * sizeof(E)];
+  };
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const uint32_t tg = lane % TG, col = lane / TG;
+  const bool active = col < W;
+  const uint32_t base = wave % WV * P * kSpan;  // the wave's first place
+  float* held = reinterpret_cast<float*>(A.cache + A.s.scales_at(block, h)) + side;
+  const int64_t row_stride = side ? A.value_row : A.key_row;
+  // (of place 0, which may lie before the rows: only places of the run are read)
+  const E* src = static_cast<const E*>(side ? A.value : A.key) +
+                 (static_cast<int64_t>(n) - off) * row_stride +
+                 static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * col;
+  auto load_pass = [&](uint32_t p, Row8 (&x)[4]) {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t place = base + kSpan * p + 4 * tg + i;
+      x[i] = Row8{};
+      if (active && place >= off && place < end) __builtin_memcpy(&x[i], src + place * row_stride, sizeof(x[i]));
     }
-    const float inv = power_inverse(scale);
-    for (uint32_t i = tid; i < cnt * D; i += kStoreThreads)
-      codes[(off + i / D) * st + (i % D) * sd] =
-          code_of(static_cast<float>(src[(i / D) * row + i % D]) * inv);
-    __syncthreads();  // every thread has read the old scale
-    if (tid == 0) *held = scale;
+  };
+  Row8 x[kKeep ? P : 1][4];
+  const float was = off ? *held : 0.0f;
+        // visit(p, rows) for the passes that hold places of the run, their rows
+        // loaded by then: all at once if they are kept, else one after the other.
+        auto each_pass = [&](bool loaded, auto&& visit) {
+          if constexpr (kKeep) {
+            if (!loaded) {
+#pragma unroll
+              for (uint32_t p = 0; p < P; ++p)
+                if (base + kSpan * (p + 1) > off && base + kSpan * p < end) load_pass(p, x[p]);
+            }
+#pragma unroll
+            for (uint32_t p = 0; p < P; ++p)
+              if (base + kSpan * (p + 1) > off && base + kSpan * p < end) visit(p, x[p]);
+          } else {
+#pragma clang loop unroll(disable)
+            for (uint32_t p = 0; p < P; ++p) {
+              if (base + kSpan * (p + 1) <= off || base + kSpan * p >= end) continue;
+              load_pass(p, x[0]);
+              visit(p, x[0]);
+            }
+          }
+        };
+        uint8_t* codes = A.cache + (side ? A.s.value_at(block, h) : A.s.key_at(block, h));
+        float amax = 0.0f;
+        bool strange = false;  // some element is not finite
+        if constexpr (sizeof(E) == 2) {
+          // two magnitudes at a time by their bits; what is not finite is left
+          // out in a second look, if there is any
+          u16x2 top = {0, 0};
+          each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j) {
+                asm volatile("" : "+v"(y[i].w[j]));  // (kept as it came, not widened)
+                top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, y[i].w[j] & 0x7FFF7FFFu));
+              }
+          });
+          uint32_t most = max<uint32_t>(top[0], top[1]);
+          strange = __ballot(most >= infinity_bits<E>()) != 0;
+          if (strange) {
+            most = 0;
+            each_pass(true, [&](uint32_t, Row8 (&y)[4]) {
+#pragma unroll
+              for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) {
+                  const uint32_t w = y[i].w[j], lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+                  if (lo < infinity_bits<E>()) most = max(most, lo);
+                  if (hi < infinity_bits<E>()) most = max(most, hi);
+                }
+            });
+          }
+          amax = static_cast<float>(__builtin_bit_cast(E, static_cast<uint16_t>(most)));
+        } else {
+          each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+              for (uint32_t j = 0; j < 8; ++j) {
+                const float v = element<E>(y[i].w, j);
+                amax = fmaxf(amax, finite_abs(v));
+                strange |= !(fabsf(v) <= 3.402823466e38f);
+              }
+          });
+          strange = __ballot(strange) != 0;
+        }
+        amax = wave_max(amax);
+        if constexpr (WV > 1) {
+          if (lane == 0) s_max[wave] = amax;
+          __syncthreads();
+#pragma unroll
+          for (uint32_t w = 0; w < WV; ++w) amax = fmaxf(amax, s_max[wave / WV * WV + w]);
+          __syncthreads();  // (also: every wave has read the old scale)
+        }
+        float scale = scale_of(amax);
+        const bool grew = off && scale > was;
+        if (off && !grew) scale = was;
+        const float again = grew ? was * power_inverse(scale) : 1.0f;
+#pragma clang loop unroll_count(kKeep ? P : 1)
+        for (uint32_t p = 0; p < P; ++p) {
+          if (base + kSpan * p >= end || (base + kSpan * (p + 1) <= off && !grew)) continue;
+          const uint32_t first = base + kSpan * p + 4 * tg;
+          if constexpr (!kKeep) load_pass(p, x[0]);
+          uint32_t lo[4], hi[4];  // the codes of dims 0 .. 3 and 4 .. 7 of each place
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            const Row8& r = x[kKeep ? p : 0][i];
+            lo[i] = codes_of<E>(r.w, 0, scale);
+            hi[i] = codes_of<E>(r.w, 1, scale);
+            if (strange) {
+              lo[i] = with_nans<E>(lo[i], r.w, 0);
+              hi[i] = with_nans<E>(hi[i], r.w, 1);
+            }
+          }
+          if (!active) continue;
+          if (side == 0) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+              const uint32_t place = first + i;
+              uint8_t* c = codes + place * D + 8 * col;
+              if (place >= off && place < end) {
+                *reinterpret_cast<u32x2*>(c) = u32x2{lo[i], hi[i]};
+              } else if (place < off && grew) {
+                for (uint32_t j = 0; j < 8; ++j) c[j] = code_of(value_of(c[j]) * again);
+              }
+            }
+          } else if (first >= off && first + 4 <= end) {
+            // four places by eight dims to eight words of four places
+            uint32_t v[2][4];
+            transpose(lo, v[0]);
+            transpose(hi, v[1]);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+              *reinterpret_cast<uint32_t*>(codes + (8 * col + j) * T + first) = v[j / 4][j % 4];
+          } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+              const uint32_t place = first + i;
+#pragma unroll
+              for (uint32_t j = 0; j < 8; ++j) {
+                uint8_t* c = codes + (8 * col + j) * T + place;
+                if (place >= off && place < end)
+                  *c = static_cast<uint8_t>((j < 4 ? lo[i] : hi[i]) >> (8 * (j % 4)));
+                else if (place < off && grew)
+                  *c = code_of(value_of(*c) * again);
+              }
+            }
+          }
+        }
+  if (lane == 0 && wave % WV == 0) *held = scale;
+}
+
+// A workgroup looks after the runs that begin in its tile of rows, for its
+// heads.  Runs that take more than one pass are done one after the other by all
+// waves, a pass each, and keep many loads in flight; shorter ones, such as a
+// decode step's single tokens, go to a wave each.
+template <typename E, int D, int T>
+__global__ void __launch_bounds__(kStoreWaves * 64) store_kernel(StoreArgs A) {
+  constexpr uint32_t kSpan = 4 * store_groups(D, T), kPasses = T / kSpan;
+  constexpr uint32_t WV = kPasses < kStoreWaves ? kPasses : kStoreWaves;
+  __shared__ float s_max[kStoreWaves];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
+  const uint32_t groups = (A.s.H + A.wg_heads - 1) / A.wg_heads;  // the heads of a tile side by side
+  const int32_t n0 = static_cast<int32_t>(blockIdx.x / groups * A.tile);
+  const uint32_t h0 = blockIdx.x % groups * A.wg_heads, items = min(A.wg_heads, A.s.H - h0) * 2;
+  // The slots of the tile's rows and of those that a run from there may reach.
+  auto slot_at = [&](int32_t n) { return n >= 0 && n < A.rows ? A.slots[n] : -1; };
+  const int32_t near = slot_at(n0 + static_cast<int32_t>(lane)), before = slot_at(n0 - 1);
+  const int32_t last = __shfl_up(near, 1);
+  const bool begins = lane < A.tile && near >= 0 && static_cast<uint32_t>(near) / T < A.s.blocks &&
+                      (near % T == 0 || (lane ? last : before) != near - 1);
+  const uint64_t runs = __ballot(begins);
+  if (runs == 0) return;
+  const int32_t far = A.tile + T > 65 ? slot_at(n0 + 64 + static_cast<int32_t>(lane)) : -1;
+  // each(long, f) calls f(row, block, off, end) for the runs of more than one pass, or the others.
+  auto each = [&](bool longer, auto&& f) {
+    for (uint64_t left = runs; left; left &= left - 1) {
+      const int32_t r = __builtin_ctzll(left);  // the run's first row in the tile
+      const int32_t slot = __builtin_amdgcn_readlane(near, r);
+      const uint32_t off = static_cast<uint32_t>(slot) % T, at = r + lane;
+      const int32_t close = __shfl(near, at & 63), wide = __shfl(far, at & 63);
+      const bool goes_on =
+          off + lane < T && (at < 64 ? close : wide) == slot + static_cast<int32_t>(lane);
+      const uint64_t stops = ~__ballot(goes_on);
+      const uint32_t end = off + (stops ? __builtin_ctzll(stops) : 64u);
+      if (((end - 1) / kSpan > off / kSpan) == longer) f(n0 + r, static_cast<uint32_t>(slot) / T, off, end);
+    }
+  };
+  if constexpr (kPasses > 1)
+    each(true, [&](int32_t n, uint32_t block, uint32_t off, uint32_t end) {
+      for (uint32_t k = wave / WV; k < items; k += kStoreWaves / WV)
+        store_item<E, D, T, WV>(A, s_max, n, block, off, end, h0 + k / 2, k % 2);
+    });
+  uint32_t turn = 0;
+  each(false, [&](int32_t n, uint32_t block, uint32_t off, uint32_t end) {
+    for (uint32_t k = 0; k < items; ++k)
+      if (turn++ % kStoreWaves == wave)
+        store_item<E, D, T, 1>(A, s_max, n, block, off, end, h0 + k / 2, k % 2);
+  });
+}
+
+using StoreFn = void (*)(StoreArgs);
+
+template <typename E, int D>
+StoreFn pick_store_tokens(uint32_t t) {
+  return t == 16 ? store_kernel<E, D, 16> : t == 32 ? store_kernel<E, D, 32> : store_kernel<E, D, 64>;
+}
+
+template <typename E>
+StoreFn pick_store(uint32_t d, uint32_t t) {
+  switch (d) {
+    case 64: return pick_store_tokens<E, 64>(t);
+    case 96: return pick_store_tokens<E, 96>(t);
+    case 128: return pick_store_tokens<E, 128>(t);
+    case 192: return pick_store_tokens<E, 192>(t);
+    default: return pick_store_tokens<E, 256>(t);
   }
 }
 
@@ -341,13 +608,9 @@ struct AttendArgs {
   Shape s;
 };
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <typename E>
 struct Vec8;
@@ -1170,11 +1433,21 @@ extern "C" int xfer_cache_store(const xfer_cache_shape* shape, void* cache, cons
   a.value_head = value_head;
   a.slots = slots;
   a.rows = rows;
-  const dim3 grid(uint32_t(rows), a.s.H);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = dtype == XFER_BF16   ? launch(store_kernel<bf16_t>, a, grid, kStoreThreads, s)
-                       : dtype == XFER_FP16 ? launch(store_kernel<fp16_t>, a, grid, kStoreThreads, s)
-                                            : launch(store_kernel<float>, a, grid, kStoreThreads, s);
+  // Rows of a workgroup's tile: a decode step wants a workgroup per token, a
+  // prompt one per block, and the lengths of runs are not known here.  Tiles of
+  // 1, 8 and T rows take, with 8 heads of 128, bfloat16 and blocks of 16 (64), in
+  // us: 256 single tokens 10, 19, 11 (13, 24, 138), 1024 of them 21, 25, 23 (27,
+  // 32, 144), 4096 60, 63, 66 (138, 145, 174); a prompt of 500 tokens 10, 9, 9 (24,
+  // 10, 13), of 2000 23, 11, 10 (28, 15, 13), of 4000 37, 15, 12 (41, 23, 15), 26k of
+  // prompts 152, 67, 46 (150, 83, 47: 3.4 TB/s read and written, waiting for memory).
+  a.tile = rows <= 256 ? 1 : rows <= 2048 ? 8 : a.s.T;
+  a.wg_heads = a.tile == 1 ? 2 : 1;
+  const uint32_t tiles = (uint32_t(rows) + a.tile - 1) / a.tile;
+  const dim3 grid(tiles * ((a.s.H + a.wg_heads - 1) / a.wg_heads));
+  const StoreFn fn = dtype == XFER_BF16   ? pick_store<bf16_t>(a.s.D, a.s.T)
+                     : dtype == XFER_FP16 ? pick_store<fp16_t>(a.s.D, a.s.T)
+                                          : pick_store<float>(a.s.D, a.s.T);
+  const hipError_t e = launch(fn, a, grid, kStoreWaves * 64, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "xfer_cache_store launch");
   return XFER_OK;
 }

@@ -134,8 +134,8 @@ class FakeTensor:
     def dim(self):
         return len(self.shape)
 
-    def stride(self, i):
-        return self._strides[i]
+    def stride(self, i=None):
+        return self._strides if i is None else self._strides[i]
 
     def numel(self):
         return int(np.prod(self.shape))
