@@ -1487,8 +1487,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rsrc(const BlockList& B,
 
 // Calls f(descriptor, byte offset in the block) for this lane's unit x of
 // access u, in the lanes of each block it meets in turn; every wave calls f
-// at least once per access (with an empty descriptor past the end).
-template <bool SRC, typename F>
+// at least once per access (with an empty descriptor past the end).  LONG:
+// blocks are 64 units or longer, so an access meets two at most.
+template <bool SRC, bool LONG, typename F>
 __device__ __forceinline__ void each_block(const BlockList& B, const ListPos& at,
                                            const BatchIds& ids, uint32_t u, const uint8_t* pool,
                                            uint32_t base, uint32_t x, uint32_t lim, F&& f) {
@@ -1496,24 +1497,26 @@ __device__ __forceinline__ void each_block(const BlockList& B, const ListPos& at
   const uint32_t last = __builtin_amdgcn_readlane(ids.entry, kUnroll + u);
   const int32_t id = __builtin_amdgcn_readlane(SRC ? ids.from : ids.to, u);
   const uint32_t y = at.rem + base + x;
-  if (first == last) {  // a whole access inside one block (or past the end)
-    const uint32_t off = (x < lim ? y - first * B.units : B.units) << 4;
-    f(block_rsrc(B, pool, id), off);
-    return;
-  }
-  const uint32_t mine = x < lim ? entry_of(B, y) : 0xFFFFFFFFu;
-  for (uint32_t e = first; e <= last; ++e) {
-    int32_t ef, et;
-    if (e == first) {
-      ef = et = id;
-    } else if (e == last) {
-      ef = et = __builtin_amdgcn_readlane(SRC ? ids.from : ids.to, kUnroll + u);
-    } else {
-      entry_ids(B, at, e, ef, et);
-      ef = __builtin_amdgcn_readfirstlane(ef);
-      et = __builtin_amdgcn_readfirstlane(et);
+  if constexpr (LONG) {
+    // the first block for all lanes (those past its end, or the chunk's, are
+    // outside the descriptor), then the second, if there is one, for its own
+    const uint32_t off = x < lim ? y - first * B.units : B.units;
+    f(block_rsrc(B, pool, id), min(off, B.units) << 4);
+    if (first != last && x < lim && off >= B.units)
+      f(block_rsrc(B, pool, __builtin_amdgcn_readlane(SRC ? ids.from : ids.to, kUnroll + u)),
+        (off - B.units) << 4);
+  } else {
+    const uint32_t mine = x < lim ? entry_of(B, y) : 0xFFFFFFFFu;
+    if (first == last) {  // (also past the end)
+      f(block_rsrc(B, pool, id), (x < lim ? y - first * B.units : B.units) << 4);
+      return;
     }
-    if (mine == e) f(block_rsrc(B, pool, SRC ? ef : et), (y - e * B.units) << 4);
+    for (uint32_t e = first; e <= last; ++e) {
+      int32_t ef, et;
+      entry_ids(B, at, e, ef, et);
+      const int32_t one = __builtin_amdgcn_readfirstlane(SRC ? ef : et);
+      if (mine == e) f(block_rsrc(B, pool, one), (y - e * B.units) << 4);
+    }
   }
 }
 
@@ -1524,28 +1527,28 @@ __device__ __forceinline__ LaneSpan unit_span(uint32_t L, uint64_t S, uint32_t P
   return LaneSpan{sp.base >> 4, sp.lim >> 4};
 }
 
-template <int LP, bool CYC>
+template <int LP, bool CYC, bool LONG>
 __device__ __forceinline__ void blocks_load(Batch& b, const BlockList& B, const ListPos& at,
                                             const BatchIds& ids, const uint8_t* pool, LaneSpan sp,
                                             uint32_t u0, uint32_t w, uint32_t P) {
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const uint32_t x = wave_unit<CYC>(w, P, u0 + u) + (threadIdx.x & 63u);
-    each_block<true>(B, at, ids, u, pool, sp.base, x, sp.lim,
+    each_block<true, LONG>(B, at, ids, u, pool, sp.base, x, sp.lim,
                      [&](__amdgpu_buffer_rsrc_t rs, uint32_t off) {
                        b.r[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, LP);
                      });
   }
 }
 
-template <int SP, bool CYC>
+template <int SP, bool CYC, bool LONG>
 __device__ __forceinline__ void blocks_store(const Batch& b, const BlockList& B, const ListPos& at,
                                              const BatchIds& ids, const uint8_t* pool, LaneSpan sp,
                                              uint32_t u0, uint32_t w, uint32_t P) {
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const uint32_t x = wave_unit<CYC>(w, P, u0 + u) + (threadIdx.x & 63u);
-    each_block<false>(B, at, ids, u, pool, sp.base, x, sp.lim,
+    each_block<false, LONG>(B, at, ids, u, pool, sp.base, x, sp.lim,
                       [&](__amdgpu_buffer_rsrc_t rs, uint32_t off) {
                         __builtin_amdgcn_raw_buffer_store_b128(b.r[u], rs, off, 0, SP);
                       });
@@ -1578,7 +1581,7 @@ __device__ bool blocks_send(const ConnArgs& A, const BlockList& B, uint32_t c, u
         Batch b;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) b.r[u] = u32x4{0u, 0u, 0u, 0u};
-        blocks_load<kPolNT, false>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
+        blocks_load<kPolNT, false, false>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
           __builtin_amdgcn_raw_buffer_store_b128(b.r[u], rd, lane_vec<false>(w, A.lanes, u0 + u), 0,
@@ -1627,7 +1630,7 @@ __device__ bool blocks_recv(const ConnArgs& A, const BlockList& B, uint32_t c, u
         for (int u = 0; u < kUnroll; ++u)
           b.r[u] = __builtin_amdgcn_raw_buffer_load_b128(rs, lane_vec<false>(w, A.lanes, u0 + u), 0,
                                                          O::kShared);
-        blocks_store<kPolNT, false>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
+        blocks_store<kPolNT, false, false>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
       }
       // The slot goes back once this wave's reads of it are complete: not
       // every read feeds a store here (an entry outside its pool), so the
@@ -1644,6 +1647,65 @@ __device__ bool blocks_recv(const ConnArgs& A, const BlockList& B, uint32_t c, u
   return true;
 }
 
+// The place in the lists one step of `units` on: no division by the block's
+// bytes, which is a long chain of instructions, within the loop.
+__device__ __forceinline__ ListPos list_next(const BlockList& B, const ListPos& at, uint32_t units) {
+  const uint32_t x = at.rem + units, e = entry_of(B, x);
+  return ListPos{at.entry + e, x - e * B.units};
+}
+
+// Zero-copy direct where a lane's share of a step fits one register batch,
+// and blocks are 64 units or longer, software pipelined: while the stores of step j drain, step j + 1 is loaded,
+// and the list entries of step j + 2 are fetched ahead of those loads.  Every
+// access of a batch loads at least once, so at most kUnroll operations in
+// flight means that the stores before them are complete.
+template <int SC, int ORD>
+__device__ bool blocks_zcd_send_piped(const ConnArgs& A, const BlockList& B, uint32_t w, Side& sd,
+                                      Shared& sh) {
+  using O = Order<SC, ORD>;
+  const uint64_t S = A.step_bytes;
+  const uint32_t P = A.lanes, units = static_cast<uint32_t>(S >> 4);
+  auto span = [&](uint64_t j) { return unit_span<true>(chunk_len(sd, S, j), S, P, w); };
+  Batch b;
+  ListPos at = list_pos(B, sd.r.beg), ahead = at;
+  LaneSpan sp = span(0), sp_ahead = sp;
+  BatchIds ids = batch_ids<true>(B, at, sp.base, sp.lim, 0, w, P), ids_ahead = ids;
+  if (sd.r.k > 1) {
+    ahead = list_next(B, at, units);
+    sp_ahead = span(1);
+    ids_ahead = batch_ids<true>(B, ahead, sp_ahead.base, sp_ahead.lim, 0, w, P);
+  }
+  blocks_load<kPolNT, true, true>(b, B, at, ids, A.src, sp, 0, w, P);
+  for (uint64_t j = 0; j < sd.r.k; ++j) {
+    const uint64_t g = sd.base + j;
+    if (threadIdx.x == 0) trace_step(A, sd, g, 0, sd.r.beg + j * S);
+    jitter(sd, g, 0);
+    blocks_store<O::kShared, true, true>(b, B, at, ids, A.dst, sp, 0, w, P);
+    compiler_fence();  // what follows issues after these stores: vmcnt counts on that
+    if (j + 1 < sd.r.k) {
+      at = ahead;
+      sp = sp_ahead;
+      ids = ids_ahead;
+      if (j + 2 < sd.r.k) {
+        ahead = list_next(B, at, units);
+        sp_ahead = span(j + 2);
+        ids_ahead = batch_ids<true>(B, ahead, sp_ahead.base, sp_ahead.lim, 0, w, P);
+      }
+      blocks_load<kPolNT, true, true>(b, B, at, ids, A.src, sp, 0, w, P);
+      wait_vmcnt<kUnroll>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    jitter(sd, g, 1);
+    if (wg_failed(sh, 0, A)) return false;
+    if (threadIdx.x == 0) {
+      trace_step(A, sd, g, 1, g + 1);
+      st_u64<SC>(&sd.rx->tail, g + 1);
+    }
+  }
+  return true;
+}
+
 // Zero-copy direct: every unit goes from its source block to its destination
 // block in one pass.
 template <int SC, int ORD>
@@ -1651,6 +1713,8 @@ __device__ bool blocks_zcd_send(const ConnArgs& A, const BlockList& B, uint32_t 
                                 Shared& sh) {
   using O = Order<SC, ORD>;
   const uint64_t S = A.step_bytes;
+  if (ORD == kOrdCoherent && B.units >= 64 && lane_blocks<true>(S, A.lanes) <= kUnroll)
+    return sd.r.k == 0 || blocks_zcd_send_piped<SC, ORD>(A, B, w, sd, sh);
   for (uint64_t j = 0; j < sd.r.k; ++j) {
     const uint64_t g = sd.base + j;
     if (threadIdx.x == 0) trace_step(A, sd, g, 0, sd.r.beg + j * S);
@@ -1663,8 +1727,8 @@ __device__ bool blocks_zcd_send(const ConnArgs& A, const BlockList& B, uint32_t 
       Batch b;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) b.r[u] = u32x4{0u, 0u, 0u, 0u};
-      blocks_load<kPolNT, true>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
-      blocks_store<O::kShared, true>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
+      blocks_load<kPolNT, true, false>(b, B, at, ids, A.src, sp, u0, w, A.lanes);
+      blocks_store<O::kShared, true, false>(b, B, at, ids, A.dst, sp, u0, w, A.lanes);
     }
     O::release();
     jitter(sd, g, 1);
