@@ -748,7 +748,7 @@ struct Values {
 
 // Workgroups a CU is to hold: bounds the registers of a lane.
 constexpr int attend_resident(int d, int nr) {
-  return nr == 2 ? (d <= 96 ? 2 : 1) : d == 64 ? 3 : d <= 128 ? 2 : 1;
+  return nr == 2 ? 2 : d == 64 ? 3 : d <= 192 ? 2 : 1;
 }
 
 template <int D, bool ONCE>
@@ -829,10 +829,13 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
       }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    top = fmaxf(top, m[x]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float keep = __builtin_amdgcn_exp2f(m[x] - base);
-    m[x] = top;
+    // The reference m follows the maximum only when that is 8 above it, so most
+    // chunks leave the accumulators alone: weights reach 256 at most, and the
+    // same powers of two leave sums and accumulators in the end.
+    const bool grows = top > m[x] + 8.0f;
+    const float next = grows ? top : m[x], base = next == -INFINITY ? 0.0f : next;
+    const float keep = grows ? __builtin_amdgcn_exp2f(m[x] - base) : 1.0f;
+    m[x] = next;
     float sum = 0.0f;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -846,8 +849,10 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
           p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
       }
     l[x] = l[x] * keep + sum;
+    if (__ballot(grows) != 0) {
 #pragma unroll
-    for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+      for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+    }
   }
   // Codes of tokens that no row sees are cleared: they may be anything, and 0
   // times NaN is NaN.
