@@ -288,7 +288,9 @@ int xfer_run_messages(xfer_conn* c, const void* src, void* dst, const size_t* of
  *   src, dst     16-byte aligned; the pools must not overlap, and the lists
  *                must not lie in dst.
  * Errors: INVALID_ARG (other protocols, sizes outside these domains, NULL
- * buffers or lists with n > 0, overlap, grid too large), STATE, HIP. */
+ * buffers or lists with n > 0, overlap, grid too large), STATE, HIP.  In a
+ * step trace the value of a zero-copy step's acquire is its byte offset in the
+ * list instead of an address. */
 int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks, void* dst,
                     size_t dst_blocks, size_t block_bytes, const int32_t* from,
                     const int32_t* to, size_t n, void* stream);
@@ -391,7 +393,10 @@ int xfer_cache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
  * Entries of the table outside the new blocks stay as they are.  rows may
  * exceed the packed rows (a padded batch) or fall short (the rest is cut).
  * The sums of the lengths must stay below 2^31.  table_stride: elements from
- * a request's row of table_width entries to the next. */
+ * a request's row of table_width entries to the next.  Rows of the table must
+ * not overlap, nor the outputs any input.
+ * Errors: INVALID_ARG (counts below 0, other block sizes, NULL or misaligned
+ * arrays), HIP. */
 int xfer_cache_plan(const int32_t* cached, const int32_t* added, int batch, int32_t* table,
                     int64_t table_stride, int table_width, const int32_t* free_blocks, int nfree,
                     int block_tokens, int32_t* slots, int32_t* positions, int rows,
@@ -428,8 +433,11 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * launch: results are right for any lengths.
  * workspace: device memory of xfer_cache_attend_workspace() bytes for these
  * arguments, 16-byte aligned, used by this call alone until it has run.
- * Scores, sums and outputs are accumulated in float; the weights exp(...)
- * are rounded to bfloat16 before they multiply the values. */
+ * Scores, sums and outputs are accumulated in float; before they multiply the
+ * values, the weights exp(...) are rounded to bfloat16 (for FP16 queries to the
+ * sum of two bfloat16 numbers).
+ * Errors: INVALID_ARG (sizes outside their domains: batch * H below 2^24, rows *
+ * heads below 2^31; NULL or misaligned buffers, too small a workspace), HIP. */
 typedef struct {
   const void* query; /* [rows][heads][D], dtype BF16 or FP16 */
   void* out;         /* [rows][heads][D], same dtype */

@@ -1340,6 +1340,7 @@ AttendWork attend_work(const Shape& s, const xfer_attend& q, const AttendPlan& p
 
 // ------------------------------------------------------------------ checks
 constexpr int kMaxHeads = 1024;
+constexpr uint64_t kMaxGrid = (1u << 24) - 1;  // workgroups of 256 threads: 2^32 threads at most
 
 int shape_of(const xfer_cache_shape* g, const char* who, Shape* out) {
   if (!g) return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": NULL shape");
@@ -1448,7 +1449,10 @@ extern "C" int xfer_cache_store(const xfer_cache_shape* shape, void* cache, cons
   a.tile = rows <= 256 ? 1 : rows <= 2048 ? 8 : a.s.T;
   a.wg_heads = a.tile == 1 ? 2 : 1;
   const uint32_t tiles = (uint32_t(rows) + a.tile - 1) / a.tile;
-  const dim3 grid(tiles * ((a.s.H + a.wg_heads - 1) / a.wg_heads));
+  const uint64_t wgs = uint64_t(tiles) * ((a.s.H + a.wg_heads - 1) / a.wg_heads);
+  if (wgs > kMaxGrid)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_cache_store: too many rows times heads for one call");
+  const dim3 grid(static_cast<uint32_t>(wgs));
   const StoreFn fn = dtype == XFER_BF16   ? pick_store<bf16_t>(a.s.D, a.s.T)
                      : dtype == XFER_FP16 ? pick_store<fp16_t>(a.s.D, a.s.T)
                                           : pick_store<float>(a.s.D, a.s.T);
@@ -1471,6 +1475,8 @@ int attend_args(const xfer_cache_shape* shape, const xfer_attend* q, const char*
                 std::string(who) + ": heads must be a multiple of kv_heads, at most 16384");
   if (int64_t(q->rows) * q->heads > 0x7FFFFFFFll)
     return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": rows * heads must stay below 2^31");
+  if (uint64_t(q->batch) * uint64_t(shape->kv_heads) > kMaxGrid)
+    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": batch * kv_heads must stay below 2^24");
   if (q->dtype != XFER_BF16 && q->dtype != XFER_FP16)
     return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": dtype must be BF16 or FP16");
   if (!(q->scale > 0.0f) || !(q->scale <= 3.402823466e38f))

@@ -57,7 +57,7 @@ def _attend(**kw):
 @pytest.mark.parametrize("kw", [dict(batch=-1), dict(rows=-1), dict(table_width=-1),
                                 dict(table_stride=3), dict(heads=0), dict(heads=3),
                                 dict(heads=1 << 17), dict(dtype=2), dict(dtype=-1),
-                                dict(rows=1 << 29, heads=4), dict(workspace_bytes=0, table_width=1 << 20, table_stride=1 << 20),
+                                dict(rows=1 << 29, heads=4), dict(batch=1 << 23), dict(workspace_bytes=0, table_width=1 << 20, table_stride=1 << 20),
                                 dict(workspace=None, table_width=1 << 20, table_stride=1 << 20),
                                 dict(workspace=P + 8, table_width=1 << 20, table_stride=1 << 20),
                                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
@@ -90,6 +90,11 @@ def test_store_refuses(i, bad):
     args[i] = bad
     assert X.lib().xfer_cache_store(*args) == INVALID
     assert xf.last_error().startswith("xfer_cache_store")
+
+
+def test_store_refuses_too_many_workgroups():
+    args = [C.byref(_shape(h=1024)), P, P, 256, 128, P, 256, 128, 0, P, 1 << 30, None]
+    assert X.lib().xfer_cache_store(*args) == INVALID and "too many" in xf.last_error()
 
 
 def test_store_of_nothing():
