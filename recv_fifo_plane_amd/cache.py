@@ -27,15 +27,17 @@ HEAD_DIMS = (64, 96, 128, 192, 256)
 
 
 _KINDS = {}  # torch dtypes of rows to xfer_dtype, filled at the first call
-_INT32 = None
+_INT32 = _FLOAT32 = _UINT8 = None
+_RAW = None  # the current stream's handle of a device, where torch gives it without an object
 
 
 def _kinds():
-    global _INT32
+    global _INT32, _FLOAT32, _UINT8, _RAW
     if not _KINDS:
         import torch
+        _INT32, _FLOAT32, _UINT8 = torch.int32, torch.float32, torch.uint8
+        _RAW = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _KINDS.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-        _INT32 = torch.int32
     return _KINDS
 
 
@@ -56,13 +58,17 @@ def _tensor(t, what, dtypes, ndim, device):
 
 def _list(t, what, n, device):
     """Address of a contiguous int32 tensor of n entries (None: any number)."""
+    try:  # the usual case, in few calls
+        if (t.dtype is _INT32 and t.is_cuda and (device is None or t.get_device() == device)
+                and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _tensor(t, what, (_INT32,), 1, device)
     have = t.shape[0]
     if n is not None and have != n:
         raise ValueError("%s: expected %d entries, got %d" % (what, n, have))
-    if have > 1 and t.stride(0) != 1:
-        raise ValueError("%s: tensor is not contiguous" % what)
-    return t.data_ptr()
+    raise ValueError("%s: tensor is not contiguous" % what)
 
 
 def _table(t, what, batch, device):
@@ -94,7 +100,7 @@ def _call(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
     import torch
     if device == torch.cuda.current_device():
-        rc = fn(*args, X._stream_handle(stream))
+        rc = fn(*args, _RAW(device) or None if stream is None and _RAW else X._stream_handle(stream))
     else:
         with torch.cuda.device(device):
             rc = fn(*args, X._stream_handle(stream))
@@ -113,11 +119,6 @@ def _keep(stream, *tensors):
     if stream != torch.cuda.current_stream():
         for t in tensors:
             t.record_stream(stream)
-
-
-def _empty(like, shape, dtype):
-    import torch
-    return torch.empty(shape, dtype=getattr(torch, dtype), device=like.device)
 
 
 def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=None,
@@ -142,9 +143,15 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
     if out is None:
         buf = cached.new_empty(sum(sizes))
         _keep(stream, buf)
-        out = BlockPlan(*buf.split(sizes))
-    slots, positions, starts, lengths, counts = (
-        _list(t, "plan_blocks: out", n, dev) for t, n in zip(out, sizes))
+        out = BlockPlan(*buf.split_with_sizes(sizes))
+        slots = buf.data_ptr()
+        positions = slots + 4 * rows
+        starts = positions + 4 * rows
+        lengths = starts + 4 * (batch + 1)
+        counts = lengths + 4 * batch
+    else:
+        slots, positions, starts, lengths, counts = (
+            _list(t, "plan_blocks: out", n, dev) for t, n in zip(out, sizes))
     _call(dev, stream, X.lib().xfer_cache_plan, at_cached, at_added, batch, at_table, stride, width,
           at_free, free.shape[0], int(block_tokens), slots, positions, rows, starts, lengths,
           counts)
@@ -246,10 +253,10 @@ class PagedCache:
         o, o_row, o_head = _rows(out, "attend: out", (dtype,), self.device, rows, heads, d)
         sums = None
         if lse is True:
-            sums = _empty(query, (rows, heads), "float32")
+            sums = query.new_empty((rows, heads), dtype=_FLOAT32)
             _keep(stream, sums)
         elif lse is not False and lse is not None:
-            sums = _tensor(lse, "attend: lse", [t for t, k in kinds.items() if k == 2], 2, self.device)
+            sums = _tensor(lse, "attend: lse", (_FLOAT32,), 2, self.device)
             if tuple(sums.shape) != (rows, heads) or not sums.is_contiguous():
                 raise ValueError("attend: lse must be contiguous of shape (%d, %d)" % (rows, heads))
         a = X.xfer_attend(q, o, None if sums is None else sums.data_ptr(), at_table, at_lengths,
@@ -262,7 +269,7 @@ class PagedCache:
         if rc:
             X.check(rc)
         if n.value:
-            work = _empty(query, (n.value,), "uint8")
+            work = query.new_empty(n.value, dtype=_UINT8)
             _keep(stream, work)
             a.workspace, a.workspace_bytes = work.data_ptr(), n.value
         _call(self.device, stream, lib.xfer_cache_attend, self._ref, self._base, ref)
@@ -270,10 +277,18 @@ class PagedCache:
 
     def send(self, conn, dst, src_ids, dst_ids, stream=None) -> None:
         """Moves block src_ids[i] of this cache to block dst_ids[i] of the cache
-        `dst` over a connection (Conn.run_blocks): int32 lists in GPU memory."""
+        `dst` over a connection (as Conn.run_blocks does): int32 lists in GPU memory."""
         mine = (self.block_tokens, self.kv_heads, self.head_dim)
         other = (dst.block_tokens, dst.kv_heads, dst.head_dim)
         if mine != other:
             raise ValueError("send: blocks of shape %s cannot go into blocks of shape %s"
                              % (mine, other))
-        conn.run_blocks(self.buffer, dst.buffer, self.block_bytes, src_ids, dst_ids, stream=stream)
+        _kinds()
+        if not self.device == dst.device == conn.device:
+            raise ValueError("send: caches on cuda:%s and cuda:%s, the connection on cuda:%s"
+                             % (self.device, dst.device, conn.device))
+        a = _list(src_ids, "send: src_ids", None, self.device)
+        n = src_ids.shape[0]
+        b = _list(dst_ids, "send: dst_ids", n, self.device)
+        _call(self.device, stream, X.lib().xfer_run_blocks, conn.handle, self._base, self.blocks,
+              dst._base, dst.blocks, self.block_bytes, a, b, n)

@@ -142,6 +142,9 @@ class FakeTensor:
     def stride(self, i=None):
         return self._strides if i is None else self._strides[i]
 
+    def get_device(self):
+        return self.device.index
+
     def numel(self):
         return int(np.prod(self.shape))
 
@@ -271,6 +274,16 @@ def test_send_and_run_blocks_arguments(cache):
         other.__dict__.update(cache.__dict__, kv_heads=4)
         with pytest.raises(ValueError, match="cannot go"):
             cache.send(conn, other, FakeTensor((3,)), FakeTensor((3,)))
+        for ids in ((FakeTensor((3,)), FakeTensor((4,))), (torch.zeros(3, dtype=torch.int32), FakeTensor((3,))),
+                    (FakeTensor((3,), strides=(2,)), FakeTensor((3,))), (FakeTensor((3,), device=1), FakeTensor((3,)))):
+            with pytest.raises(ValueError):
+                cache.send(conn, cache, *ids)
+        with pytest.raises(TypeError):
+            cache.send(conn, cache, FakeTensor((3,)), FakeTensor((3,), torch.int64))
+        conn.device = 1
+        with pytest.raises(ValueError, match="cuda:1"):
+            cache.send(conn, cache, FakeTensor((3,)), FakeTensor((3,)))
+        conn.device = 0
         pool = FakeTensor((10, 4096), torch.uint8)
         with pytest.raises(ValueError, match="ids"):
             conn.run_blocks(pool, pool, 4096, FakeTensor((3,)), FakeTensor((4,)))
