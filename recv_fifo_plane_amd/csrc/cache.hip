@@ -982,7 +982,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
         const uint32_t step = wave + k * kAttendWaves;
         if (there && step < KL) __builtin_memcpy(&q[x][k], p + key_dim<D>(step, g), 16);
       }
-      least = min(least, limit[x]);
+      if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
     }
     if (c < c1) {
       at.settle(A, c * kChunk, seen_all, g);
@@ -1016,8 +1016,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
     // branch around the loads would make every wait after it one for all of
     // them.
     auto step = [&](auto masked) {
-      const int32_t t0 = static_cast<int32_t>(c * kChunk);
-      const uint32_t tg = t0 + 16 * g, ahead = t0 + kNext;
+      const uint32_t t0 = c * kChunk, tg = t0 + 16 * g, ahead = t0 + kNext;
       const int32_t bg = at.mine;
       f32x4 s[NR][4];
 #pragma unroll
