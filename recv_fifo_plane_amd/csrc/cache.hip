@@ -1121,15 +1121,17 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
   }
 }
 
-// One workgroup per tile of rows and key/value head.
+// One workgroup per tile of rows and key/value head.  The last tiles see most
+// tokens and are begun first: with 32 heads of 128 over 8, 8 requests of 3000 to
+// 3900 tokens, 700 to 3000 of them new, take 1013 us and not 1141, 2 requests of
+// 500 to 1000 tokens, all new, 54 and not 63.
 template <typename E, int D, int NR, bool ONCE>
 __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
   __shared__ AttendShared<D, NR> sh;
   const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H;
-  for (uint32_t y = blockIdx.y;; y += gridDim.y) {
-    if (y >= units_of(A, b, NR * 16).tiles) return;
-    attend_rows<E, D, NR, ONCE>(A, sh, b, h, y * NR * 16, 0, ~0u, nullptr, nullptr);
-  }
+  const uint32_t tiles = units_of(A, b, NR * 16).tiles;
+  for (uint32_t y = blockIdx.y; y < tiles; y += gridDim.y)
+    attend_rows<E, D, NR, ONCE>(A, sh, b, h, (tiles - 1 - y) * NR * 16, 0, ~0u, nullptr, nullptr);
 }
 
 // The chunks of all requests and tiles in one line, cut into equal shares for
