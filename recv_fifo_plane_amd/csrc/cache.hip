@@ -748,7 +748,7 @@ struct Values {
 
 // Workgroups a CU is to hold: bounds the registers of a lane.
 constexpr int attend_resident(int d, int nr) {
-  return nr == 2 ? 2 : d == 64 ? 3 : d <= 192 ? 2 : 1;
+  return nr == 2 ? (d <= 128 ? 2 : 1) : d == 64 ? 3 : d <= 192 ? 2 : 1;
 }
 
 template <int D, bool ONCE>
@@ -950,16 +950,20 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
 
     // The first chunk's table entries, then its keys and values, are asked for
     // before anything is waited for: each is a trip to memory.
-    const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen));
+    // Waves with no chunk ask too, for the last block or, where no token is seen
+    // and the table may be empty, for whichever the first entry of starts names
+    // (any word will do, settle puts it in range): behind a branch around these
+    // loads every wait of the loop would be one for all of them.
+    const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen)), reach = max(seen_all, 1u);
+    if (seen_all == 0) table = A.starts;
     uint32_t c = c0 + wave, nans = 0;
     Keys<D, ONCE> keys;
     Values<D, ONCE> vals;
     Place at, next;
     constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
-    if (c < c1) {
-      at.look(A, table, c * kChunk, seen_all, g, n);
-      next.look(A, table, c * kChunk + kNext, seen_all, g, n);
-    }
+    at.look(A, table, c * kChunk, reach, g, n);
+    next.look(A, table, c * kChunk + kNext, reach, g, n);
+    __builtin_amdgcn_sched_barrier(0);
 
     // Queries: lane (g, n) takes row n's dims in the order of its key loads.
     // They wait in shared memory, the same for every wave, which frees the
@@ -984,11 +988,10 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
       }
       if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
     }
-    if (c < c1) {
-      at.settle(A, c * kChunk, seen_all, g);
-      keys.load(A, at, c * kChunk, h, g, n);
-      vals.load(A, at, c * kChunk, h, g, n);
-    }
+    at.settle(A, c * kChunk, seen_all, g);
+    keys.load(A, at, c * kChunk, h, g, n);
+    __builtin_amdgcn_sched_barrier(0);
+    vals.load(A, at, c * kChunk, h, g, n);
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -1269,12 +1272,15 @@ struct AttendKernels {
 
 template <typename E, int D, int NR, bool ONCE>
 AttendKernels attend_of() {
-  return {attend_kernel<E, D, NR, ONCE>, attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
+  if constexpr (D * NR > 256)  // (sharing needs registers that are not there)
+    return {attend_kernel<E, D, NR, ONCE>, nullptr, nullptr};
+  else
+    return {attend_kernel<E, D, NR, ONCE>, attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
 }
 
 template <typename E, int D>
 AttendKernels pick_attend_rows(int nr, bool once) {
-  if constexpr (D <= 128) {
+  if constexpr (D != 192) {
     if (nr == 2) return attend_of<E, D, 2, false>();
   }
   return once ? attend_of<E, D, 1, true>() : attend_of<E, D, 1, false>();
@@ -1304,7 +1310,16 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   int64_t most = q.max_query ? std::min(q.max_query, q.rows) : q.rows;
   if (!q.max_query && q.rows <= q.batch) most = 1;
   const int64_t rows = most * group;
-  p.nr = rows <= 16 || s.D > 128 ? 1 : 2;
+  // Two tiles of rows share the widened codes and halve the reads, but two of 192
+  // or 256 leave a CU one workgroup, and those of 256 no registers for sharing.
+  // One against two (us, drafts with 12 heads over 2, the others with 32 over 8):
+  // heads of 192: 48 requests of 3 to 5 rows 24 / 47, 8 with 1 to 600 rows after up
+  // to 5000 tokens 165 / 184, 2 prompts of 1000 93 / 110, 8 of 3000 2080 / 1840.
+  // Heads of 256: 48 drafts 39 / 60, a prompt of 100 15 / 20 (200 tiles), 256 drafts
+  // 73 / 73 (1024), 2 prompts of 1000 210 / 144 (4000), 8 with up to 600 rows 352 / 362,
+  // 8 prompts of 3000 4460 / 2580.
+  p.nr = rows <= 16 || s.D == 192 ? 1 : 2;
+  if (s.D == 256 && q.batch * int64_t(s.H) * ((rows + 15) / 16) <= 1024) p.nr = 1;
   p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.nr * 16 - 1) / (p.nr * 16)));
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
@@ -1317,7 +1332,7 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   // 8192 75 / 56; 128 requests of 410 .. 4096 106 / 106.
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
   p.flat = 0;
-  if (chunks >= (wgs <= 128 ? 24 : 64)) {
+  if (chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * p.nr <= 256) {
     // As many workgroups as are resident at once on 256 CUs, eight chunks each at least.
     const int64_t resident = 256 * attend_resident(int(s.D), p.nr);
     p.flat = uint32_t(std::max<int64_t>(

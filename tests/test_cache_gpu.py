@@ -361,6 +361,18 @@ def test_attend_many_rows(rows, T):
     check_attend(lens, rows, T, 1, 2, 256, seed=T + 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [16, 64])
+def test_attend_wide_heads_of_many_tiles(T, dtype):
+    """Heads of 256 in more than 1024 tiles of 16 rows, 32 of them to a workgroup."""
+    rng = np.random.default_rng(T)
+    rows = [int(x) for x in rng.integers(0, 17, 63)] + [17]
+    lens = [int(x) for x in rng.integers(-3, 200, 63)] + [1700]
+    lens[:4], rows[:4] = [0, 5, -5, 64], [3, 9, 1, 16]
+    check_attend(lens, rows, T, 4, 4, 256, dtype, seed=T)
+    check_attend(lens, rows, T, 4, 4, 256, dtype, seed=T + 1, bad_pages=5)
+
+
 def test_attend_rows_that_see_nothing():
     """No tokens, fewer tokens than rows, a negative length: 0 and -infinity."""
     got, lse = check_attend([0, 3, 0, 20, -5, 1], [2, 9, 0, 1, 1, 40], 16, 2, 2, 128, seed=3)
