@@ -98,7 +98,9 @@ __device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) 
 // requests, a tile of 1024 at a time, and serves its own range of rows and its
 // own share of new blocks by a search in the scanned sums.  The lengths are a
 // few KiB that every workgroup finds in the L2, so scanning them again costs
-// less than a second launch or a hand-off would.
+// less than a second launch or a hand-off would.  Bound by the chain lengths ->
+// scan -> search -> stores: 7.7 us for 64 requests of a token, 12.6 for 1000
+// prompts of 1 to 1200 tokens (a launch that does nothing: 3.6).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
   __shared__ int64_t s_tok[kPlanTile + 1], s_blk[kPlanTile + 1];
   __shared__ int32_t s_cached[kPlanTile];
@@ -374,142 +376,145 @@ __device__ __forceinline__ void store_item(const StoreArgs& A, float* s_max, int
   };
   Row8 x[kKeep ? P : 1][4];
   const float was = off ? *held : 0.0f;
-        // visit(p, rows) for the passes that hold places of the run, their rows
-        // loaded by then: all at once if they are kept, else one after the other.
-        auto each_pass = [&](bool loaded, auto&& visit) {
-          if constexpr (kKeep) {
-            if (!loaded) {
+  // visit(p, rows) for the passes that hold places of the run, their rows
+  // loaded by then: all at once if they are kept, else one after the other.
+  auto each_pass = [&](bool loaded, auto&& visit) {
+    if constexpr (kKeep) {
+      if (!loaded) {
 #pragma unroll
-              for (uint32_t p = 0; p < P; ++p)
-                if (base + kSpan * (p + 1) > off && base + kSpan * p < end) load_pass(p, x[p]);
-            }
+        for (uint32_t p = 0; p < P; ++p)
+          if (base + kSpan * (p + 1) > off && base + kSpan * p < end) load_pass(p, x[p]);
+      }
 #pragma unroll
-            for (uint32_t p = 0; p < P; ++p)
-              if (base + kSpan * (p + 1) > off && base + kSpan * p < end) visit(p, x[p]);
-          } else {
+      for (uint32_t p = 0; p < P; ++p)
+        if (base + kSpan * (p + 1) > off && base + kSpan * p < end) visit(p, x[p]);
+    } else {
 #pragma clang loop unroll(disable)
-            for (uint32_t p = 0; p < P; ++p) {
-              if (base + kSpan * (p + 1) <= off || base + kSpan * p >= end) continue;
-              load_pass(p, x[0]);
-              visit(p, x[0]);
-            }
-          }
-        };
-        uint8_t* codes = A.cache + (side ? A.s.value_at(block, h) : A.s.key_at(block, h));
-        float amax = 0.0f;
-        bool strange = false;  // some element is not finite
-        if constexpr (sizeof(E) == 2) {
-          // two magnitudes at a time by their bits; what is not finite is left
-          // out in a second look, if there is any
-          u16x2 top = {0, 0};
-          each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
+      for (uint32_t p = 0; p < P; ++p) {
+        if (base + kSpan * (p + 1) <= off || base + kSpan * p >= end) continue;
+        load_pass(p, x[0]);
+        visit(p, x[0]);
+      }
+    }
+  };
+  uint8_t* codes = A.cache + (side ? A.s.value_at(block, h) : A.s.key_at(block, h));
+  float amax = 0.0f;
+  bool strange = false;  // some element is not finite
+  if constexpr (sizeof(E) == 2) {
+    // two magnitudes at a time by their bits; what is not finite is left
+    // out in a second look, if there is any
+    u16x2 top = {0, 0};
+    each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
+      for (uint32_t i = 0; i < 4; ++i)
 #pragma unroll
-              for (uint32_t j = 0; j < 4; ++j) {
-                asm volatile("" : "+v"(y[i].w[j]));  // (kept as it came, not widened)
-                top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, y[i].w[j] & 0x7FFF7FFFu));
-              }
-          });
-          uint32_t most = max<uint32_t>(top[0], top[1]);
-          strange = __ballot(most >= infinity_bits<E>()) != 0;
-          if (strange) {
-            most = 0;
-            each_pass(true, [&](uint32_t, Row8 (&y)[4]) {
-#pragma unroll
-              for (uint32_t i = 0; i < 4; ++i)
-#pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) {
-                  const uint32_t w = y[i].w[j], lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
-                  if (lo < infinity_bits<E>()) most = max(most, lo);
-                  if (hi < infinity_bits<E>()) most = max(most, hi);
-                }
-            });
-          }
-          amax = static_cast<float>(__builtin_bit_cast(E, static_cast<uint16_t>(most)));
-        } else {
-          each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-#pragma unroll
-              for (uint32_t j = 0; j < 8; ++j) {
-                const float v = element<E>(y[i].w, j);
-                amax = fmaxf(amax, finite_abs(v));
-                strange |= !(fabsf(v) <= 3.402823466e38f);
-              }
-          });
-          strange = __ballot(strange) != 0;
+        for (uint32_t j = 0; j < 4; ++j) {
+          asm volatile("" : "+v"(y[i].w[j]));  // (kept as it came, not widened)
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, y[i].w[j] & 0x7FFF7FFFu));
         }
-        amax = wave_max(amax);
-        if constexpr (WV > 1) {
-          if (lane == 0) s_max[wave] = amax;
-          __syncthreads();
+    });
+    uint32_t most = max<uint32_t>(top[0], top[1]);
+    strange = __ballot(most >= infinity_bits<E>()) != 0;
+    if (strange) {
+      most = 0;
+      each_pass(true, [&](uint32_t, Row8 (&y)[4]) {
 #pragma unroll
-          for (uint32_t w = 0; w < WV; ++w) amax = fmaxf(amax, s_max[wave / WV * WV + w]);
-          __syncthreads();  // (also: every wave has read the old scale)
+        for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t w = y[i].w[j], lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+            if (lo < infinity_bits<E>()) most = max(most, lo);
+            if (hi < infinity_bits<E>()) most = max(most, hi);
+          }
+      });
+    }
+    amax = static_cast<float>(__builtin_bit_cast(E, static_cast<uint16_t>(most)));
+  } else {
+    each_pass(false, [&](uint32_t, Row8 (&y)[4]) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          const float v = element<E>(y[i].w, j);
+          amax = fmaxf(amax, finite_abs(v));
+          strange |= !(fabsf(v) <= 3.402823466e38f);
         }
-        float scale = scale_of(amax);
-        const bool grew = off && scale > was;
-        if (off && !grew) scale = was;
-        const float again = grew ? was * power_inverse(scale) : 1.0f;
+    });
+    strange = __ballot(strange) != 0;
+  }
+  amax = wave_max(amax);
+  if constexpr (WV > 1) {
+    if (lane == 0) s_max[wave] = amax;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t w = 0; w < WV; ++w) amax = fmaxf(amax, s_max[wave / WV * WV + w]);
+    __syncthreads();  // (also: every wave has read the old scale)
+  }
+  float scale = scale_of(amax);
+  const bool grew = off && scale > was;
+  if (off && !grew) scale = was;
+  const float again = grew ? was * power_inverse(scale) : 1.0f;
 #pragma clang loop unroll_count(kKeep ? P : 1)
-        for (uint32_t p = 0; p < P; ++p) {
-          if (base + kSpan * p >= end || (base + kSpan * (p + 1) <= off && !grew)) continue;
-          const uint32_t first = base + kSpan * p + 4 * tg;
-          if constexpr (!kKeep) load_pass(p, x[0]);
-          uint32_t lo[4], hi[4];  // the codes of dims 0 .. 3 and 4 .. 7 of each place
+  for (uint32_t p = 0; p < P; ++p) {
+    if (base + kSpan * p >= end || (base + kSpan * (p + 1) <= off && !grew)) continue;
+    const uint32_t first = base + kSpan * p + 4 * tg;
+    if constexpr (!kKeep) load_pass(p, x[0]);
+    uint32_t lo[4], hi[4];  // the codes of dims 0 .. 3 and 4 .. 7 of each place
 #pragma unroll
-          for (uint32_t i = 0; i < 4; ++i) {
-            const Row8& r = x[kKeep ? p : 0][i];
-            lo[i] = codes_of<E>(r.w, 0, scale);
-            hi[i] = codes_of<E>(r.w, 1, scale);
-            if (strange) {
-              lo[i] = with_nans<E>(lo[i], r.w, 0);
-              hi[i] = with_nans<E>(hi[i], r.w, 1);
-            }
-          }
-          if (!active) continue;
-          if (side == 0) {
+    for (uint32_t i = 0; i < 4; ++i) {
+      const Row8& r = x[kKeep ? p : 0][i];
+      lo[i] = codes_of<E>(r.w, 0, scale);
+      hi[i] = codes_of<E>(r.w, 1, scale);
+      if (strange) {
+        lo[i] = with_nans<E>(lo[i], r.w, 0);
+        hi[i] = with_nans<E>(hi[i], r.w, 1);
+      }
+    }
+    if (!active) continue;
+    if (side == 0) {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-              const uint32_t place = first + i;
-              uint8_t* c = codes + place * D + 8 * col;
-              if (place >= off && place < end) {
-                *reinterpret_cast<u32x2*>(c) = u32x2{lo[i], hi[i]};
-              } else if (place < off && grew) {
-                for (uint32_t j = 0; j < 8; ++j) c[j] = code_of(value_of(c[j]) * again);
-              }
-            }
-          } else if (first >= off && first + 4 <= end) {
-            // four places by eight dims to eight words of four places
-            uint32_t v[2][4];
-            transpose(lo, v[0]);
-            transpose(hi, v[1]);
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-              *reinterpret_cast<uint32_t*>(codes + (8 * col + j) * T + first) = v[j / 4][j % 4];
-          } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-              const uint32_t place = first + i;
-#pragma unroll
-              for (uint32_t j = 0; j < 8; ++j) {
-                uint8_t* c = codes + (8 * col + j) * T + place;
-                if (place >= off && place < end)
-                  *c = static_cast<uint8_t>((j < 4 ? lo[i] : hi[i]) >> (8 * (j % 4)));
-                else if (place < off && grew)
-                  *c = code_of(value_of(*c) * again);
-              }
-            }
-          }
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t place = first + i;
+        uint8_t* c = codes + place * D + 8 * col;
+        if (place >= off && place < end) {
+          *reinterpret_cast<u32x2*>(c) = u32x2{lo[i], hi[i]};
+        } else if (place < off && grew) {
+          for (uint32_t j = 0; j < 8; ++j) c[j] = code_of(value_of(c[j]) * again);
         }
+      }
+    } else if (first >= off && first + 4 <= end) {
+      // four places by eight dims to eight words of four places
+      uint32_t v[2][4];
+      transpose(lo, v[0]);
+      transpose(hi, v[1]);
+#pragma unroll
+      for (uint32_t j = 0; j < 8; ++j)
+        *reinterpret_cast<uint32_t*>(codes + (8 * col + j) * T + first) = v[j / 4][j % 4];
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t place = first + i;
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          uint8_t* c = codes + (8 * col + j) * T + place;
+          if (place >= off && place < end)
+            *c = static_cast<uint8_t>((j < 4 ? lo[i] : hi[i]) >> (8 * (j % 4)));
+          else if (place < off && grew)
+            *c = code_of(value_of(*c) * again);
+        }
+      }
+    }
+  }
   if (lane == 0 && wave % WV == 0) *held = scale;
 }
 
 // A workgroup looks after the runs that begin in its tile of rows, for its
 // heads.  Runs that take more than one pass are done one after the other by all
 // waves, a pass each, and keep many loads in flight; shorter ones, such as a
-// decode step's single tokens, go to a wave each.
+// decode step's single tokens, go to a wave each.  161 MB read and written for
+// 26k tokens of 29 prompts take 45 us (3.6 TB/s; a copy 32): a workgroup waits
+// for its slots, then its rows, then the largest magnitude.  Asking for the next
+// item's rows ahead changed nothing, other orders of heads and rows 47 to 55.
 template <typename E, int D, int T>
 __global__ void __launch_bounds__(kStoreWaves * 64) store_kernel(StoreArgs A) {
   constexpr uint32_t kSpan = 4 * store_groups(D, T), kPasses = T / kSpan;
@@ -746,7 +751,9 @@ struct Values {
   }
 };
 
-// Workgroups a CU is to hold: bounds the registers of a lane.
+// Workgroups a CU is to hold: bounds the registers of a lane (four waves of 512
+// / this).  Two with two tiles of 128 measured 107 us where one took 151 (chunks of
+// 8 requests); three with one tile of 128 were no faster.
 constexpr int attend_resident(int d, int nr) {
   return nr == 2 ? (d <= 128 ? 2 : 1) : d == 64 ? 3 : d <= 192 ? 2 : 1;
 }
@@ -900,9 +907,11 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 
 // Row i of a request and key/value head is query row i / group, head i %
 // group of the group.  A workgroup computes NR tiles of 16 rows of one request
-// and key/value head over one split of the tokens: its waves take chunks of 64
-// tokens in turn, each with a running maximum m, sum l and accumulator of its
-// own, and join them at the end.
+// and key/value head over a range of the tokens: its waves take chunks of 64
+// tokens in turn, each with a reference m, which the running maximum may pass
+// by 8, a sum l and an accumulator of its own, and join them at the end:
+//   p_t = 2^(s_t - m), l = sum p_t, acc = sum p_t v_t, out = acc / l,
+// the scores s_t in units of log 2.
 //
 // Both products run on the 16x16x32 matrix instruction with the cache's codes
 // as the left operand, straight from the loads: no shared memory, no
@@ -922,9 +931,20 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // range.  Rounding them is off by up to 2^-8 of each weight, at random; that is
 // below the output's own rounding for bfloat16 queries.  For float16 it would
 // be above, so there a weight goes in two parts, the rounded one and the
-// rounded rest (off by 2^-16), at one more product each.
+// rounded rest (off by 2^-16), at one more product each.  The codes are widened
+// although there are matrix instructions for 8 bits: those align a sum's
+// products to the largest with about 13 bits, which on random wide exponents
+// was off by 2^-12.5 of the sum of magnitudes (bfloat16's form 2.5 x 2^-24).
+//
+// What bounds it: memory where there are few rows (64 requests of 500 .. 8000
+// tokens, 8 heads of 128, group 4: 360 MB in 80 us, 4.5 TB/s; 2 of 65k .. 131k,
+// group 8: 402 MB in 82 us, 4.9 TB/s; a read alone reaches 6.3), each piece's
+// first trip to memory and the join making up the rest; the instructions that
+// widen, weigh and rescale where there are many (8 requests with up to 600 rows
+// each after up to 5000 tokens: 34.5 GFLOP in 97 us, 356 TFLOP/s); the chain
+// table -> codes -> products for short ones (300 tokens: 9 us).
 template <int D, int NR>
-struct AttendShared {
+struct AttendShared {  // 19 to 84 KiB
   u32x4 q[NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
   float acc[kAttendWaves][16][D + 4];
   float m[kAttendWaves][NR * 16], l[kAttendWaves][NR * 16];
@@ -1210,7 +1230,8 @@ constexpr int kJoinThreads = 256;
 // Joins the sums of the tiles that several workgroups shared: workgroup (w, h)
 // that of the tile which share w begins and later ones go on with, D / 4
 // threads for a row, the shares in order, so the result does not depend on
-// when they were done.
+// when they were done.  Bound by latency: 4.6 us behind 64 requests' decode
+// step, 9.4 where 2 long ones are spread over 512 workgroups, 6.8 for chunks.
 template <typename E, int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
   constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide, kRows = NR * 16;
