@@ -425,7 +425,9 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * sum of -infinity.  Tokens whose table entry lies outside the cache, and
  * those past the table's width, are left out; what the cache holds behind a
  * request's last token is not read into any result.  Rows of no request
- * (behind the last, or before starts[0]) are left as they were.
+ * (behind the last, or before starts[0]) are left as they were.  out and lse
+ * must not overlap what the call reads (query and out may be read and written
+ * in any order).
  * lse (or NULL): [rows][heads], the log of each row's sum of
  * exp(scale * q k^T), with which results over parts of a context are joined.
  * max_query, max_length: the largest number of query rows and of tokens of a

@@ -234,7 +234,8 @@ class PagedCache:
         table: int32 [batch, width].  scale: 1 / sqrt(head_dim) if None.
         max_query, max_length: the batch's largest number of rows and of
         tokens, where known; they shape the launch only.  Rows of no request
-        are left as they were (without `out`: undefined)."""
+        are left as they were (without `out`: undefined).  out must not share
+        memory with query."""
         kinds = _kinds()
         _tensor(query, "attend: query", kinds, 3, self.device)
         rows, heads, d = query.shape

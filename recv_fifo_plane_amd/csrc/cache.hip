@@ -99,7 +99,7 @@ __device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) 
 // own share of new blocks by a search in the scanned sums.  The lengths are a
 // few KiB that every workgroup finds in the L2, so scanning them again costs
 // less than a second launch or a hand-off would.  Bound by the chain lengths ->
-// scan -> search -> stores: 7.7 us for 64 requests of a token, 12.6 for 1000
+// scan -> search -> stores: 6 to 8 us for 64 requests of a token, 11 to 13 for 1000
 // prompts of 1 to 1200 tokens (a launch that does nothing: 3.6).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
   __shared__ int64_t s_tok[kPlanTile + 1], s_blk[kPlanTile + 1];
