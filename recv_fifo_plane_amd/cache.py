@@ -96,9 +96,18 @@ def _rows(t, what, dtypes, device, rows, heads, dim):
     return t.data_ptr(), row, head
 
 
+def _on(stream, device):
+    """Refuses a stream object of another device (a handle does not tell)."""
+    own = getattr(stream, "device", None)
+    if own is not None and own.index != device:
+        raise ValueError("stream is of %s, the tensors are on cuda:%d" % (own, device))
+
+
 def _call(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current."""
     import torch
+    if stream is not None:
+        _on(stream, device)
     if device == torch.cuda.current_device():
         rc = fn(*args, _RAW(device) or None if stream is None and _RAW else X._stream_handle(stream))
     else:
@@ -108,17 +117,36 @@ def _call(device, stream, fn, *args):
         X.check(rc)
 
 
-def _keep(stream, *tensors):
-    """Tensors made here and used on another stream than the current one stay
-    reserved until that stream has passed the call."""
+def _side(stream, device):
+    """The stream that a call launches on, None where it is the current one of
+    `device`.  A handle is one of a stream of `device`."""
     if stream is None:
-        return
+        return None
     import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    if stream != torch.cuda.current_stream():
-        for t in tensors:
-            t.record_stream(stream)
+    _on(stream, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = X._stream_handle(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    return None if stream == torch.cuda.current_stream(device) else stream
+
+
+def _empty(like, shape, dtype, side, result=True):
+    """A new tensor that a launch on the stream `side` (None: the current one) writes.
+
+    It comes from that stream's pool: the current stream's could hold memory
+    that was freed there while kernels still queued use it, and a launch on
+    another stream does not wait for those.  A result, which the caller goes on
+    to use on the current stream, stays reserved for that one too."""
+    if side is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    here = torch.cuda.current_stream(like.device.index)
+    with torch.cuda.stream(side):
+        t = like.new_empty(shape, dtype=dtype)
+    if result:
+        t.record_stream(here)
+    return t
 
 
 def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=None,
@@ -141,8 +169,7 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
         raise ValueError("plan_blocks: rows must not be negative")
     sizes = (rows, rows, batch + 1, batch, 2)
     if out is None:
-        buf = cached.new_empty(sum(sizes))
-        _keep(stream, buf)
+        buf = _empty(cached, sum(sizes), _INT32, _side(stream, dev))
         out = BlockPlan(*buf.split_with_sizes(sizes))
         slots = buf.data_ptr()
         positions = slots + 4 * rows
@@ -248,14 +275,13 @@ class PagedCache:
         batch = lengths.shape[0]
         at_starts = _list(starts, "attend: starts", batch + 1, self.device)
         at_table, stride, width = _table(table, "attend: table", batch, self.device)
+        side = _side(stream, self.device)
         if out is None:
-            out = query.new_empty((rows, heads, d))
-            _keep(stream, out)
+            out = _empty(query, (rows, heads, d), dtype, side)
         o, o_row, o_head = _rows(out, "attend: out", (dtype,), self.device, rows, heads, d)
         sums = None
         if lse is True:
-            sums = query.new_empty((rows, heads), dtype=_FLOAT32)
-            _keep(stream, sums)
+            sums = _empty(query, (rows, heads), _FLOAT32, side)
         elif lse is not False and lse is not None:
             sums = _tensor(lse, "attend: lse", (_FLOAT32,), 2, self.device)
             if tuple(sums.shape) != (rows, heads) or not sums.is_contiguous():
@@ -270,8 +296,7 @@ class PagedCache:
         if rc:
             X.check(rc)
         if n.value:
-            work = query.new_empty(n.value, dtype=_UINT8)
-            _keep(stream, work)
+            work = _empty(query, n.value, _UINT8, side, result=False)
             a.workspace, a.workspace_bytes = work.data_ptr(), n.value
         _call(self.device, stream, lib.xfer_cache_attend, self._ref, self._base, ref)
         return out if sums is None else (out, sums)
