@@ -436,8 +436,8 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * workspace: device memory of xfer_cache_attend_workspace() bytes for these
  * arguments, 16-byte aligned, used by this call alone until it has run.
  * Scores, sums and outputs are accumulated in float; before they multiply the
- * values, the weights exp(...) are rounded to bfloat16 (for FP16 queries to the
- * sum of two bfloat16 numbers).
+ * values, the weights exp(...) are rounded to the sum of two bfloat16 numbers
+ * (off by 2^-16 of the weight at most).
  * Errors: INVALID_ARG (sizes outside their domains: batch * H below 2^24, rows *
  * heads below 2^31; NULL or misaligned buffers, too small a workspace), HIP. */
 typedef struct {

@@ -815,7 +815,7 @@ __device__ __forceinline__ f32x4 seen_nans(const AttendArgs& A, const int32_t* t
 
 // The weights of a chunk's scores and their product with the values.  MASK:
 // some row does not see some token of the chunk.
-template <bool MASK, bool TWO, int DT, int NR>
+template <bool MASK, int DT, int NR>
 __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f32x4 (&acc)[NR][DT],
                                       float (&m)[NR], float (&l)[NR], const u32x4 (&vc)[DT],
                                       const int32_t (&limit)[NR], float mul, float vs,
@@ -852,8 +852,7 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
         sum += w;
         const bf16_t first = static_cast<bf16_t>(w);
         p[x][t >> 1][(t & 1) * 4 + r] = first;
-        if constexpr (TWO)
-          p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
+        p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
       }
     l[x] = l[x] * keep + sum;
     if (__ballot(grows) != 0) {
@@ -897,10 +896,8 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
     for (int x = 0; x < NR; ++x) {
       acc[x][e] = mfma(a, p[x][0], acc[x][e]);
       acc[x][e] = mfma(z, p[x][1], acc[x][e]);
-      if constexpr (TWO) {
-        acc[x][e] = mfma(a, p2[x][0], acc[x][e]);
-        acc[x][e] = mfma(z, p2[x][1], acc[x][e]);
-      }
+      acc[x][e] = mfma(a, p2[x][0], acc[x][e]);
+      acc[x][e] = mfma(z, p2[x][1], acc[x][e]);
     }
   }
 }
@@ -927,10 +924,10 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // goes into the scores' multiplier, the value scale into the widening of the
 // codes to bfloat16, where both are exact.
 //
-// Weights are bfloat16 whatever the query's type: code times scale needs its
-// range.  Rounding them is off by up to 2^-8 of each weight, at random; that is
-// below the output's own rounding for bfloat16 queries.  For float16 it would
-// be above, so there a weight goes in two parts, the rounded one and the
+// Weights multiply the values as bfloat16 whatever the query's type: code times
+// scale needs its range.  One such number would be off by up to 2^-8 of the
+// weight, which shows beside the output's own rounding (and is far above it
+// where values cancel), so a weight goes in two parts, the rounded one and the
 // rounded rest (off by 2^-16), at one more product each.  The codes are widened
 // although there are matrix instructions for 8 bits: those align a sum's
 // products to the largest with about 13 bits, which on random wide exponents
@@ -941,7 +938,8 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // group 8: 402 MB in 82 us, 4.9 TB/s; a read alone reaches 6.3), each piece's
 // first trip to memory and the join making up the rest; the instructions that
 // widen, weigh and rescale where there are many (8 requests with up to 600 rows
-// each after up to 5000 tokens: 34.5 GFLOP in 97 us, 356 TFLOP/s); the chain
+// each after up to 5000 tokens: 34.5 GFLOP in 107 us, 322 TFLOP/s, of which the
+// weights' second parts take 10 us); the chain
 // table -> codes -> products for short ones (300 tokens: 9 us).
 template <int D, int NR>
 struct AttendShared {  // 19 to 84 KiB
@@ -960,7 +958,6 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
   typedef typename Vec8<E>::type E8;
   constexpr int KL = D / 32;  // steps of 32 dims
   constexpr int DT = D / 16;  // tiles of dims
-  constexpr bool kTwo = __is_same(E, fp16_t);  // weights in two parts
   const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
   const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
@@ -1065,8 +1062,8 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
       __builtin_amdgcn_sched_barrier(0);
       // (the scales of a block that is not the request's: anything)
       const float ks = bg < 0 ? 1.0f : vals.key_scale, vs = bg < 0 ? 1.0f : vals.value_scale;
-      weigh<decltype(masked)::value, kTwo, DT, NR>(A, s, acc, m, l, vals.w, limit, ks * A.scale2, vs,
-                                                   seen_all, tg, bg, nans);
+      weigh<decltype(masked)::value, DT, NR>(A, s, acc, m, l, vals.w, limit, ks * A.scale2, vs,
+                                             seen_all, tg, bg, nans);
       __builtin_amdgcn_sched_barrier(0);
       at = next;
       next.look(A, table, ahead + kNext, seen_all, g, n);
