@@ -13,14 +13,20 @@ def two_part_bounds(ref, tokens, D, out_eps):
     As R.attend_bounds, but for the weights: bfloat16 holds 8 significant bits,
     so the first number is off by 2^-8 of the weight at most; what is left is
     exact in float (a difference of close numbers), and the second number is off
-    by 2^-8 of it: 2^-16 of the weight."""
+    by 2^-8 of it: 2^-16 of the weight.
+
+    An output below the type's normal numbers is rounded to a step that does not
+    shrink with it: float16's numbers below 2^-14 are 2^-24 apart, so half a
+    step is 2^-25 there, which 2^-11 of the output is less than (of -1.2148e-6,
+    nearest float16 number -1.1921e-6: off by 2.27e-8, 2^-11 of it 5.9e-10).
+    bfloat16's are 2^-133 apart, far below the 1e-30 allowed in any case."""
     out, lse, mag, big = ref
     u = 2.0 ** -24
     eta = 1.01 * ((D + 9) * u * big + 4 * u)
     n = 2 * tokens + 64
     tol_out = out_eps * np.abs(out) + (WEIGHT * 1.01 + 2 * eta[..., None] + 2 * n * u) * mag
     tol_lse = eta + n * u + 4 * u * (1 + np.abs(np.where(np.isfinite(lse), lse, 0.0)))
-    return tol_out * 1.01 + 1e-30, tol_lse
+    return tol_out * 1.01 + (2.0 ** -25 if out_eps == 2.0 ** -11 else 1e-30), tol_lse
 
 
 def cancelling_pairs(cache):
