@@ -348,7 +348,7 @@ class Conn:
         if ns != nd:
             raise ValueError("run_blocks: %d source ids for %d destination ids" % (ns, nd))
         for x, w in ((src_ids, "src_ids"), (dst_ids, "dst_ids")):
-            if hasattr(x, "dtype") and not str(x.dtype).endswith("int32"):
+            if hasattr(x, "dtype") and str(x.dtype) != "torch.int32":
                 raise TypeError("run_blocks: %s must be int32, got %s" % (w, x.dtype))
         s = _buf(src, sb * size, self.device, "run_blocks: src")
         d = _buf(dst, db * size, self.device, "run_blocks: dst")
