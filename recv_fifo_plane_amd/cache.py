@@ -28,14 +28,16 @@ HEAD_DIMS = (64, 96, 128, 192, 256)
 
 _KINDS = {}  # torch dtypes of rows to xfer_dtype, filled at the first call
 _INT32 = _FLOAT32 = _UINT8 = None
+_GRAD = None  # whether gradients are being recorded
 _RAW = None  # the current stream's handle of a device, where torch gives it without an object
 
 
 def _kinds():
-    global _INT32, _FLOAT32, _UINT8, _RAW
+    global _INT32, _FLOAT32, _UINT8, _RAW, _GRAD
     if not _KINDS:
         import torch
         _INT32, _FLOAT32, _UINT8 = torch.int32, torch.float32, torch.uint8
+        _GRAD = torch.is_grad_enabled
         _RAW = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _KINDS.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     return _KINDS
@@ -101,6 +103,13 @@ def _on(stream, device):
     own = getattr(stream, "device", None)
     if own is not None and own.index != device:
         raise ValueError("stream is of %s, the tensors are on cuda:%d" % (own, device))
+
+
+def _no_grad(t, what):
+    """Refuses a tensor whose gradient would be lost."""
+    if getattr(t, "requires_grad", False) and _GRAD():
+        raise ValueError("%s: there is no gradient of attention over the cache; call it under "
+                         "torch.no_grad() or with a detached tensor" % what)
 
 
 def _call(device, stream, fn, *args):
@@ -262,9 +271,11 @@ class PagedCache:
         max_query, max_length: the batch's largest number of rows and of
         tokens, where known; they shape the launch only.  Rows of no request
         are left as they were (without `out`: undefined).  out must not share
-        memory with query."""
+        memory with query.  There is no gradient: where one is being recorded,
+        a query or out that requires it is refused."""
         kinds = _kinds()
         _tensor(query, "attend: query", kinds, 3, self.device)
+        _no_grad(query, "attend: query")
         rows, heads, d = query.shape
         dtype = query.dtype
         if kinds[dtype] == 2:
@@ -278,6 +289,7 @@ class PagedCache:
         side = _side(stream, self.device)
         if out is None:
             out = _empty(query, (rows, heads, d), dtype, side)
+        _no_grad(out, "attend: out")
         o, o_row, o_head = _rows(out, "attend: out", (dtype,), self.device, rows, heads, d)
         sums = None
         if lse is True:

@@ -31,3 +31,40 @@ def test_block_lists_are_int32(cache, which, dtype):
             conn.run_blocks(*pools, 4096, *ids)
     finally:
         conn._h = None
+
+
+BF = torch.bfloat16
+
+
+def attend_args(**query):
+    q = FakeTensor((4, 4, 128), BF)
+    q.__dict__.update(query)
+    return q, FakeTensor((3, 8)), FakeTensor((3,)), FakeTensor((4,))
+
+
+class Launched(Exception):
+    pass
+
+
+def launches(monkeypatch):
+    class Library:
+        def __getattr__(self, name):
+            raise Launched(name)
+    monkeypatch.setattr(X, "_lib", Library())
+
+
+def test_attend_has_no_gradient(cache, monkeypatch):
+    """A query (or out) that asks for a gradient gets an error, not a result without
+    one; under no_grad it is computed."""
+    out = FakeTensor((4, 4, 128), BF)
+    with pytest.raises(ValueError, match="gradient"):
+        cache.attend(*attend_args(requires_grad=True), out=out)
+    out.requires_grad = True
+    with pytest.raises(ValueError, match="gradient"):
+        cache.attend(*attend_args(), out=out)
+    launches(monkeypatch)
+    for context in (torch.no_grad, torch.inference_mode):
+        with context(), pytest.raises(Launched):
+            cache.attend(*attend_args(requires_grad=True), out=out)
+    with pytest.raises(Launched):
+        cache.attend(*attend_args(requires_grad=False), out=FakeTensor((4, 4, 128), BF))
