@@ -427,7 +427,7 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * request's last token is not read into any result.  Rows of no request
  * (behind the last, or before starts[0]) are left as they were.  out and lse
  * must not overlap what the call reads (query and out may be read and written
- * in any order).
+ * in any order), nor the rows and heads of out each other.
  * lse (or NULL): [rows][heads], the log of each row's sum of
  * exp(scale * q k^T), with which results over parts of a context are joined.
  * max_query, max_length: the largest number of query rows and of tokens of a
@@ -439,7 +439,8 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * values, the weights exp(...) are rounded to the sum of two bfloat16 numbers
  * (off by 2^-16 of the weight at most).
  * Errors: INVALID_ARG (sizes outside their domains: batch * H below 2^24, rows *
- * heads below 2^31; NULL or misaligned buffers, too small a workspace), HIP. */
+ * heads below 2^31; NULL or misaligned buffers, strides of out that let its rows
+ * or heads overlap, too small a workspace), HIP. */
 typedef struct {
   const void* query; /* [rows][heads][D], dtype BF16 or FP16 */
   void* out;         /* [rows][heads][D], same dtype */

@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <string>
 #include <type_traits>
+#include <utility>
 
 #include "xfer.h"
 
@@ -1398,6 +1399,20 @@ int shape_of(const xfer_cache_shape* g, const char* who, Shape* out) {
   return XFER_OK;
 }
 
+// Whether vectors of `inner` elements, n0 times n1 of them with strides s0 and s1,
+// may share elements: they do not where the vectors of one dimension follow one
+// another and those of the other lie behind them all.
+bool vectors_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
+  typedef __int128 wide;
+  wide a = s0 < 0 ? -wide(s0) : wide(s0), b = s1 < 0 ? -wide(s1) : wide(s1);
+  if (n0 <= 1 || (n1 > 1 && a > b)) {
+    std::swap(n0, n1);
+    std::swap(a, b);
+  }
+  if (n0 <= 1) return false;
+  return a < inner || (n1 > 1 && b < a * (n0 - 1) + inner);
+}
+
 bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 }  // namespace
@@ -1545,6 +1560,9 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
       !aligned(q->table, 4) || !aligned(q->lengths, 4) || !aligned(q->starts, 4))
     return fail(XFER_ERR_INVALID_ARG,
                 "xfer_cache_attend: the cache must be 16-byte aligned, the others by their type");
+  if (vectors_overlap(q->rows, q->out_row, q->heads, q->out_head, a.s.D))
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_cache_attend: the rows and heads of out must not overlap");
   a.cache = static_cast<const uint8_t*>(cache);
   a.query = q->query;
   a.out = q->out;

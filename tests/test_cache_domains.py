@@ -1,10 +1,13 @@
 """CPU tests of refusals: calls that the cache's operators would answer wrongly
 without a word."""
+import ctypes as C
+
 import pytest
 import torch
 
 import cache_ref as R
 import recv_fifo_plane_amd as xf
+from recv_fifo_plane_amd import cache as K
 from recv_fifo_plane_amd import xfer as X
 from test_cache_refusals import FakeTensor, Unreachable
 
@@ -68,3 +71,43 @@ def test_attend_has_no_gradient(cache, monkeypatch):
             cache.attend(*attend_args(requires_grad=True), out=out)
     with pytest.raises(Launched):
         cache.attend(*attend_args(requires_grad=False), out=FakeTensor((4, 4, 128), BF))
+
+
+OVERLAPPING = [  # strides of a row and of a head, rows, heads: elements that two rows would write
+    (0, 128, 4, 4), (256, 128, 4, 4), (512, 64, 4, 4), (512, 0, 4, 4), (64, 512, 4, 4), (128, 256, 4, 4),
+    (-256, 128, 4, 4), (512, -64, 4, 4), (127, 128, 4, 1), (1, 1, 2, 1), (384, 127, 1, 4),
+    (1 << 62, 1 << 62, 4, 4), (-(1 << 63), 100, 4, 4)]
+APART = [  # and those that write each element once
+    (512, 128, 4, 4), (128, 512, 4, 4), (520, 130, 4, 4), (-512, 128, 4, 4), (512, -128, 4, 4),
+    (0, 128, 1, 4), (128, 0, 4, 1), (0, 0, 1, 1), (1 << 40, 1 << 50, 4, 4), (-(1 << 63), 128, 4, 4)]
+
+
+def raw_attend(row, head, rows, heads, **kw):
+    p = 1 << 40
+    a = X.xfer_attend(p, p, None, p, p, p, None, 0, 512, 128, row, head, 1, 1, rows, heads, 1, 0, 1.0, 0, 0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return X.lib().xfer_cache_attend(C.byref(X.xfer_cache_shape(16, 1, 128, 10)), p, C.byref(a), None)
+
+
+@pytest.mark.parametrize("row,head,rows,heads", OVERLAPPING)
+def test_attend_refuses_overlapping_outputs(row, head, rows, heads):
+    assert raw_attend(row, head, rows, heads) == X.XFER_ERR_INVALID_ARG
+    assert "overlap" in xf.last_error()
+
+
+@pytest.mark.parametrize("row,head,rows,heads", APART)
+def test_attend_takes_outputs_that_do_not_overlap(row, head, rows, heads):
+    """(refused for the workspace, which is looked at behind the strides)"""
+    assert raw_attend(row, head, rows, heads, workspace_bytes=0, table_width=1 << 20,
+                      table_stride=1 << 20) == X.XFER_ERR_INVALID_ARG
+    assert "workspace" in xf.last_error()
+
+
+def test_attend_refuses_an_expanded_out(monkeypatch):
+    c = xf.PagedCache(10, 16, 2, 128, buffer=FakeTensor((10, R.block_bytes(16, 2, 128)), torch.uint8))
+    K._kinds()
+    monkeypatch.setattr(K, "_RAW", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(xf.XferError, match="overlap"):
+        c.attend(*attend_args(), out=FakeTensor((4, 4, 128), BF, strides=(0, 128, 1)))
