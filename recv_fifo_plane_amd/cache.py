@@ -43,6 +43,16 @@ def _kinds():
     return _KINDS
 
 
+_MOST = 0x7FFFFFFF  # the library's sizes are C ints, which would drop what lies above
+
+
+def _int(v, what):
+    v = int(v)
+    if not -_MOST - 1 <= v <= _MOST:
+        raise ValueError("%s: %d is not within 2^31" % (what, v))
+    return v
+
+
 def _tensor(t, what, dtypes, ndim, device):
     """A GPU tensor of one of `dtypes` with `ndim` dimensions on `device` (None: any)."""
     if not hasattr(t, "data_ptr"):
@@ -62,7 +72,8 @@ def _list(t, what, n, device):
     """Address of a contiguous int32 tensor of n entries (None: any number)."""
     try:  # the usual case, in few calls
         if (t.dtype is _INT32 and t.is_cuda and (device is None or t.get_device() == device)
-                and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n)):
+                and t.dim() == 1 and t.is_contiguous() and (n is None or t.shape[0] == n)
+                and t.shape[0] <= _MOST):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -70,6 +81,7 @@ def _list(t, what, n, device):
     have = t.shape[0]
     if n is not None and have != n:
         raise ValueError("%s: expected %d entries, got %d" % (what, n, have))
+    _int(have, what)
     raise ValueError("%s: tensor is not contiguous" % what)
 
 
@@ -80,6 +92,7 @@ def _table(t, what, batch, device):
     have, width = t.shape
     if have != batch:
         raise ValueError("%s: expected %d rows, got %d" % (what, batch, have))
+    _int(width, what)
     stride = t.stride(0) if batch > 1 else width
     if (width > 1 and t.stride(1) != 1) or stride < width:
         raise ValueError("%s: rows must be contiguous and not overlap" % what)
@@ -173,7 +186,7 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
     at_added = _list(added, "plan_blocks: added", batch, dev)
     at_table, stride, width = _table(table, "plan_blocks: table", batch, dev)
     at_free = _list(free, "plan_blocks: free", None, dev)
-    rows = int(rows)
+    block_tokens, rows = _int(block_tokens, "plan_blocks: block_tokens"), _int(rows, "plan_blocks: rows")
     if rows < 0:
         raise ValueError("plan_blocks: rows must not be negative")
     sizes = (rows, rows, batch + 1, batch, 2)
@@ -189,7 +202,7 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
         slots, positions, starts, lengths, counts = (
             _list(t, "plan_blocks: out", n, dev) for t, n in zip(out, sizes))
     _call(dev, stream, X.lib().xfer_cache_plan, at_cached, at_added, batch, at_table, stride, width,
-          at_free, free.shape[0], int(block_tokens), slots, positions, rows, starts, lengths,
+          at_free, free.shape[0], block_tokens, slots, positions, rows, starts, lengths,
           counts)
     return out
 
@@ -201,8 +214,10 @@ class PagedCache:
                  buffer=None):
         """buffer: a contiguous uint8 tensor [blocks, block_bytes] to use, else zeros."""
         import torch
-        self.blocks, self.block_tokens = int(blocks), int(block_tokens)
-        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+        self.blocks, self.block_tokens, self.kv_heads, self.head_dim = (
+            _int(v, "PagedCache: " + what) for v, what in
+            ((blocks, "blocks"), (block_tokens, "block_tokens"), (kv_heads, "kv_heads"),
+             (head_dim, "head_dim")))
         self._shape = X.xfer_cache_shape(self.block_tokens, self.kv_heads, self.head_dim,
                                          self.blocks)
         n = C.c_size_t()
@@ -286,6 +301,7 @@ class PagedCache:
         batch = lengths.shape[0]
         at_starts = _list(starts, "attend: starts", batch + 1, self.device)
         at_table, stride, width = _table(table, "attend: table", batch, self.device)
+        max_query, max_length = _int(max_query, "attend: max_query"), _int(max_length, "attend: max_length")
         side = _side(stream, self.device)
         if out is None:
             out = _empty(query, (rows, heads, d), dtype, side)
@@ -301,8 +317,8 @@ class PagedCache:
         a = X.xfer_attend(q, o, None if sums is None else sums.data_ptr(), at_table, at_lengths,
                           at_starts, None, 0, q_row, q_head, o_row, o_head, stride, batch, rows,
                           heads, width, kinds[dtype],
-                          1.0 / math.sqrt(d) if scale is None else float(scale), int(max_query),
-                          int(max_length))
+                          1.0 / math.sqrt(d) if scale is None else float(scale), max_query,
+                          max_length)
         n, ref, lib = C.c_size_t(), C.byref(a), X.lib()
         rc = lib.xfer_cache_attend_workspace(self._ref, ref, C.byref(n))
         if rc:

@@ -111,3 +111,42 @@ def test_attend_refuses_an_expanded_out(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(xf.XferError, match="overlap"):
         c.attend(*attend_args(), out=FakeTensor((4, 4, 128), BF, strides=(0, 128, 1)))
+
+
+BIG = 1 << 32  # what a C int drops
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_sizes_of_a_cache_beyond_an_int(i):
+    sizes = [10, 16, 2, 128]
+    sizes[i] += BIG
+    with pytest.raises(ValueError, match="2\\^31"):
+        xf.PagedCache(*sizes, buffer=FakeTensor((sizes[0], R.block_bytes(16, 2, 128)), torch.uint8))
+
+
+@pytest.mark.parametrize("block,rows", [(BIG + 16, 20), (16, BIG + 20), (16, (1 << 31) + 20)])
+def test_sizes_of_a_plan_beyond_an_int(cache, block, rows):
+    out = xf.BlockPlan(*(FakeTensor((n,)) for n in (rows, rows, 4, 3, 2)))
+    with pytest.raises(ValueError, match="2\\^31"):
+        K.plan_blocks(FakeTensor((3,)), FakeTensor((3,)), FakeTensor((3, 8)), FakeTensor((5,)), block, rows,
+                      out=out)
+
+
+@pytest.mark.parametrize("free,width", [(BIG + 5, 8), (5, BIG + 8)])
+def test_lists_of_a_plan_beyond_an_int(cache, free, width):
+    out = xf.BlockPlan(*(FakeTensor((n,)) for n in (20, 20, 4, 3, 2)))
+    with pytest.raises(ValueError, match="2\\^31"):
+        K.plan_blocks(FakeTensor((3,)), FakeTensor((3,)), FakeTensor((3, width)), FakeTensor((free,)), 16, 20,
+                      out=out)
+
+
+@pytest.mark.parametrize("kw", [dict(max_query=BIG), dict(max_length=BIG + 5), dict(max_length=1 << 31)])
+def test_hints_beyond_an_int(cache, kw):
+    with pytest.raises(ValueError, match="2\\^31"):
+        cache.attend(*attend_args(), out=FakeTensor((4, 4, 128), BF), **kw)
+
+
+def test_rows_of_a_store_beyond_an_int(cache):
+    rows = FakeTensor((BIG + 4, 2, 128), BF, strides=(0, 128, 1))
+    with pytest.raises(ValueError, match="2\\^31"):
+        cache.store(rows, rows, FakeTensor((BIG + 4,)))
