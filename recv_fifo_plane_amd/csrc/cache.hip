@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * A.per_wg;
   const int64_t row1 = min<int64_t>(A.rows, row0 + A.per_wg);
   int64_t carry_tok = 0, carry_blk = 0, lost = 0;
-  for (int b0 = 0; b0 < A.batch; b0 += kPlanTile) {
-    const int cnt = min(kPlanTile, A.batch - b0);
+  for (int64_t b0 = 0; b0 < A.batch; b0 += kPlanTile) {
+    const int cnt = static_cast<int>(min<int64_t>(kPlanTile, A.batch - b0));
     int64_t tok[kPlanEach], blk[kPlanEach], sum_tok = 0, sum_blk = 0;
 #pragma unroll
     for (int i = 0; i < kPlanEach; ++i) {
@@ -1454,8 +1454,10 @@ extern "C" int xfer_cache_plan(const int32_t* cached, const int32_t* added, int 
   PlanArgs a{cached, added,  table,  free_blocks,  slots, positions,   starts, lengths,
              counts, table_stride, batch, table_width, nfree, block_tokens, rows,  0};
   // About 1024 rows or 256 requests a workgroup.
-  const int grid = std::max(1, std::min(1024, std::max((rows + 1023) / 1024, (batch + 255) / 256)));
-  a.per_wg = (rows + grid - 1) / grid;
+  // (in 64 bits: rows and batch may be 2^31 - 1)
+  const int64_t grid = std::max<int64_t>(
+      1, std::min<int64_t>(1024, std::max((int64_t(rows) + 1023) / 1024, (int64_t(batch) + 255) / 256)));
+  a.per_wg = int32_t((rows + grid - 1) / grid);
   const hipError_t e =
       launch(plan_kernel, a, dim3(uint32_t(grid)), kPlanThreads, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "xfer_cache_plan launch");
