@@ -385,11 +385,15 @@ int xfer_cache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
  * The added tokens of all requests, in order, are the packed rows:
  *   starts[batch + 1]   first row of each request, then their number
  *   lengths[batch]      cached + added
- *   slots[rows]         slot of each row's token; -1 where no block was left
- *                       or the table is too narrow, and behind the last row
+ *   slots[rows]         slot of each row's token; -1 where no block was left,
+ *                       the table is too narrow or lacks the block that the
+ *                       request's last token is in (a negative entry), and
+ *                       behind the last row
  *   positions[rows]     the token's place in its request; -1 behind the last
  *   counts[2]           new blocks the requests need (more than nfree: some
- *                       got none), and tokens that they leave without a slot
+ *                       got none), and added tokens without a slot
+ * The ids in free_blocks are blocks of the pool: a negative one (a padded
+ * list's) gives its tokens no slot either, but counts[1] leaves those out.
  * Entries of the table outside the new blocks stay as they are.  rows may
  * exceed the packed rows (a padded batch) or fall short (the rest is cut).
  * The sums of the lengths must stay below 2^31.  table_stride: elements from

@@ -97,7 +97,8 @@ __device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) 
 //
 // One launch and no word passes between workgroups: every workgroup scans all
 // requests, a tile of 1024 at a time, and serves its own range of rows and its
-// own share of new blocks by a search in the scanned sums.  The lengths are a
+// own share of new blocks by a search in the scanned sums; the last one writes
+// what belongs to requests and counts instead.  The lengths are a
 // few KiB that every workgroup finds in the L2, so scanning them again costs
 // less than a second launch or a hand-off would.  Bound by the chain lengths ->
 // scan -> search -> stores: 6 to 8 us for 64 requests of a token, 11 to 13 for 1000
@@ -108,22 +109,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
   __shared__ int64_t w_tok[kPlanThreads / 64], w_blk[kPlanThreads / 64], w_lost[kPlanThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t T = A.T;
+  const uint32_t servers = gridDim.x - 1;
+  const bool books = blockIdx.x == servers;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * A.per_wg;
-  const int64_t row1 = min<int64_t>(A.rows, row0 + A.per_wg);
+  const int64_t row1 = books ? row0 : min<int64_t>(A.rows, row0 + A.per_wg);
   int64_t carry_tok = 0, carry_blk = 0, lost = 0;
   for (int64_t b0 = 0; b0 < A.batch; b0 += kPlanTile) {
     const int cnt = static_cast<int>(min<int64_t>(kPlanTile, A.batch - b0));
     int64_t tok[kPlanEach], blk[kPlanEach], sum_tok = 0, sum_blk = 0;
+    // The block that a request's last token is in, where its new ones go on with
+    // it, and how many do: lost too if the table lacks it.
+    int32_t last[kPlanEach], more[kPlanEach];
 #pragma unroll
     for (int i = 0; i < kPlanEach; ++i) {
       const int r = tid * kPlanEach + i;
       const int64_t c = r < cnt ? max(A.cached[b0 + r], 0) : 0;
       const int64_t a = r < cnt ? max(A.added[b0 + r], 0) : 0;
       s_cached[r] = static_cast<int32_t>(c);
+      const int64_t held = (c + T - 1) / T;
+      last[i] = 0;
+      more[i] = static_cast<int32_t>(min(a, held * T - c));
+      if (books && more[i] > 0 && held <= A.width)
+        last[i] = A.table[(b0 + r) * A.table_stride + held - 1];  // (no workgroup writes held entries)
       tok[i] = sum_tok;
       blk[i] = sum_blk;
       sum_tok += a;
-      sum_blk += (c + a + T - 1) / T - (c + T - 1) / T;
+      sum_blk += (c + a + T - 1) / T - held;
     }
     int64_t inc_tok = sum_tok, inc_blk = sum_blk;  // inclusive over the wave's lanes
     for (int d = 1; d < 64; d <<= 1) {
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
     }
     __syncthreads();
     // (entries past cnt repeat the totals, so [i + 1] is right for every request)
-    if (blockIdx.x == 0) {
+    if (books) {
       for (int i = tid; i < cnt; i += kPlanThreads) {
         const int64_t c = s_cached[i], len = c + s_tok[i + 1] - s_tok[i];
         const int64_t held = (c + T - 1) / T;
@@ -167,10 +178,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
         const int64_t reach = min<int64_t>(A.width, held + max<int64_t>(0, A.nfree - s_blk[i]));
         lost += max<int64_t>(0, len - max<int64_t>(c, reach * T));
       }
+#pragma unroll
+      for (int i = 0; i < kPlanEach; ++i)
+        if (last[i] < 0) lost += more[i];
+      __syncthreads();
+      continue;
     }
     // new blocks
     for (int64_t x = s_blk[0] + static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
-         x < min<int64_t>(carry_blk, A.nfree); x += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
+         x < min<int64_t>(carry_blk, A.nfree); x += static_cast<int64_t>(servers) * kPlanThreads) {
       const int i = last_at_most(s_blk, cnt, x);
       const int64_t page = (s_cached[i] + T - 1) / T + x - s_blk[i];
       if (page < A.width) A.table[(b0 + i) * A.table_stride + page] = A.free_blocks[x];
@@ -197,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
     A.slots[n] = -1;
     A.positions[n] = -1;
   }
-  if (blockIdx.x == 0) {
+  if (books) {
     for (int d = 1; d < 64; d <<= 1) lost += __shfl_xor(lost, d);
     if (lane == 0) w_lost[wave] = lost;
     __syncthreads();
@@ -1459,7 +1475,7 @@ extern "C" int xfer_cache_plan(const int32_t* cached, const int32_t* added, int 
       1, std::min<int64_t>(1024, std::max((int64_t(rows) + 1023) / 1024, (int64_t(batch) + 255) / 256)));
   a.per_wg = int32_t((rows + grid - 1) / grid);
   const hipError_t e =
-      launch(plan_kernel, a, dim3(uint32_t(grid)), kPlanThreads, static_cast<hipStream_t>(stream));
+      launch(plan_kernel, a, dim3(uint32_t(grid) + 1), kPlanThreads, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "xfer_cache_plan launch");
   return XFER_OK;
 }
