@@ -423,9 +423,9 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
 
 /* xfer_cache_attend: softmax(scale * q k^T) v of packed query rows over the
  * cache.  Request b has the query rows starts[b] .. starts[b + 1) (of `rows`;
- * the plan's starts) and lengths[b] tokens, which include those rows' own:
- * row j of r sees the tokens 0 .. lengths[b] - r + j.  Head h of `heads` reads
- * key/value head h / (heads / H).  A row that sees nothing gives 0 and a log
+ * the plan's starts: none is below the one before) and lengths[b] tokens, which
+ * include those rows' own: row j of r sees the tokens 0 .. lengths[b] - r + j.
+ * Head h of `heads` reads key/value head h / (heads / H).  A row that sees nothing gives 0 and a log
  * sum of -infinity.  Tokens whose table entry lies outside the cache, and
  * those past the table's width, are left out; what the cache holds behind a
  * request's last token is not read into any result.  Rows of no request

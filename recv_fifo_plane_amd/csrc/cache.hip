@@ -626,6 +626,7 @@ struct AttendArgs {
   int32_t batch, rows, heads, width;
   uint32_t group;         // query heads of one key/value head
   uint32_t flat;          // workgroups of one key/value head, 0: one per tile of rows
+  uint32_t packed;        // tile numbers of one key/value head, 0: a grid of requests and tiles
   float scale2;           // scale * log2(e): weights are powers of two
   Shape s;
 };
@@ -1171,6 +1172,43 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
     attend_rows<E, D, NR, ONCE>(A, sh, b, h, (tiles - 1 - y) * NR * 16, 0, ~0u, nullptr, nullptr);
 }
 
+// Tiles numbered through the packed rows: with R rows a tile, request b's begin at
+// number first(b) = starts[b] * group / R + b, which leaves it as many as it can
+// need.  The request of number k, by a search with a lane per candidate: one trip
+// to memory for 64 requests, two for 4096.  (Starts outside the rows count as at
+// their ends, as rows_of has it.)
+__device__ __forceinline__ uint32_t first_tile(const AttendArgs& A, uint32_t b, uint32_t tile_rows) {
+  const uint32_t row = static_cast<uint32_t>(min(max(A.starts[b], 0), A.rows));
+  return row * A.group / tile_rows + b;
+}
+
+__device__ __forceinline__ uint32_t request_of(const AttendArgs& A, uint32_t k, uint32_t tile_rows) {
+  const uint32_t lane = threadIdx.x & 63u;
+  uint32_t lo = 0, n = A.batch;
+  while (n > 1) {
+    const uint32_t step = (n + 63) / 64, at = lane * step;
+    const bool there = at < n && first_tile(A, lo + at, tile_rows) <= k;
+    const uint32_t pos = max(static_cast<uint32_t>(__popcll(__ballot(there))), 1u) - 1;
+    lo += pos * step;
+    n = min(step, n - pos * step);
+  }
+  return uniform(lo);
+}
+
+// As attend_kernel, a workgroup per number and key/value head.
+template <typename E, int D, int NR>
+__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_packed_kernel(AttendArgs A) {
+  constexpr uint32_t kRows = NR * 16;
+  __shared__ AttendShared<D, NR> sh;
+  const uint32_t h = blockIdx.x % A.s.H;
+  for (uint32_t k = blockIdx.x / A.s.H; k < A.packed; k += gridDim.x / A.s.H) {
+    const uint32_t b = request_of(A, k, kRows), y = uniform(k - first_tile(A, b, kRows));
+    const uint32_t tiles = units_of(A, b, kRows).tiles;
+    if (y < tiles)  // (a number may be one that its request, or none, does not need)
+      attend_rows<E, D, NR, false>(A, sh, b, h, (tiles - 1 - y) * kRows, 0, ~0u, nullptr, nullptr);
+  }
+}
+
 // The chunks of all requests and tiles in one line, cut into equal shares for
 // as many workgroups per key/value head as the GPU holds: requests of very
 // different lengths, or few long ones, keep every CU busy to the end.  A
@@ -1302,15 +1340,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
 
 using AttendFn = void (*)(AttendArgs);
 struct AttendKernels {
-  AttendFn attend, flat, join;
+  AttendFn attend, packed, flat, join;
 };
 
 template <typename E, int D, int NR, bool ONCE>
 AttendKernels attend_of() {
   if constexpr (D * NR > 256)  // (sharing needs registers that are not there)
-    return {attend_kernel<E, D, NR, ONCE>, nullptr, nullptr};
+    return {attend_kernel<E, D, NR, ONCE>, attend_packed_kernel<E, D, NR>, nullptr, nullptr};
   else
-    return {attend_kernel<E, D, NR, ONCE>, attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
+    return {attend_kernel<E, D, NR, ONCE>, attend_packed_kernel<E, D, NR>,
+            attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
 }
 
 template <typename E, int D>
@@ -1337,7 +1376,10 @@ struct AttendPlan {
   int nr;
   uint32_t tiles;  // of a request
   uint32_t flat;   // AttendArgs::flat
+  uint32_t packed; // AttendArgs::packed
 };
+
+constexpr int64_t kEmptyWorkgroups = 16384;
 
 AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   AttendPlan p;
@@ -1366,13 +1408,23 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   // 31 / 38, of 4096 52 / 60, of 410 .. 4096 42 / 38, of 8192 95 / 104, of 820 ..
   // 8192 75 / 56; 128 requests of 410 .. 4096 106 / 106.
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
-  p.flat = 0;
+  p.flat = p.packed = 0;
   if (chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * p.nr <= 256) {
     // As many workgroups as are resident at once on 256 CUs, eight chunks each at least.
     const int64_t resident = 256 * attend_resident(int(s.D), p.nr);
     p.flat = uint32_t(std::max<int64_t>(
         1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
   }
+  // Where one request may have most of the rows, a grid of requests and tiles is
+  // mostly empty: 2000 workgroups that find nothing to do take 1 us, and hold up
+  // those behind them.  As many numbers as the packed rows have tiles, and one a
+  // request, are enough (first_tile), at a search in each workgroup.  Grid against
+  // numbers (us): 1024 requests of 16 rows and 64 tokens, no hints, 9260 / 330;
+  // 2000 rows beside 63 single ones 343 / 88; 60 requests of 8 rows and 300
+  // tokens, no hints, 29.7 / 26.6 (28k empty workgroups), with heads of 256 28.7 /
+  // 34.7 (10k).
+  const int64_t numbers = int64_t(q.rows) * group / (p.nr * 16) + q.batch;
+  if (!p.flat && wgs > numbers * s.H + kEmptyWorkgroups) p.packed = uint32_t(numbers);
   return p;
 }
 
@@ -1601,6 +1653,7 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
   a.scale2 = q->scale * 1.44269504088896341f;
   const AttendPlan p = attend_plan(a.s, *q);
   a.flat = p.flat;
+  a.packed = p.packed;
   const AttendWork work = attend_work(a.s, *q, p);
   if (p.flat && (!q->workspace || q->workspace_bytes < work.all() || !aligned(q->workspace, 16)))
     return fail(XFER_ERR_INVALID_ARG,
@@ -1615,7 +1668,10 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
                                                 : pick_attend<fp16_t>(a.s.D, p.nr, once);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
-  if (!p.flat) {
+  if (p.packed) {
+    const uint64_t most = kMaxGrid / a.s.H;
+    e = launch(k.packed, a, dim3(uint32_t(std::min<uint64_t>(p.packed, most)) * a.s.H), kAttendWaves * 64, s);
+  } else if (!p.flat) {
     e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles), kAttendWaves * 64, s);
   } else {
     e = launch(k.flat, a, dim3(p.flat * a.s.H), kAttendWaves * 64, s);
