@@ -288,7 +288,10 @@ int xfer_run_messages(xfer_conn* c, const void* src, void* dst, const size_t* of
  *   src, dst     16-byte aligned; the pools must not overlap, and the lists
  *                must not lie in dst.
  * Errors: INVALID_ARG (other protocols, sizes outside these domains, NULL
- * buffers or lists with n > 0, overlap, grid too large), STATE, HIP.  In a
+ * buffers or lists with n > 0, overlap, grid too large), STATE (also: captured
+ * into a graph on a relay connection, whose proxies hear of a transfer from
+ * this call alone, or a traced or jittered one), HIP.  Other connections' transfers may be captured on the
+ * stream of the device's last launch and replayed there.  In a
  * step trace the value of a zero-copy step's acquire is its byte offset in the
  * list instead of an address. */
 int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks, void* dst,

@@ -1049,6 +1049,15 @@ extern "C" int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks,
     return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: the pools overlap");
   if (overlap(dst, nd, from, n * 4) || overlap(dst, nd, to, n * 4))
     return fail(XFER_ERR_INVALID_ARG, "xfer_run_blocks: a list lies in the destination pool");
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  // Proxies hear of a transfer from this call alone, not from a replay; a debug
+  // launch has a number of its own, and a replay would be taken for a second
+  // block with the same work.
+  if (c->relay || debug_of(c)) {
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &capture) == hipSuccess && capture != hipStreamCaptureStatusNone)
+      return fail(XFER_ERR_STATE, "xfer_run_blocks: transfers of a relay, traced or jittered connection cannot be captured");
+  }
   const uint64_t nbytes = uint64_t(n) * block_bytes;
   std::vector<uint64_t>& add = c->add;
   rc = plan_steps(c, nbytes, 1, add, "xfer_run_blocks");
@@ -1075,7 +1084,6 @@ extern "C" int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks,
   args.total_wgs = total;
   args.xcd_remap = c->xcd_remap;
   args.rx_wgs = rx_region_of(c);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e =
       gate().run(c->device, s, [&] { return launch_blocks(v, args, c->block, s, c->coop); });
   if (e != hipSuccess) return hip_fail(e, "xfer_run_blocks launch");

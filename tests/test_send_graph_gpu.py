@@ -43,3 +43,31 @@ def test_sends_replayed(proto):
     assert state["error"] == 0
     torch.cuda.synchronize()
     conn.close()
+
+
+@pytest.mark.parametrize("fifo,jitter", [("relay", 0), ("device", 5)])
+def test_sends_that_cannot_be_replayed_are_not_captured(fifo, jitter):
+    """A replay would wait for proxies that were told of one transfer, or repeat the
+    number of a debug launch."""
+    import recv_fifo_plane_amd as xf
+    here, there = (xf.PagedCache(8, 16, 2, 64) for _ in range(2))
+    here.buffer.random_(0, 256)
+    ids = ints(range(8))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    conn = xf.Conn("simple", 2, 2, 4096, fifo, wgs_per_channel=2, timeout_ms=2000)
+    conn.set_jitter(jitter)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        here.send(conn, there, ids, ids)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            with pytest.raises(xf.XferError, match="relay"):
+                here.send(conn, there, ids, ids)
+            there.buffer.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not there.buffer.any()
+        here.send(conn, there, ids, ids)
+        torch.cuda.synchronize()
+    assert torch.equal(here.buffer, there.buffer) and conn.query(0)["error"] == 0
+    conn.close()
