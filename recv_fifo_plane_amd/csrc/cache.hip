@@ -1401,29 +1401,37 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
+  const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
+  // Tiles that the packed rows can have, and so workgroups of one head (first_tile).
+  const int64_t numbers = int64_t(q.rows) * group / (p.nr * 16) + q.batch;
+  const int64_t resident = 256 * attend_resident(int(s.D), p.nr);  // workgroups on 256 CUs
   // Sharing costs a second launch and about 8 us; it pays where few workgroups
   // would be left with long requests.  Measured at 8 key/value heads of 128,
   // group 4, one workgroup per tile against shared (us): 1 request of 1024
   // tokens 14 / 16, of 2048 21 / 17, of 16384 120 / 23; 32 requests of 2048
   // 31 / 38, of 4096 52 / 60, of 410 .. 4096 42 / 38, of 8192 95 / 104, of 820 ..
-  // 8192 75 / 56; 128 requests of 410 .. 4096 106 / 106.
-  const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
+  // 8192 75 / 56; 128 requests of 400 .. 5000 109 / 97, 1024 of them 656 / 679, of
+  // 100 .. 12000 913 / 865, of 4200 1352 / 1399: single rows gain where lengths
+  // differ and lose a twentieth where they do not.  Many rows, as workgroups for
+  // each one that is resident: 0.6 (3 requests of up to 200 rows) 76 / 69, 2.9 (8
+  // of up to 600) 326 / 185, 3.9 (1 of 2000 after 3000 tokens) 247 / 289, 8.2 (1
+  // whole prompt of 4200) 285 / 427, 9.2 (32 of up to 600) 668 / 537, 66 (8 whole
+  // prompts of 4200) 2089 / 3806; heads of 64, 16 (32 of up to 600) 456 / 521.  So
+  // from 12 on there are enough of them, whatever the lengths.
   p.flat = p.packed = 0;
-  if (chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * p.nr <= 256) {
-    // As many workgroups as are resident at once on 256 CUs, eight chunks each at least.
-    const int64_t resident = 256 * attend_resident(int(s.D), p.nr);
+  const bool enough = most > 1 && numbers * s.H > 12 * resident;
+  if (!enough && chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * p.nr <= 256) {
+    // As many workgroups as are resident at once, eight chunks each at least.
     p.flat = uint32_t(std::max<int64_t>(
         1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
   }
   // Where one request may have most of the rows, a grid of requests and tiles is
   // mostly empty: 2000 workgroups that find nothing to do take 1 us, and hold up
-  // those behind them.  As many numbers as the packed rows have tiles, and one a
-  // request, are enough (first_tile), at a search in each workgroup.  Grid against
-  // numbers (us): 1024 requests of 16 rows and 64 tokens, no hints, 9260 / 330;
-  // 2000 rows beside 63 single ones 343 / 88; 60 requests of 8 rows and 300
-  // tokens, no hints, 29.7 / 26.6 (28k empty workgroups), with heads of 256 28.7 /
-  // 34.7 (10k).
-  const int64_t numbers = int64_t(q.rows) * group / (p.nr * 16) + q.batch;
+  // those behind them.  Numbers through the packed rows leave those out, at a
+  // search in each workgroup.  Grid against numbers (us): 1024 requests of 16 rows
+  // and 64 tokens, no hints, 9260 / 330; 2000 rows beside 63 single ones 343 / 88;
+  // 60 requests of 8 rows and 300 tokens, no hints, 29.7 / 26.6 (28k empty
+  // workgroups), with heads of 256 28.7 / 34.7 (10k).
   if (!p.flat && wgs > numbers * s.H + kEmptyWorkgroups) p.packed = uint32_t(numbers);
   return p;
 }
