@@ -290,10 +290,10 @@ int xfer_run_messages(xfer_conn* c, const void* src, void* dst, const size_t* of
  * Errors: INVALID_ARG (other protocols, sizes outside these domains, NULL
  * buffers or lists with n > 0, overlap, grid too large), STATE (also: captured
  * into a graph on a relay connection, whose proxies hear of a transfer from
- * this call alone, or a traced or jittered one), HIP.  Other connections' transfers may be captured on the
- * stream of the device's last launch and replayed there.  In a
- * step trace the value of a zero-copy step's acquire is its byte offset in the
- * list instead of an address. */
+ * this call alone, or on a traced or jittered one), HIP.  Transfers of other
+ * connections may be captured on the stream of the device's last launch and
+ * replayed there.  In a step trace the value of a zero-copy step's acquire is its
+ * byte offset in the list instead of an address. */
 int xfer_run_blocks(xfer_conn* c, const void* src, size_t src_blocks, void* dst,
                     size_t dst_blocks, size_t block_bytes, const int32_t* from,
                     const int32_t* to, size_t n, void* stream);
@@ -444,7 +444,10 @@ int xfer_cache_store(const xfer_cache_shape* shape, void* cache, const void* key
  * arguments, 16-byte aligned, used by this call alone until it has run.
  * Scores, sums and outputs are accumulated in float; before they multiply the
  * values, the weights exp(...) are rounded to the sum of two bfloat16 numbers
- * (off by 2^-16 of the weight at most).
+ * (off by 2^-16 of the weight at most).  What is summed has to fit a float: the
+ * products of a query and the codes (queries below 2^110), scores scaled by up to
+ * the largest key scale (scale times that below 2^126), and up to 256 times the
+ * values of the tokens that a row sees (values times tokens below 2^119).
  * Errors: INVALID_ARG (sizes outside their domains: batch * H below 2^24, rows *
  * heads below 2^31; NULL or misaligned buffers, strides of out that let its rows
  * or heads overlap, too small a workspace), HIP. */

@@ -979,183 +979,181 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
   const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
   const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
-  {
-    const RowTile rt = row_tile(A, b, first, NR * 16);
-    c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
+  const RowTile rt = row_tile(A, b, first, NR * 16);
+  c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
 
-    // The first chunk's table entries, then its keys and values, are asked for
-    // before anything is waited for: each is a trip to memory.
-    // Waves with no chunk ask too, for the last block or, where no token is seen
-    // and the table may be empty, for whichever the first entry of starts names
-    // (any word will do, settle puts it in range): behind a branch around these
-    // loads every wait of the loop would be one for all of them.
-    const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen)), reach = max(seen_all, 1u);
-    if (seen_all == 0) table = A.starts;
-    uint32_t c = c0 + wave, nans = 0;
-    Keys<D, ONCE> keys;
-    Values<D, ONCE> vals;
-    Place at, next;
-    constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
-    at.look(A, table, c * kChunk, reach, g, n);
-    next.look(A, table, c * kChunk + kNext, reach, g, n);
-    __builtin_amdgcn_sched_barrier(0);
+  // The first chunk's table entries, then its keys and values, are asked for
+  // before anything is waited for: each is a trip to memory.
+  // Waves with no chunk ask too, for the last block or, where no token is seen
+  // and the table may be empty, for whichever the first entry of starts names
+  // (any word will do, settle puts it in range): behind a branch around these
+  // loads every wait of the loop would be one for all of them.
+  const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen)), reach = max(seen_all, 1u);
+  if (seen_all == 0) table = A.starts;
+  uint32_t c = c0 + wave, nans = 0;
+  Keys<D, ONCE> keys;
+  Values<D, ONCE> vals;
+  Place at, next;
+  constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
+  at.look(A, table, c * kChunk, reach, g, n);
+  next.look(A, table, c * kChunk + kNext, reach, g, n);
+  __builtin_amdgcn_sched_barrier(0);
 
-    // Queries: lane (g, n) takes row n's dims in the order of its key loads.
-    // They wait in shared memory, the same for every wave, which frees the
-    // registers that decide how many waves a CU holds.
-    constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
-    int32_t limit[NR];        // last token that the row sees
-    int32_t least = rt.seen;  // the first of them
-    u32x4 q[NR][QL];
+  // Queries: lane (g, n) takes row n's dims in the order of its key loads.
+  // They wait in shared memory, the same for every wave, which frees the
+  // registers that decide how many waves a CU holds.
+  constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
+  int32_t limit[NR];        // last token that the row sees
+  int32_t least = rt.seen;  // the first of them
+  u32x4 q[NR][QL];
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const uint32_t i = first + x * 16 + n;
-      const int64_t j = i / A.group, row = rt.start + j;
-      const bool there = i < rt.rows;
-      limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
-      const E* p = static_cast<const E*>(A.query) + row * A.query_row +
-                   static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
+  for (int x = 0; x < NR; ++x) {
+    const uint32_t i = first + x * 16 + n;
+    const int64_t j = i / A.group, row = rt.start + j;
+    const bool there = i < rt.rows;
+    limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
+    const E* p = static_cast<const E*>(A.query) + row * A.query_row +
+                 static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
 #pragma unroll
-      for (int k = 0; k < QL; ++k) {
-        q[x][k] = u32x4{0u, 0u, 0u, 0u};
-        const uint32_t step = wave + k * kAttendWaves;
-        if (there && step < KL) __builtin_memcpy(&q[x][k], p + key_dim<D>(step, g), 16);
-      }
-      if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
+    for (int k = 0; k < QL; ++k) {
+      q[x][k] = u32x4{0u, 0u, 0u, 0u};
+      const uint32_t step = wave + k * kAttendWaves;
+      if (there && step < KL) __builtin_memcpy(&q[x][k], p + key_dim<D>(step, g), 16);
     }
-    at.settle(A, c * kChunk, seen_all, g);
-    keys.load(A, at, c * kChunk, h, g, n);
-    __builtin_amdgcn_sched_barrier(0);
-    vals.load(A, at, c * kChunk, h, g, n);
+    if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
+  }
+  at.settle(A, c * kChunk, seen_all, g);
+  keys.load(A, at, c * kChunk, h, g, n);
+  __builtin_amdgcn_sched_barrier(0);
+  vals.load(A, at, c * kChunk, h, g, n);
+#pragma unroll
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int k = 0; k < QL; ++k)
+      if (wave + k * kAttendWaves < KL) sh.q[x][wave + k * kAttendWaves][lane] = q[x][k];
+  for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+  least = __builtin_amdgcn_readfirstlane(least);
+  __syncthreads();
+
+  float m[NR], l[NR];
+  f32x4 acc[NR][DT];
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    m[x] = -INFINITY;
+    l[x] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  // A chunk's keys are loaded while the chunk before is still at its weights
+  // and values, its values as soon as those are done.  Loads return in the
+  // order they were asked for, so its table entries come a step earlier yet,
+  // ahead of the values of the chunk before: waiting for them waits for no
+  // codes.  The last step loads too (the last block again, near at hand): a
+  // branch around the loads would make every wait after it one for all of
+  // them.
+  auto step = [&](auto masked) {
+    const uint32_t t0 = c * kChunk, tg = t0 + 16 * g, ahead = t0 + kNext;
+    const int32_t bg = at.mine;
+    f32x4 s[NR][4];
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int k = 0; k < QL; ++k)
-        if (wave + k * kAttendWaves < KL) sh.q[x][wave + k * kAttendWaves][lane] = q[x][k];
-    for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
-    least = __builtin_amdgcn_readfirstlane(least);
-    __syncthreads();
-
-    float m[NR], l[NR];
-    f32x4 acc[NR][DT];
+      for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      m[x] = -INFINITY;
-      l[x] = 0.0f;
+    for (int k = 0; k < KL; ++k) {
+      E8 b8[NR];
 #pragma unroll
-      for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    // A chunk's keys are loaded while the chunk before is still at its weights
-    // and values, its values as soon as those are done.  Loads return in the
-    // order they were asked for, so its table entries come a step earlier yet,
-    // ahead of the values of the chunk before: waiting for them waits for no
-    // codes.  The last step loads too (the last block again, near at hand): a
-    // branch around the loads would make every wait after it one for all of
-    // them.
-    auto step = [&](auto masked) {
-      const uint32_t t0 = c * kChunk, tg = t0 + 16 * g, ahead = t0 + kNext;
-      const int32_t bg = at.mine;
-      f32x4 s[NR][4];
+      for (int x = 0; x < NR; ++x) b8[x] = __builtin_bit_cast(E8, sh.q[x][k][lane]);
 #pragma unroll
-      for (int x = 0; x < NR; ++x)
+      for (int t = 0; t < 4; ++t) {
+        E8 a;
+        widen(keys.lo(t, k), keys.hi(t, k), 1.0f, a);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < KL; ++k) {
-        E8 b8[NR];
-#pragma unroll
-        for (int x = 0; x < NR; ++x) b8[x] = __builtin_bit_cast(E8, sh.q[x][k][lane]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          E8 a;
-          widen(keys.lo(t, k), keys.hi(t, k), 1.0f, a);
-#pragma unroll
-          for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[x], s[x][t]);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      next.settle(A, ahead, seen_all, g);
-      keys.load(A, next, ahead, h, g, n);
-      __builtin_amdgcn_sched_barrier(0);
-      // (the scales of a block that is not the request's: anything)
-      const float ks = bg < 0 ? 1.0f : vals.key_scale, vs = bg < 0 ? 1.0f : vals.value_scale;
-      weigh<decltype(masked)::value, DT, NR>(A, s, acc, m, l, vals.w, limit, ks * A.scale2, vs,
-                                             seen_all, tg, bg, nans);
-      __builtin_amdgcn_sched_barrier(0);
-      at = next;
-      next.look(A, table, ahead + kNext, seen_all, g, n);
-      vals.load(A, at, ahead, h, g, n);
-      c += kAttendWaves;
-    };
-    // Chunks that every row sees whole, up to the first that is not; then the rest.
-    const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
-    while (c < whole && __ballot(at.mine < 0) == 0) step(std::false_type());
-    const uint32_t rest = c;
-    while (c < c1) step(std::true_type());
-    const bool any_nan = __ballot(nans != 0) != 0;
-
-    // Join the waves.
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      l[x] += __shfl_xor(l[x], 16);
-      l[x] += __shfl_xor(l[x], 32);
-      if (g == 0) {
-        sh.m[wave][x * 16 + n] = m[x];
-        sh.l[wave][x * 16 + n] = l[x];
+        for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[x], s[x][t]);
       }
     }
-    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    next.settle(A, ahead, seen_all, g);
+    keys.load(A, next, ahead, h, g, n);
+    __builtin_amdgcn_sched_barrier(0);
+    // (the scales of a block that is not the request's: anything)
+    const float ks = bg < 0 ? 1.0f : vals.key_scale, vs = bg < 0 ? 1.0f : vals.value_scale;
+    weigh<decltype(masked)::value, DT, NR>(A, s, acc, m, l, vals.w, limit, ks * A.scale2, vs,
+                                           seen_all, tg, bg, nans);
+    __builtin_amdgcn_sched_barrier(0);
+    at = next;
+    next.look(A, table, ahead + kNext, seen_all, g, n);
+    vals.load(A, at, ahead, h, g, n);
+    c += kAttendWaves;
+  };
+  // Chunks that every row sees whole, up to the first that is not; then the rest.
+  const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
+  while (c < whole && __ballot(at.mine < 0) == 0) step(std::false_type());
+  const uint32_t rest = c;
+  while (c < c1) step(std::true_type());
+  const bool any_nan = __ballot(nans != 0) != 0;
+
+  // Join the waves.
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      float top = sh.m[0][x * 16 + n];
-      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      const float f = __builtin_amdgcn_exp2f(m[x] - base);
+  for (int x = 0; x < NR; ++x) {
+    l[x] += __shfl_xor(l[x], 16);
+    l[x] += __shfl_xor(l[x], 32);
+    if (g == 0) {
+      sh.m[wave][x * 16 + n] = m[x];
+      sh.l[wave][x * 16 + n] = l[x];
+    }
+  }
+  __syncthreads();
 #pragma unroll
-      for (int e = 0; e < DT; ++e)
-        *reinterpret_cast<f32x4*>(&sh.acc[wave][n][16 * e + 4 * g]) = acc[x][e] * f;
-      if (any_nan) {
+  for (int x = 0; x < NR; ++x) {
+    float top = sh.m[0][x * 16 + n];
+    for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(m[x] - base);
+#pragma unroll
+    for (int e = 0; e < DT; ++e)
+      *reinterpret_cast<f32x4*>(&sh.acc[wave][n][16 * e + 4 * g]) = acc[x][e] * f;
+    if (any_nan) {
 #pragma clang loop unroll(disable)
-        for (uint32_t i = 0; i < DT * ((c1 - rest + kAttendWaves - 1) / kAttendWaves); ++i) {
-          const uint32_t d = 16 * (i % DT) + 4 * g;
-          const int32_t t0 = (rest + i / DT * kAttendWaves) * kChunk;
-          f32x4* o = reinterpret_cast<f32x4*>(&sh.acc[wave][n][d]);
-          *o += seen_nans(A, table, h, t0, min(t0 + kChunk - 1, limit[x]), d);
-        }
+      for (uint32_t i = 0; i < DT * ((c1 - rest + kAttendWaves - 1) / kAttendWaves); ++i) {
+        const uint32_t d = 16 * (i % DT) + 4 * g;
+        const int32_t t0 = (rest + i / DT * kAttendWaves) * kChunk;
+        f32x4* o = reinterpret_cast<f32x4*>(&sh.acc[wave][n][d]);
+        *o += seen_nans(A, table, h, t0, min(t0 + kChunk - 1, limit[x]), d);
       }
-      __syncthreads();
-      for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
-        const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + x * 16 + r;
-        const int64_t row = rt.start + ri / A.group;
-        if (ri >= rt.rows) continue;
-        float top = sh.m[0][x * 16 + r], sum = 0.0f;
-        for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + r]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int w = 0; w < kAttendWaves; ++w) {
-          sum += sh.l[w][x * 16 + r] * __builtin_amdgcn_exp2f(sh.m[w][x * 16 + r] - base);
-          o += *reinterpret_cast<const f32x4*>(&sh.acc[w][r][d]);
-        }
-        const uint32_t head = h * A.group + ri % A.group;
-        const int64_t at = row * A.heads + head;
-        if (part == nullptr) {
-          const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-          E v[4];
-          for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
-          __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + d, v, 8);
-          if (d == 0 && A.lse)
-            A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
-        } else {
-          *reinterpret_cast<f32x4*>(part + (x * 16 + r) * D + d) = o;
-          if (d == 0) {
-            stats[(x * 16 + r) * 2] = top;
-            stats[(x * 16 + r) * 2 + 1] = sum;
-          }
-        }
-      }
-      __syncthreads();
     }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
+      const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + x * 16 + r;
+      const int64_t row = rt.start + ri / A.group;
+      if (ri >= rt.rows) continue;
+      float top = sh.m[0][x * 16 + r], sum = 0.0f;
+      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + r]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int w = 0; w < kAttendWaves; ++w) {
+        sum += sh.l[w][x * 16 + r] * __builtin_amdgcn_exp2f(sh.m[w][x * 16 + r] - base);
+        o += *reinterpret_cast<const f32x4*>(&sh.acc[w][r][d]);
+      }
+      const uint32_t head = h * A.group + ri % A.group;
+      const int64_t at = row * A.heads + head;
+      if (part == nullptr) {
+        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        E v[4];
+        for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+        __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + d, v, 8);
+        if (d == 0 && A.lse)
+          A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<f32x4*>(part + (x * 16 + r) * D + d) = o;
+        if (d == 0) {
+          stats[(x * 16 + r) * 2] = top;
+          stats[(x * 16 + r) * 2 + 1] = sum;
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -1211,8 +1209,10 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
 
 // The chunks of all requests and tiles in one line, cut into equal shares for
 // as many workgroups per key/value head as the GPU holds: requests of very
-// different lengths, or few long ones, keep every CU busy to the end.  A
-// workgroup writes the tiles that lie whole in its share and leaves the sums
+// different lengths, or few long ones, keep every CU busy to the end.  Every tile
+// of a request counts all of its chunks, those past the tile's last row too:
+// shares are even where few rows follow many tokens, while for a whole prompt
+// half of the units are skipped, most of them at its front.  A workgroup writes the tiles that lie whole in its share and leaves the sums
 // of at most two others, the first and the last, to join_kernel.  Every
 // workgroup sums up the requests' units for itself.
 template <typename E, int D, int NR, bool ONCE>
@@ -1292,50 +1292,48 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
   if (t.request < 0 || tid >= kGroups * kWide) return;
   const uint32_t rows = rows_of(A, t.request);
   const int64_t start = A.starts[t.request];
-  {
-    const uint32_t r = blockIdx.z * kGroups + tid / kWide, i = t.tile * kRows + r;
-    if (r >= kRows || i >= rows) return;
-    // the first share's second place, the later ones' first
-    const uint64_t p0 = (static_cast<uint64_t>(w * A.s.H + h) * 2 + 1) * kRows + r;
-    const uint64_t step = 2ull * A.s.H * kRows, p1 = p0 - kRows + step;
-    float top = -INFINITY, sum = 0.0f;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr uint32_t kTake = 8;  // shares taken together: their loads are in flight at once
-    for (uint32_t k0 = 0; k0 <= t.last - w; k0 += kTake) {
-      float m[kTake], l[kTake];
-      f32x4 v[kTake];
+  const uint32_t r = blockIdx.z * kGroups + tid / kWide, i = t.tile * kRows + r;
+  if (r >= kRows || i >= rows) return;
+  // the first share's second place, the later ones' first
+  const uint64_t p0 = (static_cast<uint64_t>(w * A.s.H + h) * 2 + 1) * kRows + r;
+  const uint64_t step = 2ull * A.s.H * kRows, p1 = p0 - kRows + step;
+  float top = -INFINITY, sum = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr uint32_t kTake = 8;  // shares taken together: their loads are in flight at once
+  for (uint32_t k0 = 0; k0 <= t.last - w; k0 += kTake) {
+    float m[kTake], l[kTake];
+    f32x4 v[kTake];
 #pragma unroll
-      for (uint32_t k = 0; k < kTake; ++k) {
-        const bool there = k0 + k <= t.last - w;
-        const uint64_t p = k0 + k == 0 || !there ? p0 : p1 + (k0 + k - 1) * step;
-        m[k] = there ? A.stats[p * 2] : -INFINITY;
-        l[k] = there ? A.stats[p * 2 + 1] : 0.0f;
-        v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (there) v[k] = *reinterpret_cast<const f32x4*>(A.part + p * D + 4 * d);
-      }
-      const float was = top;
-#pragma unroll
-      for (uint32_t k = 0; k < kTake; ++k) top = fmaxf(top, m[k]);
-      const float base = top == -INFINITY ? 0.0f : top;
-      const float keep = __builtin_amdgcn_exp2f(was - base);
-      sum *= keep;
-      o *= keep;
-#pragma unroll
-      for (uint32_t k = 0; k < kTake; ++k) {
-        const float f = __builtin_amdgcn_exp2f(m[k] - base);
-        sum += l[k] * f;
-        o += v[k] * f;
-      }
+    for (uint32_t k = 0; k < kTake; ++k) {
+      const bool there = k0 + k <= t.last - w;
+      const uint64_t p = k0 + k == 0 || !there ? p0 : p1 + (k0 + k - 1) * step;
+      m[k] = there ? A.stats[p * 2] : -INFINITY;
+      l[k] = there ? A.stats[p * 2 + 1] : 0.0f;
+      v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (there) v[k] = *reinterpret_cast<const f32x4*>(A.part + p * D + 4 * d);
     }
-    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    const int64_t row = start + i / A.group;
-    const uint32_t head = h * A.group + i % A.group;
-    E v[4];
-    for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
-    __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
-    if (d == 0 && A.lse)
-      A.lse[row * A.heads + head] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+    const float was = top;
+#pragma unroll
+    for (uint32_t k = 0; k < kTake; ++k) top = fmaxf(top, m[k]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float keep = __builtin_amdgcn_exp2f(was - base);
+    sum *= keep;
+    o *= keep;
+#pragma unroll
+    for (uint32_t k = 0; k < kTake; ++k) {
+      const float f = __builtin_amdgcn_exp2f(m[k] - base);
+      sum += l[k] * f;
+      o += v[k] * f;
+    }
   }
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+  const int64_t row = start + i / A.group;
+  const uint32_t head = h * A.group + i % A.group;
+  E v[4];
+  for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+  __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
+  if (d == 0 && A.lse)
+    A.lse[row * A.heads + head] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 using AttendFn = void (*)(AttendArgs);
@@ -1671,7 +1669,13 @@ extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cach
   a.begun = reinterpret_cast<Begun*>(mem);
   a.part = reinterpret_cast<float*>(mem + work.begun);
   a.stats = reinterpret_cast<float*>(mem + work.begun + work.part);
-  const bool once = p.tiles == 1;  // no other workgroup reads the same tokens
+  // With one tile a request no other workgroup reads the same tokens (but for
+  // requests that share blocks), and loads that leave the caches alone serve long
+  // even reads better (us, with against without): 64 single rows over 4000 tokens
+  // each, 8 heads of 128, 92 / 99; 2 over 65k and 131k 84 / 92; 128 over 3500, heads
+  // of 64, 76 / 85.  Where latency counts they lose: 48 over 100 .. 3000, heads of
+  // 256, 42.6 / 38.4; 100 over 300, heads of 192, 17.3 / 15.2.
+  const bool once = p.tiles == 1;
   const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr, once)
                                                 : pick_attend<fp16_t>(a.s.D, p.nr, once);
   const hipStream_t s = static_cast<hipStream_t>(stream);
