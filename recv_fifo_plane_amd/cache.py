@@ -92,7 +92,8 @@ def _table(t, what, batch, device):
     have, width = t.shape
     if have != batch:
         raise ValueError("%s: expected %d rows, got %d" % (what, batch, have))
-    _int(width, what)
+    if width > _MOST:
+        _int(width, what)
     stride = t.stride(0) if batch > 1 else width
     if (width > 1 and t.stride(1) != 1) or stride < width:
         raise ValueError("%s: rows must be contiguous and not overlap" % what)
@@ -118,9 +119,9 @@ def _on(stream, device):
         raise ValueError("stream is of %s, the tensors are on cuda:%d" % (own, device))
 
 
-def _no_grad(t, what):
-    """Refuses a tensor whose gradient would be lost."""
-    if getattr(t, "requires_grad", False) and _GRAD():
+def _no_grad(what):
+    """Refuses a tensor that requires a gradient, which would be lost."""
+    if _GRAD():
         raise ValueError("%s: there is no gradient of attention over the cache; call it under "
                          "torch.no_grad() or with a detached tensor" % what)
 
@@ -154,7 +155,8 @@ def _side(stream, device):
 
 
 def _empty(like, shape, dtype, side, result=True):
-    """A new tensor that a launch on the stream `side` (None: the current one) writes.
+    """A new tensor that a launch on the stream `side` writes (None: the current one,
+    where callers in a hurry call new_empty themselves).
 
     It comes from that stream's pool: the current stream's could hold memory
     that was freed there while kernels still queued use it, and a launch on
@@ -186,12 +188,16 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
     at_added = _list(added, "plan_blocks: added", batch, dev)
     at_table, stride, width = _table(table, "plan_blocks: table", batch, dev)
     at_free = _list(free, "plan_blocks: free", None, dev)
-    block_tokens, rows = _int(block_tokens, "plan_blocks: block_tokens"), _int(rows, "plan_blocks: rows")
+    block_tokens, rows = int(block_tokens), int(rows)
     if rows < 0:
         raise ValueError("plan_blocks: rows must not be negative")
+    if rows > _MOST or not 0 <= block_tokens <= _MOST:
+        _int(rows, "plan_blocks: rows")
+        _int(block_tokens, "plan_blocks: block_tokens")
     sizes = (rows, rows, batch + 1, batch, 2)
     if out is None:
-        buf = _empty(cached, sum(sizes), _INT32, _side(stream, dev))
+        buf = (cached.new_empty(sum(sizes)) if stream is None
+               else _empty(cached, sum(sizes), _INT32, _side(stream, dev)))
         out = BlockPlan(*buf.split_with_sizes(sizes))
         slots = buf.data_ptr()
         positions = slots + 4 * rows
@@ -290,7 +296,8 @@ class PagedCache:
         a query or out that requires it is refused."""
         kinds = _kinds()
         _tensor(query, "attend: query", kinds, 3, self.device)
-        _no_grad(query, "attend: query")
+        if getattr(query, "requires_grad", False):
+            _no_grad("attend: query")
         rows, heads, d = query.shape
         dtype = query.dtype
         if kinds[dtype] == 2:
@@ -301,15 +308,21 @@ class PagedCache:
         batch = lengths.shape[0]
         at_starts = _list(starts, "attend: starts", batch + 1, self.device)
         at_table, stride, width = _table(table, "attend: table", batch, self.device)
-        max_query, max_length = _int(max_query, "attend: max_query"), _int(max_length, "attend: max_length")
-        side = _side(stream, self.device)
+        max_query, max_length = int(max_query), int(max_length)
+        if not (0 <= max_query <= _MOST and 0 <= max_length <= _MOST):
+            _int(max_query, "attend: max_query")
+            _int(max_length, "attend: max_length")
+        side = None if stream is None else _side(stream, self.device)
         if out is None:
-            out = _empty(query, (rows, heads, d), dtype, side)
-        _no_grad(out, "attend: out")
+            out = (query.new_empty((rows, heads, d)) if side is None
+                   else _empty(query, (rows, heads, d), dtype, side))
+        elif getattr(out, "requires_grad", False):
+            _no_grad("attend: out")
         o, o_row, o_head = _rows(out, "attend: out", (dtype,), self.device, rows, heads, d)
         sums = None
         if lse is True:
-            sums = _empty(query, (rows, heads), _FLOAT32, side)
+            sums = (query.new_empty((rows, heads), dtype=_FLOAT32) if side is None
+                    else _empty(query, (rows, heads), _FLOAT32, side))
         elif lse is not False and lse is not None:
             sums = _tensor(lse, "attend: lse", (_FLOAT32,), 2, self.device)
             if tuple(sums.shape) != (rows, heads) or not sums.is_contiguous():
@@ -324,7 +337,8 @@ class PagedCache:
         if rc:
             X.check(rc)
         if n.value:
-            work = _empty(query, n.value, _UINT8, side, result=False)
+            work = (query.new_empty(n.value, dtype=_UINT8) if side is None
+                    else _empty(query, n.value, _UINT8, side, result=False))
             a.workspace, a.workspace_bytes = work.data_ptr(), n.value
         _call(self.device, stream, lib.xfer_cache_attend, self._ref, self._base, ref)
         return out if sums is None else (out, sums)

@@ -124,7 +124,7 @@ def test_sizes_of_a_cache_beyond_an_int(i):
         xf.PagedCache(*sizes, buffer=FakeTensor((sizes[0], R.block_bytes(16, 2, 128)), torch.uint8))
 
 
-@pytest.mark.parametrize("block,rows", [(BIG + 16, 20), (16, BIG + 20), (16, (1 << 31) + 20)])
+@pytest.mark.parametrize("block,rows", [(BIG + 16, 20), (16 - BIG, 20), (16, BIG + 20), (16, (1 << 31) + 20)])
 def test_sizes_of_a_plan_beyond_an_int(cache, block, rows):
     out = xf.BlockPlan(*(FakeTensor((n,)) for n in (rows, rows, 4, 3, 2)))
     with pytest.raises(ValueError, match="2\\^31"):
@@ -140,7 +140,7 @@ def test_lists_of_a_plan_beyond_an_int(cache, free, width):
                       out=out)
 
 
-@pytest.mark.parametrize("kw", [dict(max_query=BIG), dict(max_length=BIG + 5), dict(max_length=1 << 31)])
+@pytest.mark.parametrize("kw", [dict(max_query=BIG), dict(max_length=BIG + 5), dict(max_query=5 - BIG), dict(max_length=1 << 31)])
 def test_hints_beyond_an_int(cache, kw):
     with pytest.raises(ValueError, match="2\\^31"):
         cache.attend(*attend_args(), out=FakeTensor((4, 4, 128), BF), **kw)
