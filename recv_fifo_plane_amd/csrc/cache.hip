@@ -101,7 +101,7 @@ __device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) 
 // what belongs to requests and counts instead.  The lengths are a
 // few KiB that every workgroup finds in the L2, so scanning them again costs
 // less than a second launch or a hand-off would.  Bound by the chain lengths ->
-// scan -> search -> stores: 6 to 8 us for 64 requests of a token, 11 to 13 for 1000
+// scan -> search -> stores: 5.3 us for 64 requests of a token, 11 for 1000
 // prompts of 1 to 1200 tokens (a launch that does nothing: 3.6).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs A) {
   __shared__ int64_t s_tok[kPlanTile + 1], s_blk[kPlanTile + 1];
@@ -770,8 +770,9 @@ struct Values {
 };
 
 // Workgroups a CU is to hold: bounds the registers of a lane (four waves of 512
-// / this).  Two with two tiles of 128 measured 107 us where one took 151 (chunks of
-// 8 requests); three with one tile of 128 were no faster.
+// / this).  Two with two tiles of 128 measured 118 us where one took 187 (chunks of
+// 8 requests), 1135 and 1650 (8 prompts of 3000 tokens); three with one tile of 128
+// were no faster.
 constexpr int attend_resident(int d, int nr) {
   return nr == 2 ? (d <= 128 ? 2 : 1) : d == 64 ? 3 : d <= 192 ? 2 : 1;
 }
@@ -958,7 +959,7 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // widen, weigh and rescale where there are many (8 requests with up to 600 rows
 // each after up to 5000 tokens: 34.5 GFLOP in 107 us, 322 TFLOP/s, of which the
 // weights' second parts take 10 us); the chain
-// table -> codes -> products for short ones (300 tokens: 9 us).
+// table -> codes -> products for short ones (300 tokens: 8 us).
 template <int D, int NR>
 struct AttendShared {  // 19 to 84 KiB
   u32x4 q[NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
@@ -1159,8 +1160,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
 
 // One workgroup per tile of rows and key/value head.  The last tiles see most
 // tokens and are begun first: with 32 heads of 128 over 8, 8 requests of 3000 to
-// 3900 tokens, 700 to 3000 of them new, take 1013 us and not 1141, 2 requests of
-// 500 to 1000 tokens, all new, 54 and not 63.
+// 3900 tokens, 700 to 3000 of them new, take 1290 us and not 1390.
 template <typename E, int D, int NR, bool ONCE>
 __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
   __shared__ AttendShared<D, NR> sh;
@@ -1386,13 +1386,13 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   if (!q.max_query && q.rows <= q.batch) most = 1;
   const int64_t rows = most * group;
   // Two tiles of rows share the widened codes and halve the reads, but two of 192
-  // or 256 leave a CU one workgroup, and those of 256 no registers for sharing.
-  // One against two (us, drafts with 12 heads over 2, the others with 32 over 8):
-  // heads of 192: 48 requests of 3 to 5 rows 24 / 47, 8 with 1 to 600 rows after up
-  // to 5000 tokens 165 / 184, 2 prompts of 1000 93 / 110, 8 of 3000 2080 / 1840.
-  // Heads of 256: 48 drafts 39 / 60, a prompt of 100 15 / 20 (200 tiles), 256 drafts
-  // 73 / 73 (1024), 2 prompts of 1000 210 / 144 (4000), 8 with up to 600 rows 352 / 362,
-  // 8 prompts of 3000 4460 / 2580.
+  // or 256 leave a CU one workgroup, and no registers for sharing.  One against
+  // two (us, drafts with 12 heads over 2, the others with 32 over 8): heads of 192:
+  // 48 requests of 3 to 5 rows 27 / 42, 256 of them 58 / 52, 8 with 1 to 600 rows
+  // after up to 4400 tokens 208 / 438, 2 prompts of 1000 99 / 120, 8 of 3000 2060 /
+  // 2210.  Heads of 256: 48 drafts 39 / 48, a prompt of 100 12.6 / 16.8 (200 tiles),
+  // 256 drafts 86 / 63 (1024), 2 prompts of 1000 208 / 151 (4000), 8 with up to 600
+  // rows 439 / 548, 8 prompts of 3000 4140 / 2770.
   p.nr = rows <= 16 || s.D == 192 ? 1 : 2;
   if (s.D == 256 && q.batch * int64_t(s.H) * ((rows + 15) / 16) <= 1024) p.nr = 1;
   p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.nr * 16 - 1) / (p.nr * 16)));
