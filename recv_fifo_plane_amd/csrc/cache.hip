@@ -958,8 +958,8 @@ __device__ __forceinline__ void weigh(const AttendArgs& A, f32x4 (&s)[NR][4], f3
 // first trip to memory and the join making up the rest; the instructions that
 // widen, weigh and rescale where there are many (8 requests with up to 600 rows
 // each after up to 5000 tokens: 34.5 GFLOP in 107 us, 322 TFLOP/s, of which the
-// weights' second parts take 10 us); the chain
-// table -> codes -> products for short ones (300 tokens: 8 us).
+// weights' second parts take 10 us); the chain table -> codes -> products for
+// short ones (300 tokens: 8 us).
 template <int D, int NR>
 struct AttendShared {  // 19 to 84 KiB
   u32x4 q[NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
@@ -1212,9 +1212,10 @@ __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) att
 // different lengths, or few long ones, keep every CU busy to the end.  Every tile
 // of a request counts all of its chunks, those past the tile's last row too:
 // shares are even where few rows follow many tokens, while for a whole prompt
-// half of the units are skipped, most of them at its front.  A workgroup writes the tiles that lie whole in its share and leaves the sums
-// of at most two others, the first and the last, to join_kernel.  Every
-// workgroup sums up the requests' units for itself.
+// half of the units are skipped, most of them at its front.  A workgroup writes
+// the tiles that lie whole in its share and leaves the sums of at most two others,
+// the first and the last, to join_kernel.  Every workgroup sums up the requests'
+// units for itself.
 template <typename E, int D, int NR, bool ONCE>
 __global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_flat_kernel(AttendArgs A) {
   constexpr uint32_t kThreads = kAttendWaves * 64, kRows = NR * 16;
