@@ -101,8 +101,9 @@ def draw(rng):
         batch, hi, q = rng.randint(1, 5), _log(rng, 600, 4000), rng.randint(16, 400)
         group = min(group, 4)
     elif kind == "whole":
-        batch, hi = rng.randint(1, 4), _log(rng, 40, 2000)
-        q, group = hi, min(group, 4)
+        batch, group = rng.randint(1, 4), min(group, 4)
+        hi = min(_log(rng, 40, 2000), int(math.sqrt(2.7e10 / (batch * kv * group * dim))))
+        q = hi
     else:
         batch = _log(rng, 1, 80)
         hi = min(_log(rng, 2, 90000), max(2, int(4e8 / (batch * kv * dim * 2))))
