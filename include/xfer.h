@@ -472,6 +472,71 @@ int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const xfer_attend
 int xfer_cache_attend(const xfer_cache_shape* shape, const void* cache, const xfer_attend* args,
                       void* stream);
 
+/* xfer_cache_load: a cache's tokens as rows again.  Request b has the rows starts[b]
+ * .. starts[b + 1) (of `rows`; none is below the one before) and lengths[b] tokens,
+ * of which those rows are the last: row j of r is token lengths[b] - r + j, as for
+ * xfer_cache_attend.  So a plan's starts give back the tokens that it added, and sums
+ * of the lengths whole contexts.  Its key and value, code * scale, are rounded
+ * once to dtype, to nearest even (bfloat16 and float hold all of them; in float16
+ * what is too large becomes infinite).  A token whose table entry lies outside the
+ * cache, or past the table's width, gives 0, and so does one below the first.  Rows
+ * of no request are left as they were.  The rows and heads of an output must not
+ * overlap, nor an output anything else of the call.
+ * Errors: INVALID_ARG (sizes outside their domains: batch below 2^27; NULL or
+ * misaligned buffers, strides that let an output's rows or heads overlap), HIP. */
+typedef struct {
+  void* key;   /* [rows][H][D] of dtype */
+  void* value; /* [rows][H][D] of dtype */
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* starts;
+  int64_t key_row, key_head, value_row, value_head, table_stride;
+  int batch, rows, table_width;
+  int dtype; /* xfer_dtype */
+} xfer_load;
+
+int xfer_cache_load(const xfer_cache_shape* shape, const void* cache, const xfer_load* args,
+                    void* stream);
+
+/* ------------------------------------------------------- cache in 4 bits
+ * The same cache with codes of 4 bits: half the bytes to hand over and to read.
+ * Block tables, slots and plans are those above, and xfer_run_blocks moves its blocks
+ * (of xfer_mxcache_block_bytes() bytes) too.
+ *
+ * A code is an e2m1 number: bit 3 the sign, bits 2 .. 0 one of 0, 0.5, 1, 1.5, 2, 3, 4
+ * and 6.  It stands for code * 2^(s - 127), s a byte that the 32 dims 32 i .. 32 i + 31 of a
+ * token's key, or of its value, in one head have in common (9 .. 252, or 255 where
+ * some of them are not finite: all 32 are NaN then).  2^(s - 127) is the smallest power of
+ * two, 2^-118 at least and 2^125 at most, of which the largest magnitude is 7 times
+ * or less: a number up to 7 is at most as far from 6 as it may be from another code.
+ * A record holds, for each of the H heads, the key codes, then the value codes,
+ * T * D / 2 bytes each; then the bytes s, [H][2][D / 32][T] (0 for keys, 1 for values);
+ * then zero to 127 bytes up to a multiple of 128.
+ *   Keys: [T][D / 2]; byte j of a token holds dim 2 j in its bits 3 .. 0, dim 2 j + 1
+ * in its bits 7 .. 4.
+ *   Values: the dims are divided into parts of 64 (D = 64), 64 and 32 (96), 128 (128), 128
+ * and 64 (192), or 128 and 128 (256), one behind the other.  A part of P dims takes
+ * T * P / 2 bytes, [T / u][16][u][b] with b = P / 32 and u = 16 / b: byte k of [i][n][j] holds
+ * dims 2 (b n + k) and 2 (b n + k) + 1 of the part and of token i u + j, as above.
+ *
+ * xfer_mxcache_store: as xfer_cache_store, but every token has scales of its own:
+ * rows may come in any order, and what is stored is never rounded again.  The
+ * slots of a call must differ (-1 and others outside the cache apart).  Numbers
+ * are rounded to nearest even, and to 6 * 2^125 where they are beyond it.
+ * xfer_mxcache_load, xfer_mxcache_attend: as xfer_cache_load, xfer_cache_attend (keys
+ * for codes and their largest scale, in what has to fit a float: the products of a
+ * query and a key, scores, and up to 256 times the values that a row sees). */
+int xfer_mxcache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
+int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, const void* key, int64_t key_row,
+                       int64_t key_head, const void* value, int64_t value_row, int64_t value_head,
+                       int dtype, const int32_t* slots, int rows, void* stream);
+int xfer_mxcache_load(const xfer_cache_shape* shape, const void* cache, const xfer_load* args,
+                      void* stream);
+int xfer_mxcache_attend_workspace(const xfer_cache_shape* shape, const xfer_attend* args,
+                                  size_t* bytes);
+int xfer_mxcache_attend(const xfer_cache_shape* shape, const void* cache, const xfer_attend* args,
+                        void* stream);
+
 /* --------------------------------------------------------------- inspect */
 /* Synchronous read of one channel's control words (lane 0 reported; the
  * lanes_agree field compares the others) and of the sticky error.  The

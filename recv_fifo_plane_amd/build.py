@@ -4,14 +4,17 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libxfer.so")
 SOURCES = [os.path.join(CSRC, f)
-           for f in ("kernels.hip", "noalloc.hip", "cache.hip", "conn.cpp", "relay.cpp", "sched.cpp")]
+           for f in ("cache.hip", "mxcache.hip", "kernels.hip", "noalloc.hip", "conn.cpp", "relay.cpp",
+                    "sched.cpp")]
 HEADERS = [os.path.join(CSRC, "xfer_internal.h"), os.path.join(CSRC, "relay.h"),
+           os.path.join(CSRC, "cache_common.h"),
            os.path.join(ROOT, "include", "xfer.h")]
 ARCH = os.environ.get("XFER_OFFLOAD_ARCH", "gfx950")
 
@@ -42,15 +45,16 @@ def build(verbose: bool = False) -> str:
     """Compile every source and link libxfer.so next to this file."""
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
+    objs, cmds = [], []
     for src in SOURCES:
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         flags = COMMON + (DEVICE if src.endswith(".hip") else HOST)
-        cmd = [HIPCC] + flags + ["-c", src, "-o", obj]
+        cmds.append([HIPCC] + flags + ["-c", src, "-o", obj])
         if verbose:
-            print(" ".join(cmd))
-        _run(cmd)
+            print(" ".join(cmds[-1]))
         objs.append(obj)
+    with ThreadPoolExecutor(4) as pool:  # (the longest sources come first)
+        list(pool.map(_run, cmds))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs + ["-lhsa-runtime64", "-lpthread"]
     if verbose:

@@ -1,10 +1,11 @@
-"""A paged cache of keys and values in 8 bits, whose blocks a connection moves.
+"""A paged cache of keys and values in 8 or 4 bits, whose blocks a connection moves.
 
 The endpoint that runs a prompt plans room for its tokens (plan_blocks), stores
 their keys and values (PagedCache.store) and sends the blocks
 (PagedCache.send); the endpoint that answers attends to them
-(PagedCache.attend).  Argument checks and marshalling only: the work is that of
-the library's HIP kernels (xfer_cache_* and xfer_run_blocks in include/xfer.h).
+(PagedCache.attend), or reads them back as rows (PagedCache.load).  Argument checks
+and marshalling only: the work is that of the library's HIP kernels (xfer_cache_*,
+xfer_mxcache_* and xfer_run_blocks in include/xfer.h).
 """
 from __future__ import annotations
 
@@ -213,13 +214,27 @@ def plan_blocks(cached, added, table, free, block_tokens: int, rows: int, out=No
     return out
 
 
+_Names = namedtuple("_Names", "block_bytes store load attend_workspace attend")
+
+
 class PagedCache:
     """A pool of cache blocks in GPU memory: uint8 [blocks, block_bytes]."""
 
+    bits = 8
+    # The library's functions for codes of 8 and of 4 bits.
+    _NAMES = {bits: _Names(*("xfer_%s_%s" % (kind, name) for name in _Names._fields))
+              for bits, kind in ((8, "cache"), (4, "mxcache"))}
+
     def __init__(self, blocks: int, block_tokens: int, kv_heads: int, head_dim: int, device=None,
-                 buffer=None):
-        """buffer: a contiguous uint8 tensor [blocks, block_bytes] to use, else zeros."""
+                 buffer=None, bits: int = 8):
+        """buffer: a contiguous uint8 tensor [blocks, block_bytes] to use, else zeros.
+
+        bits: 8 holds e4m3 numbers with a scale per block and head, 4 holds e2m1
+        numbers with a scale per token, head and 32 dims (half the bytes)."""
         import torch
+        if bits not in self._NAMES:
+            raise ValueError("PagedCache: bits must be 8 or 4, got %r" % (bits,))
+        self.bits = int(bits)
         self.blocks, self.block_tokens, self.kv_heads, self.head_dim = (
             _int(v, "PagedCache: " + what) for v, what in
             ((blocks, "blocks"), (block_tokens, "block_tokens"), (kv_heads, "kv_heads"),
@@ -227,7 +242,7 @@ class PagedCache:
         self._shape = X.xfer_cache_shape(self.block_tokens, self.kv_heads, self.head_dim,
                                          self.blocks)
         n = C.c_size_t()
-        X.check(X.lib().xfer_cache_block_bytes(C.byref(self._shape), C.byref(n)))
+        X.check(getattr(X.lib(), self._NAMES[self.bits].block_bytes)(C.byref(self._shape), C.byref(n)))
         self.block_bytes = n.value
         if buffer is None:
             buffer = torch.zeros(self.blocks, self.block_bytes, dtype=torch.uint8,
@@ -242,26 +257,34 @@ class PagedCache:
         self.device = buffer.device.index
         self._ref, self._base = C.byref(self._shape), buffer.data_ptr()
 
+    def _of_8_bits(self, what):
+        if self.bits != 8:
+            raise ValueError("%s: codes of 4 bits share bytes, and their scales are a token's own; "
+                             "load() gives what they stand for" % what)
+
     def _view(self, dtype, shape, strides, at):
         b = self.buffer.view(dtype)
         return b.as_strided(shape, strides, b.storage_offset() + at)
 
     def keys(self):
-        """Key codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view)."""
+        """Key codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view; 8 bits)."""
+        self._of_8_bits("keys")
         import torch
         h, t, d = self.kv_heads, self.block_tokens, self.head_dim
         return self._view(torch.float8_e4m3fn, (self.blocks, h, t, d),
                           (self.block_bytes, 2 * t * d, d, 1), 0)
 
     def values(self):
-        """Value codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view)."""
+        """Value codes, float8_e4m3fn [blocks, kv_heads, block_tokens, head_dim] (a view; 8 bits)."""
+        self._of_8_bits("values")
         import torch
         h, t, d = self.kv_heads, self.block_tokens, self.head_dim
         return self._view(torch.float8_e4m3fn, (self.blocks, h, t, d),
                           (self.block_bytes, 2 * t * d, 1, t), t * d)
 
     def scales(self):
-        """Scales of keys and values, float32 [blocks, kv_heads, 2] (a view)."""
+        """Scales of keys and values, float32 [blocks, kv_heads, 2] (a view; 8 bits)."""
+        self._of_8_bits("scales")
         import torch
         h, t, d = self.kv_heads, self.block_tokens, self.head_dim
         return self._view(torch.float32, (self.blocks, h, 2), (self.block_bytes // 4, 2, 1),
@@ -278,8 +301,53 @@ class PagedCache:
         v, v_row, v_head = _rows(value, "store: value", (dtype,), self.device, rows, self.kv_heads,
                                  self.head_dim)
         at = _list(slots, "store: slots", rows, self.device)
-        _call(self.device, stream, X.lib().xfer_cache_store, self._ref, self._base, k, k_row, k_head,
+        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].store), self._ref, self._base, k, k_row, k_head,
               v, v_row, v_head, kinds[dtype], at, rows)
+
+    def load(self, table, lengths, starts, rows: int, dtype=None, out=None, stream=None):
+        """Keys and values of the cache's tokens as packed rows [rows, kv_heads,
+        head_dim] (bfloat16, float16 or float32; bfloat16 if dtype is None).
+
+        Request b has the rows starts[b] .. starts[b + 1) and lengths[b] tokens, of
+        which those rows are the last, as in attend: a plan's starts give the
+        tokens that it added, sums of the lengths whole contexts.  table: int32
+        [batch, width].  out: (key, value) to write into (any strides of rows and
+        heads), else new tensors.  Tokens that the table lacks give 0; rows of no
+        request are left as they were (without `out`: undefined)."""
+        kinds = _kinds()
+        rows = int(rows)
+        if rows < 0:
+            raise ValueError("load: rows must not be negative")
+        if rows > _MOST:
+            _int(rows, "load: rows")
+        at_lengths = _list(lengths, "load: lengths", None, self.device)
+        batch = lengths.shape[0]
+        at_starts = _list(starts, "load: starts", batch + 1, self.device)
+        at_table, stride, width = _table(table, "load: table", batch, self.device)
+        shape = (rows, self.kv_heads, self.head_dim)
+        if out is None:
+            if dtype is None:
+                import torch
+                dtype = torch.bfloat16
+            if dtype not in kinds:
+                raise TypeError("load: unsupported dtype %s" % (dtype,))
+            side = None if stream is None else _side(stream, self.device)
+            out = tuple(self.buffer.new_empty(shape, dtype=dtype) if side is None
+                        else _empty(self.buffer, shape, dtype, side) for _ in range(2))
+        else:
+            if len(out) != 2:
+                raise ValueError("load: out must be a key and a value tensor")
+            for t in out:
+                if getattr(t, "requires_grad", False) and _GRAD():
+                    raise ValueError("load: out requires a gradient; there is none of what is read")
+        key, value = out
+        k, k_row, k_head = _rows(key, "load: out key", kinds if dtype is None else (dtype,),
+                                 self.device, *shape)
+        v, v_row, v_head = _rows(value, "load: out value", (key.dtype,), self.device, *shape)
+        a = X.xfer_load(k, v, at_table, at_lengths, at_starts, k_row, k_head, v_row, v_head, stride,
+                        batch, rows, width, kinds[key.dtype])
+        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].load), self._ref, self._base, C.byref(a))
+        return key, value
 
     def attend(self, query, table, lengths, starts, scale=None, out=None, lse=False, max_query=0,
                max_length=0, stream=None):
@@ -332,15 +400,15 @@ class PagedCache:
                           heads, width, kinds[dtype],
                           1.0 / math.sqrt(d) if scale is None else float(scale), max_query,
                           max_length)
-        n, ref, lib = C.c_size_t(), C.byref(a), X.lib()
-        rc = lib.xfer_cache_attend_workspace(self._ref, ref, C.byref(n))
+        n, ref, lib, names = C.c_size_t(), C.byref(a), X.lib(), self._NAMES[self.bits]
+        rc = getattr(lib, names.attend_workspace)(self._ref, ref, C.byref(n))
         if rc:
             X.check(rc)
         if n.value:
             work = (query.new_empty(n.value, dtype=_UINT8) if side is None
                     else _empty(query, n.value, _UINT8, side, result=False))
             a.workspace, a.workspace_bytes = work.data_ptr(), n.value
-        _call(self.device, stream, lib.xfer_cache_attend, self._ref, self._base, ref)
+        _call(self.device, stream, getattr(lib, names.attend), self._ref, self._base, ref)
         return out if sums is None else (out, sums)
 
     def send(self, conn, dst, src_ids, dst_ids, stream=None) -> None:
@@ -348,6 +416,9 @@ class PagedCache:
         `dst` over a connection (as Conn.run_blocks does): int32 lists in GPU memory."""
         mine = (self.block_tokens, self.kv_heads, self.head_dim)
         other = (dst.block_tokens, dst.kv_heads, dst.head_dim)
+        if self.bits != dst.bits:
+            raise ValueError("send: blocks of %d bits cannot go into a cache of %d"
+                             % (self.bits, dst.bits))
         if mine != other:
             raise ValueError("send: blocks of shape %s cannot go into blocks of shape %s"
                              % (mine, other))

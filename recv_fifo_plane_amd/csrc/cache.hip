@@ -8,55 +8,33 @@
 // scale, a power of two: dequantising and rescaling by it are exact, and an
 // e4m3 number, which has an exponent of its own, gains nothing from a finer
 // scale.
-#include <hip/hip_runtime.h>
+#include "cache_common.h"
+
 #include <math.h>
-#include <stdint.h>
 #include <string.h>
 
-#include <algorithm>
-#include <string>
 #include <type_traits>
-#include <utility>
-
-#include "xfer.h"
 
 namespace xfer {
-
-void set_error(int code, const std::string& msg);  // conn.cpp
-
 namespace {
 
-int fail(int code, const std::string& msg) {
-  set_error(code, msg);
-  return code;
+// -------------------------------------------------------------------- form
+__device__ __forceinline__ uint64_t key_at(const Shape& s, uint32_t block, uint32_t h) {
+  return block * s.block_bytes + static_cast<uint64_t>(2u * h) * s.T * s.D;
+}
+__device__ __forceinline__ uint64_t value_at(const Shape& s, uint32_t block, uint32_t h) {
+  return key_at(s, block, h) + static_cast<uint64_t>(s.T) * s.D;
+}
+__device__ __forceinline__ uint64_t scales_at(const Shape& s, uint32_t block, uint32_t h) {
+  return block * s.block_bytes + 2ull * s.H * s.T * s.D + 8u * h;
 }
 
-int hip_fail(hipError_t e, const char* what) {
-  set_error(XFER_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-  return XFER_ERR_HIP;
+int shape8_of(const xfer_cache_shape* g, const char* who, Shape* out) {
+  const int rc = shape_of(g, who, out);
+  if (rc) return rc;
+  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
+  return XFER_OK;
 }
-
-template <typename Fn, typename Args>
-hipError_t launch(Fn fn, const Args& a, dim3 grid, int block, hipStream_t s) {
-  void* kargs[] = {const_cast<Args*>(&a)};
-  return hipLaunchKernel(reinterpret_cast<const void*>(fn), grid, dim3(block), kargs, 0, s);
-}
-
-// ------------------------------------------------------------------- shape
-struct Shape {
-  uint64_t block_bytes;
-  uint32_t T, H, D, blocks;
-  uint32_t log2T;
-  __device__ uint64_t key_at(uint32_t block, uint32_t h) const {
-    return block * block_bytes + static_cast<uint64_t>(2u * h) * T * D;
-  }
-  __device__ uint64_t value_at(uint32_t block, uint32_t h) const {
-    return key_at(block, h) + static_cast<uint64_t>(T) * D;
-  }
-  __device__ uint64_t scales_at(uint32_t block, uint32_t h) const {
-    return block * block_bytes + 2ull * H * T * D + 8u * h;
-  }
-};
 
 // -------------------------------------------------------------------- plan
 struct PlanArgs {
@@ -238,13 +216,6 @@ struct StoreArgs {
   Shape s;
 };
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16_t;
-typedef _Float16 fp16_t;
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 fp16x2 __attribute__((ext_vector_type(2)));
-
 // Smallest power of two, 2^-118 at least, that brings amax (finite) to 448 =
 // 1.75 * 2^8 or below.  amax = (1 + m / 2^23) * 2^(x - 127) from its bits; a
 // subnormal amax falls under the floor.
@@ -377,7 +348,7 @@ __device__ __forceinline__ void store_item(const StoreArgs& A, float* s_max, int
   const uint32_t tg = lane % TG, col = lane / TG;
   const bool active = col < W;
   const uint32_t base = wave % WV * P * kSpan;  // the wave's first place
-  float* held = reinterpret_cast<float*>(A.cache + A.s.scales_at(block, h)) + side;
+  float* held = reinterpret_cast<float*>(A.cache + scales_at(A.s, block, h)) + side;
   const int64_t row_stride = side ? A.value_row : A.key_row;
   // (of place 0, which may lie before the rows: only places of the run are read)
   const E* src = static_cast<const E*>(side ? A.value : A.key) +
@@ -414,7 +385,7 @@ __device__ __forceinline__ void store_item(const StoreArgs& A, float* s_max, int
       }
     }
   };
-  uint8_t* codes = A.cache + (side ? A.s.value_at(block, h) : A.s.key_at(block, h));
+  uint8_t* codes = A.cache + (side ? value_at(A.s, block, h) : key_at(A.s, block, h));
   float amax = 0.0f;
   bool strange = false;  // some element is not finite
   if constexpr (sizeof(E) == 2) {
@@ -597,44 +568,6 @@ StoreFn pick_store(uint32_t d, uint32_t t) {
 }
 
 // ------------------------------------------------------------------ attend
-// A tile of rows whose tokens several workgroups share, from w on to `last`.
-struct Begun {
-  int32_t request;  // -1: there is none
-  uint32_t tile, last, pad;
-};
-
-// The same value in every lane, known to the compiler as such.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-  return static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32 |
-         uniform(static_cast<uint32_t>(v));
-}
-
-struct AttendArgs {
-  const uint8_t* cache;
-  const void* query;
-  void* out;
-  float* lse;
-  const int32_t* table;
-  const int32_t* lengths;
-  const int32_t* starts;
-  // A launch whose workgroups share the tokens out evenly (flat > 0):
-  Begun* begun;     // [flat] the tile that a workgroup begins and does not finish
-  float* part;      // [workgroups][2][tile rows][D] sums of weighted values of begun tiles
-  float* stats;     // [workgroups][2][tile rows][2] their maxima and sums of weights
-  int64_t query_row, query_head, out_row, out_head, table_stride;
-  int32_t batch, rows, heads, width;
-  uint32_t group;         // query heads of one key/value head
-  uint32_t flat;          // workgroups of one key/value head, 0: one per tile of rows
-  uint32_t packed;        // tile numbers of one key/value head, 0: a grid of requests and tiles
-  float scale2;           // scale * log2(e): weights are powers of two
-  Shape s;
-};
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 fp16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 template <typename E>
 struct Vec8;
 template <>
@@ -661,80 +594,7 @@ __device__ __forceinline__ void widen(uint32_t lo, uint32_t hi, float scale, fp1
   const fp16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
   r = fp16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma(fp16x8 a, fp16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 
-constexpr int kAttendWaves = 4;
-constexpr int kChunk = 64;  // tokens a wave takes at once
-
-// The rows of one request and key/value head that a workgroup computes.
-struct RowTile {
-  int64_t start;  // first packed row of the request
-  int64_t ahead;  // tokens before its first row's own (negative: rows that see nothing)
-  int32_t seen;   // tokens that the tile's last row sees
-  uint32_t rows;  // rows times group
-};
-
-// Rows of request b that there are (a start below 0 has none).
-__device__ __forceinline__ uint32_t rows_of(const AttendArgs& A, uint32_t b) {
-  const int64_t start = A.starts[b], end = min<int64_t>(A.starts[b + 1], A.rows);
-  return start < 0 || end <= start ? 0u : static_cast<uint32_t>(end - start) * A.group;
-}
-
-__device__ __forceinline__ RowTile row_tile(const AttendArgs& A, uint32_t b, uint32_t first,
-                                            uint32_t tile_rows) {
-  RowTile r;
-  r.start = A.starts[b];
-  const int64_t queries = static_cast<int64_t>(A.starts[b + 1]) - r.start, length = A.lengths[b];
-  const int64_t held = min<int64_t>(length, static_cast<int64_t>(A.width) * A.s.T);
-  r.ahead = length - queries;
-  r.rows = rows_of(A, b);
-  const uint32_t last = min(r.rows, first + tile_rows);
-  r.seen = 0;
-  if (last > first)
-    r.seen = static_cast<int32_t>(
-        max<int64_t>(0, min<int64_t>(held, r.ahead + (last - 1) / A.group + 1)));
-  r.seen = __builtin_amdgcn_readfirstlane(r.seen);  // (the same in every lane)
-  r.rows = __builtin_amdgcn_readfirstlane(r.rows);
-  return r;
-}
-
-// Request b's tiles of rows and, for each of them, units of work: chunks of
-// its tokens (one at least, so that every row is written).  A tile that sees
-// fewer tokens has units that hold nothing.
-struct Units {
-  uint32_t tiles, chunks;
-  __device__ uint64_t all() const { return static_cast<uint64_t>(tiles) * chunks; }
-};
-
-__device__ __forceinline__ Units units_of(const AttendArgs& A, uint32_t b, uint32_t tile_rows) {
-  const int64_t held = min<int64_t>(A.lengths[b], static_cast<int64_t>(A.width) * A.s.T);
-  const uint32_t chunks = (static_cast<uint32_t>(max<int64_t>(1, held)) + kChunk - 1) / kChunk;
-  return Units{(rows_of(A, b) + tile_rows - 1) / tile_rows, chunks};
-}
-
-// A lane's blocks in a chunk: as the holder of scores and values of tokens
-// 16g .. (-1: none), and as a loader of key lines (line n is token 16 (n / 4) +
-// 4t + n % 4; any block where there is none).
-struct Place {
-  int32_t mine, line;
-  // (seen > 0; the entries of tokens past it are those of the last)
-  __device__ __forceinline__ void look(const AttendArgs& A, const int32_t* table, uint32_t t0,
-                                       uint32_t seen, uint32_t g, uint32_t n) {
-    mine = table[min(t0 + 16 * g, seen - 1) >> A.s.log2T];
-    line = table[min(t0 + 16 * (n >> 2), seen - 1) >> A.s.log2T];
-  }
-  __device__ __forceinline__ void settle(const AttendArgs& A, uint32_t t0, uint32_t seen, uint32_t g) {
-    if (static_cast<uint32_t>(mine) >= A.s.blocks || t0 + 16 * g >= seen) mine = -1;
-    if (static_cast<uint32_t>(line) >= A.s.blocks) line = 0;
-  }
-};
-
-// The dims of lane group g in step k of 32: sixteen-byte loads of the keys
 // serve two steps where D allows.
 template <int D>
 __device__ __forceinline__ uint32_t key_dim(uint32_t k, uint32_t g) {
@@ -742,14 +602,6 @@ __device__ __forceinline__ uint32_t key_dim(uint32_t k, uint32_t g) {
     return 64 * (k / 2) + 16 * g + 8 * (k % 2);
   else
     return 32 * k + 8 * g;
-}
-
-template <bool ONCE, typename V>
-__device__ __forceinline__ V fetch(const uint8_t* p) {
-  if constexpr (ONCE)
-    return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
-  else
-    return *reinterpret_cast<const V*>(p);
 }
 
 // A chunk's value codes and the scales of the lane's block.
@@ -760,8 +612,8 @@ struct Values {
   __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
                                        uint32_t g, uint32_t n) {
     const uint32_t block = max(at.mine, 0), T = A.s.T;
-    const uint8_t* p = A.cache + A.s.value_at(block, h) + n * T + ((t0 + 16 * g) & (T - 1));
-    const float* s = reinterpret_cast<const float*>(A.cache + A.s.scales_at(block, h));
+    const uint8_t* p = A.cache + value_at(A.s, block, h) + n * T + ((t0 + 16 * g) & (T - 1));
+    const float* s = reinterpret_cast<const float*>(A.cache + scales_at(A.s, block, h));
     key_scale = s[0];
     value_scale = s[1];
 #pragma unroll
@@ -785,7 +637,7 @@ struct Keys {
   __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
                                        uint32_t g, uint32_t n) {
     const uint32_t tk = t0 + 16 * (n >> 2);
-    const uint8_t* p = A.cache + A.s.key_at(at.line, h) +
+    const uint8_t* p = A.cache + key_at(A.s, at.line, h) +
                        ((tk & (A.s.T - 1)) + (n & 3u)) * D + (kWide ? 16 : 8) * g;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -824,7 +676,7 @@ __device__ __forceinline__ f32x4 seen_nans(const AttendArgs& A, const int32_t* t
   for (int32_t t = t0; t <= last; ++t) {
     const int32_t id = table[t >> A.s.log2T];
     if (static_cast<uint32_t>(id) >= A.s.blocks) continue;
-    const uint8_t* v = A.cache + A.s.value_at(id, h) + (t & (A.s.T - 1));
+    const uint8_t* v = A.cache + value_at(A.s, id, h) + (t & (A.s.T - 1));
 #pragma clang loop unroll(disable)
     for (uint32_t k = 0; k < 4; ++k)
       if ((v[static_cast<uint64_t>(d + k) * A.s.T] & 0x7F) == 0x7F) r[k] = NAN;
@@ -1158,205 +1010,27 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& A, AttendShared<D,
   }
 }
 
-// One workgroup per tile of rows and key/value head.  The last tiles see most
-// tokens and are begun first: with 32 heads of 128 over 8, 8 requests of 3000 to
-// 3900 tokens, 700 to 3000 of them new, take 1290 us and not 1390.
 template <typename E, int D, int NR, bool ONCE>
-__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_kernel(AttendArgs A) {
-  __shared__ AttendShared<D, NR> sh;
-  const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H;
-  const uint32_t tiles = units_of(A, b, NR * 16).tiles;
-  for (uint32_t y = blockIdx.y; y < tiles; y += gridDim.y)
-    attend_rows<E, D, NR, ONCE>(A, sh, b, h, (tiles - 1 - y) * NR * 16, 0, ~0u, nullptr, nullptr);
-}
-
-// Tiles numbered through the packed rows: with R rows a tile, request b's begin at
-// number first(b) = starts[b] * group / R + b, which leaves it as many as it can
-// need.  The request of number k, by a search with a lane per candidate: one trip
-// to memory for 64 requests, two for 4096.  (Starts outside the rows count as at
-// their ends, as rows_of has it.)
-__device__ __forceinline__ uint32_t first_tile(const AttendArgs& A, uint32_t b, uint32_t tile_rows) {
-  const uint32_t row = static_cast<uint32_t>(min(max(A.starts[b], 0), A.rows));
-  return row * A.group / tile_rows + b;
-}
-
-__device__ __forceinline__ uint32_t request_of(const AttendArgs& A, uint32_t k, uint32_t tile_rows) {
-  const uint32_t lane = threadIdx.x & 63u;
-  uint32_t lo = 0, n = A.batch;
-  while (n > 1) {
-    const uint32_t step = (n + 63) / 64, at = lane * step;
-    const bool there = at < n && first_tile(A, lo + at, tile_rows) <= k;
-    const uint32_t pos = max(static_cast<uint32_t>(__popcll(__ballot(there))), 1u) - 1;
-    lo += pos * step;
-    n = min(step, n - pos * step);
+struct Core {
+  typedef E Elem;
+  typedef AttendShared<D, NR> Shared;
+  static constexpr int kDim = D, kRows = NR * 16, kResident = attend_resident(D, NR);
+  static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
+                                              uint32_t first, uint32_t c0, uint32_t c1, float* part,
+                                              float* stats) {
+    attend_rows<E, D, NR, ONCE>(A, sh, b, h, first, c0, c1, part, stats);
   }
-  return uniform(lo);
-}
-
-// As attend_kernel, a workgroup per number and key/value head.
-template <typename E, int D, int NR>
-__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_packed_kernel(AttendArgs A) {
-  constexpr uint32_t kRows = NR * 16;
-  __shared__ AttendShared<D, NR> sh;
-  const uint32_t h = blockIdx.x % A.s.H;
-  for (uint32_t k = blockIdx.x / A.s.H; k < A.packed; k += gridDim.x / A.s.H) {
-    const uint32_t b = request_of(A, k, kRows), y = uniform(k - first_tile(A, b, kRows));
-    const uint32_t tiles = units_of(A, b, kRows).tiles;
-    if (y < tiles)  // (a number may be one that its request, or none, does not need)
-      attend_rows<E, D, NR, false>(A, sh, b, h, (tiles - 1 - y) * kRows, 0, ~0u, nullptr, nullptr);
-  }
-}
-
-// The chunks of all requests and tiles in one line, cut into equal shares for
-// as many workgroups per key/value head as the GPU holds: requests of very
-// different lengths, or few long ones, keep every CU busy to the end.  Every tile
-// of a request counts all of its chunks, those past the tile's last row too:
-// shares are even where few rows follow many tokens, while for a whole prompt
-// half of the units are skipped, most of them at its front.  A workgroup writes
-// the tiles that lie whole in its share and leaves the sums of at most two others,
-// the first and the last, to join_kernel.  Every workgroup sums up the requests'
-// units for itself.
-template <typename E, int D, int NR, bool ONCE>
-__global__ void __launch_bounds__(kAttendWaves * 64, attend_resident(D, NR)) attend_flat_kernel(AttendArgs A) {
-  constexpr uint32_t kThreads = kAttendWaves * 64, kRows = NR * 16;
-  __shared__ AttendShared<D, NR> sh;
-  __shared__ uint64_t s_pre[kThreads], s_wave[kAttendWaves];
-  const uint32_t h = blockIdx.x % A.s.H, w = blockIdx.x / A.s.H, tid = threadIdx.x;
-  const uint32_t batch = A.batch, seg = (batch + kThreads - 1) / kThreads;
-  const uint32_t b0 = min(batch, tid * seg), b1 = min(batch, b0 + seg);
-  uint64_t sum = 0;
-  for (uint32_t b = b0; b < b1; ++b) sum += units_of(A, b, kRows).all();
-  uint64_t run = sum;  // inclusive over the wave's lanes
-  for (uint32_t d = 1; d < 64; d <<= 1) {
-    const uint64_t o = __shfl_up(static_cast<unsigned long long>(run), d);
-    if ((tid & 63u) >= d) run += o;
-  }
-  if ((tid & 63u) == 63u) s_wave[tid >> 6] = run;
-  __syncthreads();
-  uint64_t pre = run - sum, all = 0;
-  for (uint32_t k = 0; k < kAttendWaves; ++k) {
-    if (k < (tid >> 6)) pre += s_wave[k];
-    all += s_wave[k];
-  }
-  s_pre[tid] = pre;
-  __syncthreads();
-  all = uniform(all);
-  const uint64_t flat = min<uint64_t>(A.flat, all);  // (so every share holds a unit)
-  if (h == 0 && tid == 0) A.begun[w].request = -1;
-  if (w >= flat) return;
-  const uint64_t lo = all * w / flat, hi = all * (w + 1) / flat;
-  uint32_t first = 0, last = kThreads;  // the last segment that begins at or before lo
-  while (last - first > 1) {
-    const uint32_t mid = (first + last) / 2;
-    if (s_pre[mid] <= lo)
-      first = mid;
-    else
-      last = mid;
-  }
-  uint32_t b = uniform(first) * seg;
-  uint64_t u = lo, at = uniform(s_pre[first]);  // the unit to do, the request's first
-  Units q = units_of(A, b, kRows);
-  for (;;) {
-    while (at + q.all() <= u && b + 1 < batch) {  // (u < all: a request with units follows)
-      at = uniform(at + q.all());
-      q = units_of(A, ++b, kRows);
-    }
-    q.chunks = uniform(q.chunks);
-    const uint32_t y = uniform(static_cast<uint32_t>((u - at) / q.chunks));
-    const uint64_t begin = at + static_cast<uint64_t>(y) * q.chunks, end = begin + q.chunks;
-    const uint64_t to = min(hi, end);
-    const bool whole = begin >= lo && end <= hi;
-    if (end > hi && begin >= lo && h == 0 && tid == 0)
-      A.begun[w] = Begun{static_cast<int32_t>(b), y, static_cast<uint32_t>((end * flat - 1) / all), 0};
-    const uint32_t slot = (blockIdx.x * 2 + (begin >= lo ? 1 : 0)) * kRows;
-    attend_rows<E, D, NR, ONCE>(A, sh, b, h, y * kRows, static_cast<uint32_t>(u - begin),
-                                static_cast<uint32_t>(to - begin),
-                                whole ? nullptr : A.part + static_cast<uint64_t>(slot) * D,
-                                A.stats + slot * 2);
-    u = to;
-    if (u == hi) return;
-  }
-}
-
-constexpr int kJoinThreads = 256;
-
-// Joins the sums of the tiles that several workgroups shared: workgroup (w, h)
-// that of the tile which share w begins and later ones go on with, D / 4
-// threads for a row, the shares in order, so the result does not depend on
-// when they were done.  Bound by latency: 4.6 us behind 64 requests' decode
-// step, 9.4 where 2 long ones are spread over 512 workgroups, 6.8 for chunks.
-template <typename E, int D, int NR>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
-  constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide, kRows = NR * 16;
-  const uint32_t w = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, d = tid % kWide;
-  const Begun t = A.begun[w];
-  if (t.request < 0 || tid >= kGroups * kWide) return;
-  const uint32_t rows = rows_of(A, t.request);
-  const int64_t start = A.starts[t.request];
-  const uint32_t r = blockIdx.z * kGroups + tid / kWide, i = t.tile * kRows + r;
-  if (r >= kRows || i >= rows) return;
-  // the first share's second place, the later ones' first
-  const uint64_t p0 = (static_cast<uint64_t>(w * A.s.H + h) * 2 + 1) * kRows + r;
-  const uint64_t step = 2ull * A.s.H * kRows, p1 = p0 - kRows + step;
-  float top = -INFINITY, sum = 0.0f;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr uint32_t kTake = 8;  // shares taken together: their loads are in flight at once
-  for (uint32_t k0 = 0; k0 <= t.last - w; k0 += kTake) {
-    float m[kTake], l[kTake];
-    f32x4 v[kTake];
-#pragma unroll
-    for (uint32_t k = 0; k < kTake; ++k) {
-      const bool there = k0 + k <= t.last - w;
-      const uint64_t p = k0 + k == 0 || !there ? p0 : p1 + (k0 + k - 1) * step;
-      m[k] = there ? A.stats[p * 2] : -INFINITY;
-      l[k] = there ? A.stats[p * 2 + 1] : 0.0f;
-      v[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (there) v[k] = *reinterpret_cast<const f32x4*>(A.part + p * D + 4 * d);
-    }
-    const float was = top;
-#pragma unroll
-    for (uint32_t k = 0; k < kTake; ++k) top = fmaxf(top, m[k]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float keep = __builtin_amdgcn_exp2f(was - base);
-    sum *= keep;
-    o *= keep;
-#pragma unroll
-    for (uint32_t k = 0; k < kTake; ++k) {
-      const float f = __builtin_amdgcn_exp2f(m[k] - base);
-      sum += l[k] * f;
-      o += v[k] * f;
-    }
-  }
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  const int64_t row = start + i / A.group;
-  const uint32_t head = h * A.group + i % A.group;
-  E v[4];
-  for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
-  __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + 4 * d, v, 8);
-  if (d == 0 && A.lse)
-    A.lse[row * A.heads + head] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
-}
-
-using AttendFn = void (*)(AttendArgs);
-struct AttendKernels {
-  AttendFn attend, packed, flat, join;
 };
 
-template <typename E, int D, int NR, bool ONCE>
-AttendKernels attend_of() {
-  if constexpr (D * NR > 256)  // (sharing needs registers that are not there)
-    return {attend_kernel<E, D, NR, ONCE>, attend_packed_kernel<E, D, NR>, nullptr, nullptr};
-  else
-    return {attend_kernel<E, D, NR, ONCE>, attend_packed_kernel<E, D, NR>,
-            attend_flat_kernel<E, D, NR, ONCE>, join_kernel<E, D, NR>};
-}
+
 
 template <typename E, int D>
 AttendKernels pick_attend_rows(int nr, bool once) {
   if constexpr (D != 192) {
-    if (nr == 2) return attend_of<E, D, 2, false>();
+    if (nr == 2) return attend_kernels<Core<E, D, 2, false>, Core<E, D, 2, false>, (2 * D <= 256)>();
   }
-  return once ? attend_of<E, D, 1, true>() : attend_of<E, D, 1, false>();
+  return once ? attend_kernels<Core<E, D, 1, true>, Core<E, D, 1, false>, true>()
+              : attend_kernels<Core<E, D, 1, false>, Core<E, D, 1, false>, true>();
 }
 
 template <typename E>
@@ -1369,16 +1043,6 @@ AttendKernels pick_attend(uint32_t d, int nr, bool once) {
     default: return pick_attend_rows<E, 256>(nr, once);
   }
 }
-
-// The launch of a call: row tiles of a workgroup, and how the work is shared.
-struct AttendPlan {
-  int nr;
-  uint32_t tiles;  // of a request
-  uint32_t flat;   // AttendArgs::flat
-  uint32_t packed; // AttendArgs::packed
-};
-
-constexpr int64_t kEmptyWorkgroups = 16384;
 
 AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   AttendPlan p;
@@ -1394,16 +1058,17 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   // 2210.  Heads of 256: 48 drafts 39 / 48, a prompt of 100 12.6 / 16.8 (200 tiles),
   // 256 drafts 86 / 63 (1024), 2 prompts of 1000 208 / 151 (4000), 8 with up to 600
   // rows 439 / 548, 8 prompts of 3000 4140 / 2770.
-  p.nr = rows <= 16 || s.D == 192 ? 1 : 2;
-  if (s.D == 256 && q.batch * int64_t(s.H) * ((rows + 15) / 16) <= 1024) p.nr = 1;
-  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.nr * 16 - 1) / (p.nr * 16)));
+  int nr = rows <= 16 || s.D == 192 ? 1 : 2;
+  if (s.D == 256 && q.batch * int64_t(s.H) * ((rows + 15) / 16) <= 1024) nr = 1;
+  p.tile = nr * 16;
+  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + nr * 16 - 1) / (nr * 16)));
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
   // Tiles that the packed rows can have, and so workgroups of one head (first_tile).
-  const int64_t numbers = int64_t(q.rows) * group / (p.nr * 16) + q.batch;
-  const int64_t resident = 256 * attend_resident(int(s.D), p.nr);  // workgroups on 256 CUs
+  const int64_t numbers = int64_t(q.rows) * group / (nr * 16) + q.batch;
+  const int64_t resident = 256 * attend_resident(int(s.D), nr);  // workgroups on 256 CUs
   // Sharing costs a second launch and about 8 us; it pays where few workgroups
   // would be left with long requests.  Measured at 8 key/value heads of 128,
   // group 4, one workgroup per tile against shared (us): 1 request of 1024
@@ -1419,7 +1084,7 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   // from 12 on there are enough of them, whatever the lengths.
   p.flat = p.packed = 0;
   const bool enough = most > 1 && numbers * s.H > 12 * resident;
-  if (!enough && chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * p.nr <= 256) {
+  if (!enough && chunks >= (wgs <= 128 ? 24 : 64) && int(s.D) * nr <= 256) {
     // As many workgroups as are resident at once, eight chunks each at least.
     p.flat = uint32_t(std::max<int64_t>(
         1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
@@ -1435,61 +1100,6 @@ AttendPlan attend_plan(const Shape& s, const xfer_attend& q) {
   return p;
 }
 
-// The workspace: the begun tiles, their sums and the sums' statistics.
-struct AttendWork {
-  size_t begun, part, stats;
-  size_t all() const { return begun + part + stats; }
-};
-
-AttendWork attend_work(const Shape& s, const xfer_attend& q, const AttendPlan& p) {
-  if (!p.flat) return AttendWork{0, 0, 0};
-  const size_t tiles = size_t(p.flat) * s.H * 2 * size_t(p.nr) * 16;
-  return AttendWork{size_t(p.flat) * sizeof(Begun), tiles * s.D * sizeof(float),
-                    tiles * 2 * sizeof(float)};
-}
-
-// ------------------------------------------------------------------ checks
-constexpr int kMaxHeads = 1024;
-constexpr uint64_t kMaxGrid = (1u << 24) - 1;  // workgroups of 256 threads: 2^32 threads at most
-
-int shape_of(const xfer_cache_shape* g, const char* who, Shape* out) {
-  if (!g) return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": NULL shape");
-  if (g->block_tokens != 16 && g->block_tokens != 32 && g->block_tokens != 64)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": block_tokens must be 16, 32 or 64");
-  if (g->kv_heads < 1 || g->kv_heads > kMaxHeads)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": kv_heads must be 1..1024");
-  if (g->head_dim != 64 && g->head_dim != 96 && g->head_dim != 128 && g->head_dim != 192 &&
-      g->head_dim != 256)
-    return fail(XFER_ERR_INVALID_ARG,
-                std::string(who) + ": head_dim must be 64, 96, 128, 192 or 256");
-  if (g->blocks < 1 || int64_t(g->blocks) * g->block_tokens > 0x7FFFFFFFll)
-    return fail(XFER_ERR_INVALID_ARG,
-                std::string(who) + ": blocks must be >= 1 and hold at most 2^31 - 1 tokens");
-  out->T = uint32_t(g->block_tokens);
-  out->log2T = out->T == 16 ? 4 : out->T == 32 ? 5 : 6;
-  out->H = uint32_t(g->kv_heads);
-  out->D = uint32_t(g->head_dim);
-  out->blocks = uint32_t(g->blocks);
-  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
-  return XFER_OK;
-}
-
-// Whether vectors of `inner` elements, n0 times n1 of them with strides s0 and s1,
-// may share elements: they do not where the vectors of one dimension follow one
-// another and those of the other lie behind them all.
-bool vectors_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
-  typedef __int128 wide;
-  wide a = s0 < 0 ? -wide(s0) : wide(s0), b = s1 < 0 ? -wide(s1) : wide(s1);
-  if (n0 <= 1 || (n1 > 1 && a > b)) {
-    std::swap(n0, n1);
-    std::swap(a, b);
-  }
-  if (n0 <= 1) return false;
-  return a < inner || (n1 > 1 && b < a * (n0 - 1) + inner);
-}
-
-bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
 }  // namespace
 }  // namespace xfer
 
@@ -1497,7 +1107,7 @@ using namespace xfer;
 
 extern "C" int xfer_cache_block_bytes(const xfer_cache_shape* shape, size_t* bytes) {
   Shape s;
-  const int rc = shape_of(shape, "xfer_cache_block_bytes", &s);
+  const int rc = shape8_of(shape, "xfer_cache_block_bytes", &s);
   if (rc) return rc;
   if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_cache_block_bytes: NULL bytes");
   *bytes = size_t(s.block_bytes);
@@ -1544,7 +1154,7 @@ extern "C" int xfer_cache_store(const xfer_cache_shape* shape, void* cache, cons
                                 int64_t value_row, int64_t value_head, int dtype,
                                 const int32_t* slots, int rows, void* stream) {
   StoreArgs a;
-  const int rc = shape_of(shape, "xfer_cache_store", &a.s);
+  const int rc = shape8_of(shape, "xfer_cache_store", &a.s);
   if (rc) return rc;
   if (dtype != XFER_BF16 && dtype != XFER_FP16 && dtype != XFER_FP32)
     return fail(XFER_ERR_INVALID_ARG, "xfer_cache_store: unknown dtype");
@@ -1587,37 +1197,11 @@ extern "C" int xfer_cache_store(const xfer_cache_shape* shape, void* cache, cons
   return XFER_OK;
 }
 
-namespace {
-
-int attend_args(const xfer_cache_shape* shape, const xfer_attend* q, const char* who, Shape* s) {
-  const int rc = shape_of(shape, who, s);
-  if (rc) return rc;
-  if (!q) return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": NULL arguments");
-  if (q->batch < 0 || q->rows < 0 || q->table_width < 0 || q->table_stride < q->table_width)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": need batch, rows and table_width >= 0 "
-                                                         "and table_stride >= table_width");
-  if (q->heads < 1 || q->heads > 16 * kMaxHeads || q->heads % shape->kv_heads)
-    return fail(XFER_ERR_INVALID_ARG,
-                std::string(who) + ": heads must be a multiple of kv_heads, at most 16384");
-  if (int64_t(q->rows) * q->heads > 0x7FFFFFFFll)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": rows * heads must stay below 2^31");
-  if (uint64_t(q->batch) * uint64_t(shape->kv_heads) > kMaxGrid)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": batch * kv_heads must stay below 2^24");
-  if (q->dtype != XFER_BF16 && q->dtype != XFER_FP16)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": dtype must be BF16 or FP16");
-  if (!(q->scale > 0.0f) || !(q->scale <= 3.402823466e38f))
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": scale must be positive and finite");
-  if (q->max_query < 0 || q->max_length < 0)
-    return fail(XFER_ERR_INVALID_ARG, std::string(who) + ": max_query and max_length must be >= 0");
-  return XFER_OK;
-}
-
-}  // namespace
-
 extern "C" int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const xfer_attend* q,
                                            size_t* bytes) {
   Shape s;
-  const int rc = attend_args(shape, q, "xfer_cache_attend_workspace", &s);
+  int rc = shape8_of(shape, "xfer_cache_attend_workspace", &s);
+  if (!rc) rc = attend_args(s, q, "xfer_cache_attend_workspace");
   if (rc) return rc;
   if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_cache_attend_workspace: NULL bytes");
   *bytes = attend_work(s, *q, attend_plan(s, *q)).all();
@@ -1626,73 +1210,21 @@ extern "C" int xfer_cache_attend_workspace(const xfer_cache_shape* shape, const 
 
 extern "C" int xfer_cache_attend(const xfer_cache_shape* shape, const void* cache,
                                  const xfer_attend* q, void* stream) {
-  AttendArgs a;
-  const int rc = attend_args(shape, q, "xfer_cache_attend", &a.s);
+  Shape s;
+  int rc = shape8_of(shape, "xfer_cache_attend", &s);
+  if (!rc) rc = attend_args(s, q, "xfer_cache_attend");
   if (rc) return rc;
   if (q->rows == 0 || q->batch == 0) return XFER_OK;
-  if (!cache || !q->query || !q->out || !q->lengths || !q->starts ||
-      (q->table_width > 0 && !q->table))
-    return fail(XFER_ERR_INVALID_ARG, "xfer_cache_attend: NULL buffer with rows to compute");
-  if (!aligned(cache, 16) || !aligned(q->query, 2) || !aligned(q->out, 2) || !aligned(q->lse, 4) ||
-      !aligned(q->table, 4) || !aligned(q->lengths, 4) || !aligned(q->starts, 4))
-    return fail(XFER_ERR_INVALID_ARG,
-                "xfer_cache_attend: the cache must be 16-byte aligned, the others by their type");
-  if (vectors_overlap(q->rows, q->out_row, q->heads, q->out_head, a.s.D))
-    return fail(XFER_ERR_INVALID_ARG,
-                "xfer_cache_attend: the rows and heads of out must not overlap");
-  a.cache = static_cast<const uint8_t*>(cache);
-  a.query = q->query;
-  a.out = q->out;
-  a.lse = q->lse;
-  a.table = q->table;
-  a.lengths = q->lengths;
-  a.starts = q->starts;
-  a.query_row = q->query_row;
-  a.query_head = q->query_head;
-  a.out_row = q->out_row;
-  a.out_head = q->out_head;
-  a.table_stride = q->table_stride;
-  a.batch = q->batch;
-  a.rows = q->rows;
-  a.heads = q->heads;
-  a.width = q->table_width;
-  a.group = uint32_t(q->heads) / a.s.H;
-  a.scale2 = q->scale * 1.44269504088896341f;
-  const AttendPlan p = attend_plan(a.s, *q);
-  a.flat = p.flat;
-  a.packed = p.packed;
-  const AttendWork work = attend_work(a.s, *q, p);
-  if (p.flat && (!q->workspace || q->workspace_bytes < work.all() || !aligned(q->workspace, 16)))
-    return fail(XFER_ERR_INVALID_ARG,
-                "xfer_cache_attend: the workspace must hold xfer_cache_attend_workspace() bytes, "
-                "16-byte aligned");
-  uint8_t* mem = static_cast<uint8_t*>(q->workspace);
-  a.begun = reinterpret_cast<Begun*>(mem);
-  a.part = reinterpret_cast<float*>(mem + work.begun);
-  a.stats = reinterpret_cast<float*>(mem + work.begun + work.part);
   // With one tile a request no other workgroup reads the same tokens (but for
   // requests that share blocks), and loads that leave the caches alone serve long
   // even reads better (us, with against without): 64 single rows over 4000 tokens
   // each, 8 heads of 128, 92 / 99; 2 over 65k and 131k 84 / 92; 128 over 3500, heads
   // of 64, 76 / 85.  Where latency counts they lose: 48 over 100 .. 3000, heads of
   // 256, 42.6 / 38.4; 100 over 300, heads of 192, 17.3 / 15.2.
-  const bool once = p.tiles == 1;
-  const AttendKernels k = q->dtype == XFER_BF16 ? pick_attend<bf16_t>(a.s.D, p.nr, once)
-                                                : pick_attend<fp16_t>(a.s.D, p.nr, once);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e;
-  if (p.packed) {
-    const uint64_t most = kMaxGrid / a.s.H;
-    e = launch(k.packed, a, dim3(uint32_t(std::min<uint64_t>(p.packed, most)) * a.s.H), kAttendWaves * 64, s);
-  } else if (!p.flat) {
-    e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles), kAttendWaves * 64, s);
-  } else {
-    e = launch(k.flat, a, dim3(p.flat * a.s.H), kAttendWaves * 64, s);
-    if (e == hipSuccess) {
-      const uint32_t rows = uint32_t(kJoinThreads) / (a.s.D / 4);  // of a join workgroup
-      e = launch(k.join, a, dim3(p.flat, a.s.H, (uint32_t(p.nr) * 16 + rows - 1) / rows), kJoinThreads, s);
-    }
-  }
-  if (e != hipSuccess) return hip_fail(e, "xfer_cache_attend launch");
-  return XFER_OK;
+  const auto pick = [&](int dtype, const AttendPlan& p) {
+    const int nr = p.tile / 16;
+    const bool once = p.tiles == 1;
+    return dtype == XFER_BF16 ? pick_attend<bf16_t>(s.D, nr, once) : pick_attend<fp16_t>(s.D, nr, once);
+  };
+  return attend_call(s, cache, q, attend_plan(s, *q), pick, stream, "xfer_cache_attend");
 }

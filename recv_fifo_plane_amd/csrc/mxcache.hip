@@ -1,0 +1,1089 @@
+// gfx950 kernels of the paged 4-bit cache: stores and attention, and the reading
+// back of either cache.  Their entry points (xfer_mxcache_*, xfer_cache_load) are at
+// the end of the file.
+//
+// A block is one record of bytes: per key/value head the key codes, then the value
+// codes, T * D / 2 bytes each, and behind the heads a byte of scale for each head,
+// side (key, value), 32 dims and token, [H][2][D / 32][T], padded to 128 bytes.  A
+// code is an e2m1 number, a scale byte s stands for 2^(s - 127), 255 for 32 dims
+// of which some are not finite.  So a token's codes and scales are its own:
+// storing one never touches another's, whatever the order of the rows, and
+// nothing is rounded twice.
+//
+// Keys lie as [T][D / 2], dim 2j in the lower half of byte j: sixteen bytes are 32
+// dims of a token, which is what a lane of the matrix instruction's left operand takes
+// of a head of 128, with one scale.  Values lie in parts of 128, 64 or 32 dims as
+// D is made of (96 = 64 + 32, 192 = 128 + 64): a sixteenth of the part's dims, b = 4,
+// 2 or 1 bytes, of u = 16 / b tokens together, [T / u][16][u][b].  A lane then loads
+// sixteen tokens of its dims in pieces of sixteen bytes, and one scale serves all
+// dims that it has of a token.
+#include "cache_common.h"
+
+#include <math.h>
+
+#include <type_traits>
+
+namespace xfer {
+namespace {
+
+// -------------------------------------------------------------------- form
+// The parts that the dims of a head are divided into.
+constexpr int part_count(int d) { return d == 64 || d == 128 ? 1 : 2; }
+constexpr int part_dims(int d, int p) {
+  return p == 0 ? (d >= 128 ? 128 : 64) : d == 96 ? 32 : d == 192 ? 64 : 128;
+}
+constexpr int part_at(int d, int p) { return p == 0 ? 0 : part_dims(d, 0); }
+
+__device__ __forceinline__ uint64_t keys4_at(const Shape& s, uint32_t block, uint32_t h) {
+  return block * s.block_bytes + static_cast<uint64_t>(h) * s.T * s.D;
+}
+__device__ __forceinline__ uint64_t values4_at(const Shape& s, uint32_t block, uint32_t h) {
+  return keys4_at(s, block, h) + s.T * s.D / 2;
+}
+// Of a side's dims 32 * group .. 32 * group + 31.
+__device__ __forceinline__ uint64_t scales4_at(const Shape& s, uint32_t block, uint32_t h, uint32_t side,
+                                               uint32_t group) {
+  return block * s.block_bytes + static_cast<uint64_t>(s.H) * s.T * s.D +
+         ((2 * h + side) * (s.D / 32) + group) * s.T;
+}
+
+int shape4_of(const xfer_cache_shape* g, const char* who, Shape* out) {
+  const int rc = shape_of(g, who, out);
+  if (rc) return rc;
+  const uint64_t codes = uint64_t(out->H) * out->T * out->D;
+  out->block_bytes = codes + ((codes / 16 + 127) & ~127ull);
+  return XFER_OK;
+}
+
+int shape8_of(const xfer_cache_shape* g, const char* who, Shape* out) {
+  const int rc = shape_of(g, who, out);
+  if (rc) return rc;
+  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
+  return XFER_OK;
+}
+
+// The power of two that a byte of w (0 the lowest) stands for; NaN for 255, as
+// the conversions take it.
+__device__ __forceinline__ float power_of(uint32_t w, uint32_t byte) {
+  return __uint_as_float((w >> (8 * byte) & 255u) << 23);
+}
+
+// The two numbers of a byte of w, times scale: exact in bfloat16 and float for
+// the scales of a cache, rounded to nearest even in float16.
+__device__ __forceinline__ bf16x2 two_bf16(uint32_t w, int byte, float scale) {
+  switch (byte) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  }
+}
+template <typename E>
+__device__ __forceinline__ void eight_of(uint32_t w, float scale, E (&out)[8]) {
+  if constexpr (__is_same(E, bf16_t)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x2 p = two_bf16(w, j, scale);
+      out[2 * j] = p[0];
+      out[2 * j + 1] = p[1];
+    }
+  } else if constexpr (__is_same(E, fp16_t)) {
+    const fp16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0);
+    const fp16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1);
+    const fp16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2);
+    const fp16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3);
+    const E all[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    __builtin_memcpy(out, all, sizeof(all));
+  } else {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 0);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 1);
+    const auto c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 2);
+    const auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, 3);
+    const E all[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    __builtin_memcpy(out, all, sizeof(all));
+  }
+}
+
+// Byte j of the four words, as word j.
+__device__ __forceinline__ void transpose(const uint32_t (&w)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// ------------------------------------------------------------------- store
+struct Store4Args {
+  uint8_t* cache;
+  const void* key;
+  const void* value;
+  int64_t key_row, key_head, value_row, value_head;  // strides in elements
+  const int32_t* slots;
+  int32_t rows;
+  Shape s;
+};
+
+// Exponent of the smallest power of two, 2^-118 to 2^125, that brings a magnitude
+// (its bits, finite) to 7 = 1.75 * 2^2 or below.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 23) - 127 - 2 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, -118), 125);
+}
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// Largest of x in four neighbouring lanes.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t x) {
+  x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xF, 0xF, true)));
+  return max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xF, 0xF, true)));
+}
+
+// Eight neighbouring dims of a row.
+template <typename E>
+struct Piece {
+  uint32_t w[2 * sizeof(E)];
+
+  // Bits of the largest magnitude, as a float's (magnitudes are ordered as their
+  // bits are, those that are not finite last).
+  __device__ __forceinline__ uint32_t largest() const {
+    if constexpr (sizeof(E) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      u16x2 m = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
+      const uint16_t most = max(m[0], m[1]);
+      return __float_as_uint(static_cast<float>(__builtin_bit_cast(E, most)));
+    }
+  }
+  // Their codes, dim j in bits 4j ..: divided by scale (a power of two) and rounded to
+  // nearest even in one step, at most 6.
+  __device__ __forceinline__ uint32_t codes(float scale) const {
+    uint32_t r = 0;
+    if constexpr (__is_same(E, bf16_t)) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[0]), scale, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[1]), scale, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[2]), scale, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[3]), scale, 3);
+    } else if constexpr (__is_same(E, fp16_t)) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(fp16x2, w[0]), scale, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(fp16x2, w[1]), scale, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(fp16x2, w[2]), scale, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(fp16x2, w[3]), scale, 3);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[0]), __uint_as_float(w[1]), scale, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[2]), __uint_as_float(w[3]), scale, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[4]), __uint_as_float(w[5]), scale, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[6]), __uint_as_float(w[7]), scale, 3);
+    }
+    return r;
+  }
+};
+
+// Offset of dims 8 * piece .. of token t among a head's value codes: unit i of the
+// value_units(piece) that eight dims are in.
+template <int D>
+__device__ __forceinline__ uint32_t value_unit_at(uint32_t T, uint32_t piece, uint32_t i, uint32_t t) {
+  const uint32_t d = 8 * piece, p = part_count(D) > 1 && d >= part_dims(D, 0) ? 1 : 0;
+  const uint32_t at = p ? part_at(D, 1) : 0, dims = p ? part_dims(D, 1) : part_dims(D, 0);
+  const uint32_t b = dims / 32, u = 16 / b, n = (d - at) / (dims / 16) + i;
+  return T * at / 2 + t / u * 256 + n * 16 + t % u * b;
+}
+
+constexpr int kStoreThreads = 256;
+
+// A thread takes eight dims of one head and side of a row: four neighbours have
+// the 32 that share a scale.  The rows' dims are numbered one after the other,
+// keys before values, and a workgroup takes the next EACH * 256 pieces of eight.
+// (the first kernel, simple: figures follow)
+template <typename E, int D, int EACH>
+__global__ void __launch_bounds__(kStoreThreads) store4_kernel(Store4Args A) {
+  constexpr uint32_t W = D / 8;
+  const uint32_t side_pieces = A.s.H * W, row_pieces = 2 * side_pieces;
+  const uint64_t base = static_cast<uint64_t>(blockIdx.x) * (kStoreThreads * EACH);
+  const uint64_t row0 = base / row_pieces;
+  const uint32_t rest = static_cast<uint32_t>(base - row0 * row_pieces) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const uint32_t q = rest + i * kStoreThreads, ahead = q / row_pieces;
+    const uint32_t side = q - ahead * row_pieces >= side_pieces ? 1 : 0;
+    const uint32_t c = q - ahead * row_pieces - side * side_pieces, h = c / W, piece = c % W;
+    const uint64_t row = row0 + ahead;
+    if (row >= static_cast<uint64_t>(A.rows)) continue;
+    const int32_t slot = A.slots[row];
+    const E* src = static_cast<const E*>(side ? A.value : A.key) +
+                   static_cast<int64_t>(row) * (side ? A.value_row : A.key_row) +
+                   static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
+    Piece<E> x;
+    __builtin_memcpy(&x, src, sizeof(x));
+    const uint32_t most = max_of_four(x.largest());
+    const uint32_t block = static_cast<uint32_t>(slot) >> A.s.log2T, t = static_cast<uint32_t>(slot) & (A.s.T - 1);
+    if (slot < 0 || block >= A.s.blocks) continue;
+    const bool fine = most < 0x7F800000u;
+    const uint32_t e = fine ? static_cast<uint32_t>(exponent_of(most) + 127) : 255u;
+    const uint32_t codes = fine ? x.codes(__uint_as_float(e << 23)) : 0u;
+    if (side == 0) {
+      *reinterpret_cast<uint32_t*>(A.cache + keys4_at(A.s, block, h) + t * (D / 2) + 4 * piece) = codes;
+    } else {
+      uint8_t* v = A.cache + values4_at(A.s, block, h);
+      if (D >= 128 && (D != 192 || piece < 16)) {
+        *reinterpret_cast<uint32_t*>(v + value_unit_at<D>(A.s.T, piece, 0, t)) = codes;
+      } else if (D != 96 || piece < 8) {
+        *reinterpret_cast<uint16_t*>(v + value_unit_at<D>(A.s.T, piece, 0, t)) = static_cast<uint16_t>(codes);
+        *reinterpret_cast<uint16_t*>(v + value_unit_at<D>(A.s.T, piece, 1, t)) = static_cast<uint16_t>(codes >> 16);
+      } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) v[value_unit_at<D>(A.s.T, piece, k, t)] = static_cast<uint8_t>(codes >> (8 * k));
+      }
+    }
+    if (piece % 4 == 0) A.cache[scales4_at(A.s, block, h, side, piece / 4) + t] = static_cast<uint8_t>(e);
+  }
+}
+
+using Store4Fn = void (*)(Store4Args);
+
+template <typename E, int EACH>
+Store4Fn pick_store4(uint32_t d) {
+  switch (d) {
+    case 64: return store4_kernel<E, 64, EACH>;
+    case 96: return store4_kernel<E, 96, EACH>;
+    case 128: return store4_kernel<E, 128, EACH>;
+    case 192: return store4_kernel<E, 192, EACH>;
+    default: return store4_kernel<E, 256, EACH>;
+  }
+}
+
+// -------------------------------------------------------------------- load
+struct LoadArgs {
+  const uint8_t* cache;
+  void* key;
+  void* value;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* starts;
+  int64_t key_row, key_head, value_row, value_head, table_stride;
+  int32_t batch, rows, width;
+  uint32_t numbers;  // of tiles
+  Shape s;
+};
+
+constexpr int kLoadThreads = 256;
+constexpr int kLoadTile = 16;  // tokens, the first a multiple of it
+
+// Tiles numbered through the packed rows: request b's begin at number first(b) =
+// starts[b] / 16 + 2 b.  Its rows, n of them, touch (n + 14) / 16 + 1 tiles at most, which
+// is n / 16 + 2 or less.
+__device__ __forceinline__ uint32_t first_load(const LoadArgs& A, uint32_t b) {
+  return static_cast<uint32_t>(min(max(A.starts[b], 0), A.rows)) / kLoadTile + 2 * b;
+}
+
+// Four tokens' codes of eight dims of one side, and their scales.
+template <int BITS, int D>
+struct Quad;
+
+template <int D>
+struct Quad<4, D> {
+  uint32_t w[4], s;
+  __device__ __forceinline__ void load(const Shape& S, const uint8_t* cache, uint32_t block, uint32_t h,
+                                       uint32_t side, uint32_t piece, uint32_t t) {
+    s = *reinterpret_cast<const uint32_t*>(cache + scales4_at(S, block, h, side, piece / 4) + t);
+    if (side == 0) {
+      const uint8_t* k = cache + keys4_at(S, block, h) + t * (D / 2) + 4 * piece;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(k + j * (D / 2));
+      return;
+    }
+    const uint8_t* v = cache + values4_at(S, block, h);
+    if (D >= 128 && (D != 192 || piece < 16)) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(v + value_unit_at<D>(S.T, piece, 0, t));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = x[j];
+    } else if (D != 96 || piece < 8) {
+      const u32x2 a = *reinterpret_cast<const u32x2*>(v + value_unit_at<D>(S.T, piece, 0, t));
+      const u32x2 b = *reinterpret_cast<const u32x2*>(v + value_unit_at<D>(S.T, piece, 1, t));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = __builtin_amdgcn_perm(b[j / 2], a[j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+    } else {
+      uint32_t x[4];
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint32_t*>(v + value_unit_at<D>(S.T, piece, j, t));
+      transpose(x, w);
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ void rows(int j, E (&out)[8]) const {
+    eight_of<E>(w[j], power_of(s, j), out);
+  }
+};
+
+template <int D>
+struct Quad<8, D> {
+  uint32_t w[4][2];
+  float s;
+  __device__ __forceinline__ void load(const Shape& S, const uint8_t* cache, uint32_t block, uint32_t h,
+                                       uint32_t side, uint32_t piece, uint32_t t) {
+    const uint8_t* p = cache + block * S.block_bytes;
+    s = reinterpret_cast<const float*>(p + 2ull * S.H * S.T * D)[2 * h + side];
+    p += (2ull * h + side) * S.T * D;
+    if (side == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const u32x2 x = *reinterpret_cast<const u32x2*>(p + (t + j) * D + 8 * piece);
+        w[j][0] = x[0];
+        w[j][1] = x[1];
+      }
+      return;
+    }
+    uint32_t x[2][4], y[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) x[k / 4][k % 4] = *reinterpret_cast<const uint32_t*>(p + (8 * piece + k) * S.T + t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      transpose(x[i], y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j][i] = y[j];
+    }
+  }
+  template <typename E>
+  __device__ __forceinline__ void rows(int j, E (&out)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = w[j][i];
+      if constexpr (__is_same(E, bf16_t)) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true);
+        const E all[4] = {a[0], a[1], b[0], b[1]};
+        __builtin_memcpy(out + 4 * i, all, sizeof(all));
+      } else if constexpr (__is_same(E, fp16_t)) {
+        const fp16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, s, false);
+        const fp16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, s, true);
+        const E all[4] = {a[0], a[1], b[0], b[1]};
+        __builtin_memcpy(out + 4 * i, all, sizeof(all));
+      } else {
+        const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(x, s, false);
+        const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(x, s, true);
+        const E all[4] = {a[0], a[1], b[0], b[1]};
+        __builtin_memcpy(out + 4 * i, all, sizeof(all));
+      }
+    }
+  }
+};
+
+// A workgroup takes a tile of a request's tokens and, of the tile's keys and values,
+// its share: a thread four tokens of eight dims at a time, neighbours the
+// neighbouring dims, so that rows are written in long pieces.
+template <int BITS, typename E, int D>
+__global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs A) {
+  constexpr uint32_t W = D / 8;
+  const uint32_t lane = threadIdx.x & 63u;
+  for (uint32_t k = blockIdx.x; k < A.numbers; k += gridDim.x) {
+    // the last request that begins at or before number k, by a lane per candidate
+    uint32_t b = 0, n = A.batch;
+    while (n > 1) {
+      const uint32_t step = (n + 63) / 64, at = lane * step;
+      const bool there = at < n && first_load(A, b + at) <= k;
+      const uint32_t pos = max(static_cast<uint32_t>(__popcll(__ballot(there))), 1u) - 1;
+      b += pos * step;
+      n = min(step, n - pos * step);
+    }
+    b = uniform(b);
+    const int64_t start = A.starts[b], end = min<int64_t>(A.starts[b + 1], A.rows);
+    if (start < 0 || end <= start) continue;
+    // row start holds token ahead (it may be negative: then there is none)
+    const int64_t ahead = static_cast<int64_t>(A.lengths[b]) - (static_cast<int64_t>(A.starts[b + 1]) - start);
+    const int64_t tile = (ahead >> 4) + (k - first_load(A, b));
+    if (tile * kLoadTile >= ahead + (end - start)) continue;
+    const int64_t t0 = tile * kLoadTile, page = t0 >> A.s.log2T;
+    int32_t block = -1;
+    if (t0 >= 0 && page < A.width) block = A.table[b * A.table_stride + page];
+    if (static_cast<uint32_t>(block) >= A.s.blocks) block = -1;
+    const uint32_t off = static_cast<uint32_t>(t0) & (A.s.T - 1);
+    const uint32_t side_pieces = A.s.H * W, all = 2 * 4 * side_pieces;
+    for (uint32_t i = blockIdx.y * kLoadThreads + threadIdx.x; i < all; i += gridDim.y * kLoadThreads) {
+      const uint32_t quad = i / side_pieces & 3u, side = i / side_pieces >> 2, c = i % side_pieces;
+      const uint32_t h = c / W, piece = c % W;
+      Quad<BITS, D> q;
+      if (block >= 0) q.load(A.s, A.cache, static_cast<uint32_t>(block), h, side, piece, off + 4 * quad);
+      E* out = static_cast<E*>(side ? A.value : A.key) + static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
+      const int64_t stride = side ? A.value_row : A.key_row;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t row = start + t0 + 4 * quad + j - ahead;
+        if (row < start || row >= end) continue;
+        E x[8] = {};
+        if (block >= 0) q.rows(j, x);
+        __builtin_memcpy(out + row * stride, x, sizeof(x));
+      }
+    }
+  }
+}
+
+using LoadFn = void (*)(LoadArgs);
+
+template <int BITS, typename E>
+LoadFn pick_load_dim(uint32_t d) {
+  switch (d) {
+    case 64: return load_kernel<BITS, E, 64>;
+    case 96: return load_kernel<BITS, E, 96>;
+    case 128: return load_kernel<BITS, E, 128>;
+    case 192: return load_kernel<BITS, E, 192>;
+    default: return load_kernel<BITS, E, 256>;
+  }
+}
+
+template <int BITS>
+LoadFn pick_load(uint32_t d, int dtype) {
+  return dtype == XFER_BF16   ? pick_load_dim<BITS, bf16_t>(d)
+         : dtype == XFER_FP16 ? pick_load_dim<BITS, fp16_t>(d)
+                              : pick_load_dim<BITS, float>(d);
+}
+
+// ------------------------------------------------------------------ attend
+// Step k of 32 dims of the score product takes dims key4_dim(k, g) .. + 7 from lane
+// group g: a part's steps follow one another in the lane's load of it.
+template <int D>
+__device__ __forceinline__ uint32_t key4_dim(uint32_t k, uint32_t g) {
+  const uint32_t p = part_count(D) > 1 && k >= part_dims(D, 0) / 32 ? 1 : 0;
+  const uint32_t at = p ? part_at(D, 1) : 0, dims = p ? part_dims(D, 1) : part_dims(D, 0);
+  return at + dims / 4 * g + 8 * (k - at / 32);
+}
+
+template <bool ONCE, int WORDS>
+__device__ __forceinline__ void fetch_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (WORDS == 4) {
+    const u32x4 x = fetch<ONCE, u32x4>(p);
+    for (int i = 0; i < 4; ++i) w[i] = x[i];
+  } else if constexpr (WORDS == 2) {
+    const u32x2 x = fetch<ONCE, u32x2>(p);
+    for (int i = 0; i < 2; ++i) w[i] = x[i];
+  } else {
+    w[0] = fetch<ONCE, uint32_t>(p);
+  }
+}
+
+// f(part, its number as a constant) for every part of D.
+template <int D, typename F>
+__device__ __forceinline__ void each_part(F&& f) {
+  f(std::integral_constant<int, 0>());
+  if constexpr (part_count(D) > 1) f(std::integral_constant<int, 1>());
+}
+
+// A chunk's key codes and scales: tile t's line n of a lane.
+template <int D, bool ONCE>
+struct Keys4 {
+  uint32_t w[4][D / 32];
+  u32x4 s[part_count(D)];
+  __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
+                                       uint32_t g, uint32_t n) {
+    const uint32_t block = at.line, tk = (t0 + 16 * (n >> 2)) & (A.s.T - 1);
+    const uint8_t* k = A.cache + keys4_at(A.s, block, h) + (tk + (n & 3u)) * (D / 2);
+    const uint8_t* x = A.cache + scales4_at(A.s, block, h, 0, 0) + tk;
+    each_part<D>([&](auto part) {
+      constexpr int p = part.value, dims = part_dims(D, p), from = part_at(D, p);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        fetch_words<ONCE, dims / 32>(k + 4 * t * (D / 2) + from / 2 + dims / 8 * g, &w[t][from / 32]);
+      s[p] = fetch<ONCE, u32x4>(x + (from / 32 + g * (dims / 32) / 4) * A.s.T);
+    });
+  }
+};
+
+// A chunk's value codes and scales: sixteen tokens of a lane.
+template <int D, bool ONCE>
+struct Values4 {
+  u32x4 w[D / 32];
+  u32x4 s[part_count(D)];
+  __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, uint32_t t0, uint32_t h,
+                                       uint32_t g, uint32_t n) {
+    const uint32_t block = max(at.mine, 0), T = A.s.T, t = (t0 + 16 * g) & (T - 1);
+    const uint8_t* v = A.cache + values4_at(A.s, block, h) + n * 16;
+    const uint8_t* x = A.cache + scales4_at(A.s, block, h, 1, 0) + t;
+    each_part<D>([&](auto part) {
+      constexpr int p = part.value, dims = part_dims(D, p), from = part_at(D, p), b = dims / 32;
+#pragma unroll
+      for (int i = 0; i < b; ++i)
+        w[from / 32 + i] = fetch<ONCE, u32x4>(v + T * from / 2 + t * b * 16 + i * 256);
+      s[p] = fetch<ONCE, u32x4>(x + (from / 32 + n * b / 16) * T);
+    });
+  }
+};
+
+// Which of the parts' 32 dims that a lane holds results of have a token t0 .. last whose
+// values are not finite: NaN for those, else 0.  Rarely run, so it is a plain loop.
+template <int D>
+__device__ __forceinline__ void seen_nans4(const AttendArgs& A, const int32_t* table, uint32_t h, int32_t t0,
+                                           int32_t last, uint32_t g, float (&r)[part_count(D)]) {
+#pragma clang loop unroll(disable)
+  for (int32_t t = t0; t <= last; ++t) {
+    const int32_t id = table[t >> A.s.log2T];
+    if (static_cast<uint32_t>(id) >= A.s.blocks) continue;
+    each_part<D>([&](auto part) {
+      constexpr int p = part.value, dims = part_dims(D, p), from = part_at(D, p);
+      const uint32_t group = from / 32 + g * (dims / 32) / 4;
+      if (A.cache[scales4_at(A.s, id, h, 1, group) + (t & (A.s.T - 1))] == 255) r[p] = NAN;
+    });
+  }
+}
+
+// A float16 query as the sum of two bfloat16 numbers, exactly: it has 11 significant
+// bits, the rounded one takes 8 of them.
+__device__ __forceinline__ void two_parts(u32x4 q, u32x4& hi, u32x4& lo) {
+  const fp16x8 x = __builtin_bit_cast(fp16x8, q);
+  bf16x8 a, b;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = static_cast<float>(x[j]);
+    a[j] = static_cast<bf16_t>(v);
+    b[j] = static_cast<bf16_t>(fabsf(v) <= 65504.0f ? v - static_cast<float>(a[j]) : 0.0f);
+  }
+  hi = __builtin_bit_cast(u32x4, a);
+  lo = __builtin_bit_cast(u32x4, b);
+}
+
+__device__ __forceinline__ bf16x8 widen4(uint32_t w, float scale) {
+  bf16x8 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bf16x2 p = two_bf16(w, j, scale);
+    r[2 * j] = p[0];
+    r[2 * j + 1] = p[1];
+  }
+  return r;
+}
+
+// The weights of a chunk's scores s, in units of 1 / mul, as two bfloat16 numbers each:
+// p the rounded ones, p2 the rounded rests.  Maxima m, sums l and accumulators acc go
+// along.  MASK: some row does not see some token of the chunk; limit: the last token
+// that each row sees; tg: the lane's first of sixteen; bg: their block (below 0: none).
+template <bool MASK, int DT, int NR>
+__device__ __forceinline__ void weights_of(f32x4 (&s)[NR][4], f32x4 (&acc)[NR][DT], float (&m)[NR],
+                                           float (&l)[NR], const int32_t (&limit)[NR], float mul,
+                                           int32_t tg, int32_t bg, bf16x8 (&p)[NR][2],
+                                           bf16x8 (&p2)[NR][2]) {
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const int32_t seen = bg < 0 ? 0 : limit[x] - tg + 1;  // of this lane's sixteen tokens
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v = s[x][t][r] * mul;
+        if (MASK && 4 * t + r >= seen) v = -INFINITY;
+        s[x][t][r] = v;
+        top = fmaxf(top, v);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // The reference m follows the maximum only when that is 8 above it, so most
+    // chunks leave the accumulators alone: weights reach 256 at most, and the
+    // same powers of two leave sums and accumulators in the end.
+    const bool grows = top > m[x] + 8.0f;
+    const float next = grows ? top : m[x], base = next == -INFINITY ? 0.0f : next;
+    const float keep = grows ? __builtin_amdgcn_exp2f(m[x] - base) : 1.0f;
+    m[x] = next;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w = __builtin_amdgcn_exp2f(s[x][t][r] - base);
+        sum += w;
+        const bf16_t first = static_cast<bf16_t>(w);
+        p[x][t >> 1][(t & 1) * 4 + r] = first;
+        p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
+      }
+    l[x] = l[x] * keep + sum;
+    if (__ballot(grows) != 0) {
+#pragma unroll
+      for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+    }
+  }
+}
+
+// Writes the sixteen rows first .. of a request from what each wave of the workgroup
+// has of them: its sums of weighted values acc, relative to the rows' largest maximum
+// already, and its maxima m and sums l, `stride` from a wave's to the next's.  part
+// null: the rows of out and lse, else their sums to part and stats.
+template <typename E, int D>
+__device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&acc)[kAttendWaves][16][D + 4],
+                                           const float* m, const float* l, uint32_t stride,
+                                           const RowTile& rt, uint32_t h, uint32_t first, float* part,
+                                           float* stats) {
+  for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
+    const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + r;
+    const int64_t row = rt.start + ri / A.group;
+    if (ri >= rt.rows) continue;
+    float top = m[r], sum = 0.0f;
+    for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, m[w * stride + r]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = 0; w < kAttendWaves; ++w) {
+      sum += l[w * stride + r] * __builtin_amdgcn_exp2f(m[w * stride + r] - base);
+      o += *reinterpret_cast<const f32x4*>(&acc[w][r][d]);
+    }
+    const uint32_t head = h * A.group + ri % A.group;
+    const int64_t at = row * A.heads + head;
+    if (part == nullptr) {
+      const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+      E v[4];
+      for (int k = 0; k < 4; ++k) v[k] = static_cast<E>(o[k] * inv);
+      __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + d, v, 8);
+      if (d == 0 && A.lse)
+        A.lse[at] = (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+    } else {
+      *reinterpret_cast<f32x4*>(part + r * D + d) = o;
+      if (d == 0) {
+        stats[r * 2] = top;
+        stats[r * 2 + 1] = sum;
+      }
+    }
+  }
+}
+
+// The product of a chunk's weights p + p2 with the values.  A byte of codes gives two
+// dims of a token, the left operand wants eight tokens of a dim: two bytes of
+// neighbouring tokens, each widened with its own scale, and the halves put together.
+template <int D, int NR>
+__device__ __forceinline__ void weigh4(const u32x4 (&w)[D / 32], const u32x4 (&vs)[part_count(D)],
+                                       const bf16x8 (&p)[NR][2], const bf16x8 (&p2)[NR][2],
+                                       f32x4 (&acc)[NR][D / 16]) {
+  each_part<D>([&](auto part) {
+    constexpr int pt = part.value, dims = part_dims(D, pt), from = part_at(D, pt), b = dims / 32;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float scale[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) scale[k] = power_of(vs[pt][2 * s + k / 4], k % 4);
+#pragma unroll
+      for (int j = 0; j < b; ++j) {
+        u32x4 even, odd;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t c[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int byte = (8 * s + 2 * k + i) * b + j;
+            c[i] = __builtin_bit_cast(uint32_t, two_bf16(w[from / 32 + byte / 16][byte / 4 % 4], byte % 4, scale[2 * k + i]));
+          }
+          even[k] = __builtin_amdgcn_perm(c[1], c[0], 0x05040100u);
+          odd[k] = __builtin_amdgcn_perm(c[1], c[0], 0x07060302u);
+        }
+        const bf16x8 a = __builtin_bit_cast(bf16x8, even), z = __builtin_bit_cast(bf16x8, odd);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+          f32x4& e = acc[x][from / 16 + 2 * j];
+          f32x4& o = acc[x][from / 16 + 2 * j + 1];
+          e = mfma(a, p[x][s], e);
+          o = mfma(z, p[x][s], o);
+          e = mfma(a, p2[x][s], e);
+          o = mfma(z, p2[x][s], o);
+        }
+      }
+    }
+  });
+}
+
+// The scales of tokens that no row sees are replaced by 1, as they may be anything and 0
+// times infinity or NaN is NaN; so are the NaN of the others, which reach the rows
+// that see their token and no other: they are looked for again in memory at the end.
+__device__ __forceinline__ void mask_scales(u32x4& v, int32_t held, uint32_t& nans) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int left = held - 4 * w;
+    const uint32_t mask = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    const uint32_t nan = (((v[w] & 0x7F7F7F7Fu) + 0x01010101u) & v[w] & 0x80808080u & mask) >> 7;
+    nans |= nan;
+    const uint32_t keep = mask & ~(nan * 0xFFu);
+    v[w] = (v[w] & keep) | (0x7F7F7F7Fu & ~keep);
+  }
+}
+
+template <typename E, int D, int NR>
+struct Shared4 {
+  static constexpr int kQueries = __is_same(E, fp16_t) ? 2 : 1;  // bfloat16 numbers of one
+  union {
+    u32x4 q[kQueries][NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
+    float acc[kAttendWaves][16][D + 4];
+  };
+  float m[kAttendWaves][NR * 16], l[kAttendWaves][NR * 16];
+};
+
+constexpr int attend4_resident(int d, int nr) {
+  return nr == 1 ? (d <= 96 ? 3 : d <= 192 ? 2 : 1) : d <= 128 ? 2 : 1;
+}
+
+// Attention as over 8-bit codes (cache.hip's kernels have its mathematics: which token
+// sits where, one running maximum and sum a wave, weights in two bfloat16 numbers):
+// S^T = K Q^T and O^T = V^T P^T on the 16x16x32 matrix instruction, the cache's codes
+// the left operand, waves that take chunks of 64 tokens in turn.  What differs: scales
+// belong to a token's 32 dims, so keys and values are widened with them to
+// bfloat16, exactly; a float16 query goes in two bfloat16 numbers, exactly, since
+// keys need bfloat16's range; a lane's result tile e of a part holds dims b' n + e, the
+// b' dims that its sixteen-byte pieces have of each token.
+template <typename E, int D, int NR, bool ONCE>
+struct Core4 {
+  typedef E Elem;
+  typedef Shared4<E, D, NR> Shared;
+  static constexpr int kDim = D, kRows = NR * 16, kResident = attend4_resident(D, NR);
+
+  static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
+                                              uint32_t first, uint32_t c0, uint32_t c1, float* part,
+                                              float* stats) {
+    constexpr int KL = D / 32, DT = D / 16, NQ = Shared::kQueries;
+    const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
+    const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
+    const RowTile rt = row_tile(A, b, first, NR * 16);
+    c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
+
+    // (waves with no chunk load too, any block: behind a branch around the loads every
+    // wait of the loop would be one for all of them)
+    const uint32_t seen_all = uniform(static_cast<uint32_t>(rt.seen)), reach = max(seen_all, 1u);
+    if (seen_all == 0) table = A.starts;
+    uint32_t c = c0 + wave, nans = 0;
+    Keys4<D, ONCE> keys;
+    Values4<D, ONCE> vals;
+    Place at, next;
+    constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
+    at.look(A, table, c * kChunk, reach, g, n);
+    next.look(A, table, c * kChunk + kNext, reach, g, n);
+    __builtin_amdgcn_sched_barrier(0);
+
+    constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
+    int32_t limit[NR];        // last token that the row sees
+    int32_t least = rt.seen;  // the first of them
+    u32x4 q[NR][QL];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const uint32_t i = first + x * 16 + n;
+      const int64_t j = i / A.group, row = rt.start + j;
+      const bool there = i < rt.rows;
+      limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
+      const E* p = static_cast<const E*>(A.query) + row * A.query_row +
+                   static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
+#pragma unroll
+      for (int k = 0; k < QL; ++k) {
+        q[x][k] = u32x4{0u, 0u, 0u, 0u};
+        const uint32_t step = wave + k * kAttendWaves;
+        if (there && step < KL) __builtin_memcpy(&q[x][k], p + key4_dim<D>(step, g), 16);
+      }
+      if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
+    }
+    at.settle(A, c * kChunk, seen_all, g);
+    keys.load(A, at, c * kChunk, h, g, n);
+    __builtin_amdgcn_sched_barrier(0);
+    vals.load(A, at, c * kChunk, h, g, n);
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int k = 0; k < QL; ++k) {
+        const uint32_t step = wave + k * kAttendWaves;
+        if (step >= KL) continue;
+        if constexpr (NQ == 2) {
+          u32x4 hi, lo;
+          two_parts(q[x][k], hi, lo);
+          sh.q[0][x][step][lane] = hi;
+          sh.q[NQ - 1][x][step][lane] = lo;
+        } else {
+          sh.q[0][x][step][lane] = q[x][k];
+        }
+      }
+    for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+    least = __builtin_amdgcn_readfirstlane(least);
+    __syncthreads();
+
+    float m[NR], l[NR];
+    f32x4 acc[NR][DT];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x] = -INFINITY;
+      l[x] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // The order of loads is that of the 8-bit codes: the next chunk's keys once this
+    // one's scores are done, its values once this one's are used up.
+    auto step = [&](auto masked) {
+      constexpr bool MASK = decltype(masked)::value;
+      const uint32_t t0 = c * kChunk, tg = t0 + 16 * g, ahead = t0 + kNext;
+      const int32_t bg = at.mine;
+      f32x4 s[NR][4];
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < KL; ++k) {
+        constexpr int kFirst = part_dims(D, 0) / 32;
+        const int pt = k < kFirst ? 0 : part_count(D) - 1;
+        bf16x8 b8[NQ][NR];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+          for (int x = 0; x < NR; ++x) b8[i][x] = __builtin_bit_cast(bf16x8, sh.q[i][x][k][lane]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bf16x8 a = widen4(keys.w[t][k], power_of(keys.s[pt][t], n & 3u));
+#pragma unroll
+          for (int i = NQ - 1; i >= 0; --i)
+#pragma unroll
+            for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[i][x], s[x][t]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      next.settle(A, ahead, seen_all, g);
+      keys.load(A, next, ahead, h, g, n);
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 p[NR][2], p2[NR][2];
+      weights_of<MASK, DT, NR>(s, acc, m, l, limit, A.scale2, tg, bg, p, p2);
+      if constexpr (MASK) {
+        const int32_t held = bg < 0 ? 0 : static_cast<int32_t>(seen_all) - static_cast<int32_t>(tg);
+#pragma unroll
+        for (int k = 0; k < part_count(D); ++k) mask_scales(vals.s[k], held, nans);
+      }
+      weigh4<D, NR>(vals.w, vals.s, p, p2, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      at = next;
+      next.look(A, table, ahead + kNext, seen_all, g, n);
+      vals.load(A, at, ahead, h, g, n);
+      c += kAttendWaves;
+    };
+    // Chunks that every row sees whole, up to the first that is not; then the rest.
+    const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
+    while (c < whole && __ballot(at.mine < 0) == 0) step(std::false_type());
+    const uint32_t rest = c;
+    while (c < c1) step(std::true_type());
+    const bool any_nan = __ballot(nans != 0) != 0;
+
+    // Join the waves.
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      l[x] += __shfl_xor(l[x], 16);
+      l[x] += __shfl_xor(l[x], 32);
+      if (g == 0) {
+        sh.m[wave][x * 16 + n] = m[x];
+        sh.l[wave][x * 16 + n] = l[x];
+      }
+    }
+    __syncthreads();  // (and no wave needs the queries any more)
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      float top = sh.m[0][x * 16 + n];
+      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
+      const float f = __builtin_amdgcn_exp2f(m[x] - (top == -INFINITY ? 0.0f : top));
+      float nan[part_count(D)] = {};
+      if (any_nan) {
+#pragma clang loop unroll(disable)
+        for (uint32_t i = rest; i < c1; i += kAttendWaves)
+          seen_nans4<D>(A, table, h, i * kChunk, min(static_cast<int32_t>(i * kChunk) + kChunk - 1, limit[x]), g, nan);
+      }
+      // result tile e of a part, row 4g + r of it: dim dims / 16 * (4g + r) + e
+      each_part<D>([&](auto pt) {
+        constexpr int k = pt.value, wide = part_dims(D, k) / 16, from = part_at(D, k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < wide; ++e)
+            sh.acc[wave][n][from + wide * (4 * g + r) + e] = acc[x][from / 16 + e][r] * f + nan[k];
+      });
+      __syncthreads();
+      write_rows<E, D>(A, sh.acc, &sh.m[0][x * 16], &sh.l[0][x * 16], NR * 16, rt, h, first + x * 16,
+                       part ? part + x * 16 * D : nullptr, stats + x * 32);
+      __syncthreads();
+    }
+  }
+};
+
+template <typename E, int D>
+AttendKernels pick_attend4_rows(int nr, bool once) {
+  if (nr == 2) return attend_kernels<Core4<E, D, 2, false>, Core4<E, D, 2, false>, true>();
+  return once ? attend_kernels<Core4<E, D, 1, true>, Core4<E, D, 1, false>, true>()
+              : attend_kernels<Core4<E, D, 1, false>, Core4<E, D, 1, false>, true>();
+}
+
+template <typename E>
+AttendKernels pick_attend4(uint32_t d, int nr, bool once) {
+  switch (d) {
+    case 64: return pick_attend4_rows<E, 64>(nr, once);
+    case 96: return pick_attend4_rows<E, 96>(nr, once);
+    case 128: return pick_attend4_rows<E, 128>(nr, once);
+    case 192: return pick_attend4_rows<E, 192>(nr, once);
+    default: return pick_attend4_rows<E, 256>(nr, once);
+  }
+}
+
+// The launch of a call, by the rules of 8-bit codes for now.
+AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
+  AttendPlan p;
+  const int64_t group = q.heads / int(s.H);
+  int64_t most = q.max_query ? std::min(q.max_query, q.rows) : q.rows;
+  if (!q.max_query && q.rows <= q.batch) most = 1;
+  const int64_t rows = most * group;
+  const int nr = rows <= 16 ? 1 : 2;
+  p.tile = nr * 16;
+  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
+  const int64_t width = int64_t(q.table_width) * s.T;
+  const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
+  const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
+  const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
+  const int64_t numbers = int64_t(q.rows) * group / p.tile + q.batch;
+  const int64_t resident = 256 * attend4_resident(int(s.D), nr);
+  p.flat = p.packed = 0;
+  const bool enough = most > 1 && numbers * s.H > 12 * resident;
+  if (!enough && chunks >= (wgs <= 128 ? 24 : 64))
+    p.flat = uint32_t(std::max<int64_t>(
+        1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
+  if (!p.flat && wgs > numbers * s.H + kEmptyWorkgroups) p.packed = uint32_t(numbers);
+  return p;
+}
+
+}  // namespace
+}  // namespace xfer
+
+using namespace xfer;
+
+extern "C" int xfer_mxcache_block_bytes(const xfer_cache_shape* shape, size_t* bytes) {
+  Shape s;
+  const int rc = shape4_of(shape, "xfer_mxcache_block_bytes", &s);
+  if (rc) return rc;
+  if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_block_bytes: NULL bytes");
+  *bytes = size_t(s.block_bytes);
+  return XFER_OK;
+}
+
+extern "C" int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, const void* key,
+                                  int64_t key_row, int64_t key_head, const void* value,
+                                  int64_t value_row, int64_t value_head, int dtype,
+                                  const int32_t* slots, int rows, void* stream) {
+  Store4Args a;
+  const int rc = shape4_of(shape, "xfer_mxcache_store", &a.s);
+  if (rc) return rc;
+  if (dtype != XFER_BF16 && dtype != XFER_FP16 && dtype != XFER_FP32)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_store: unknown dtype");
+  if (rows < 0) return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_store: rows must be >= 0");
+  if (rows == 0) return XFER_OK;
+  if (!cache || !key || !value || !slots)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_store: NULL buffer with rows to store");
+  const size_t size = dtype == XFER_FP32 ? 4 : 2;
+  if (!aligned(cache, 16) || !aligned(slots, 4) || !aligned(key, size) || !aligned(value, size))
+    return fail(XFER_ERR_INVALID_ARG,
+                "xfer_mxcache_store: the cache must be 16-byte aligned, the others by their type");
+  a.cache = static_cast<uint8_t*>(cache);
+  a.key = key;
+  a.value = value;
+  a.key_row = key_row;
+  a.key_head = key_head;
+  a.value_row = value_row;
+  a.value_head = value_head;
+  a.slots = slots;
+  a.rows = rows;
+  const uint64_t pieces = uint64_t(rows) * a.s.H * 2 * (a.s.D / 8);
+  const uint64_t wgs = (pieces + kStoreThreads - 1) / kStoreThreads;
+  if (wgs > kMaxGrid)
+    return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_store: too many rows times heads for one call");
+  const Store4Fn fn = dtype == XFER_BF16   ? pick_store4<bf16_t, 1>(a.s.D)
+                      : dtype == XFER_FP16 ? pick_store4<fp16_t, 1>(a.s.D)
+                                           : pick_store4<float, 1>(a.s.D);
+  const hipError_t e = launch(fn, a, dim3(uint32_t(wgs)), kStoreThreads, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "xfer_mxcache_store launch");
+  return XFER_OK;
+}
+
+namespace {
+
+int load_call(const Shape& s, int bits, const void* cache, const xfer_load* q, void* stream, const char* who) {
+  const std::string w(who);
+  if (!q) return fail(XFER_ERR_INVALID_ARG, w + ": NULL arguments");
+  if (q->batch < 0 || q->rows < 0 || q->table_width < 0 || q->table_stride < q->table_width)
+    return fail(XFER_ERR_INVALID_ARG,
+                w + ": need batch, rows and table_width >= 0 and table_stride >= table_width");
+  if (q->batch > 0x7FFFFFF)
+    return fail(XFER_ERR_INVALID_ARG, w + ": batch must stay below 2^27");
+  if (q->dtype != XFER_BF16 && q->dtype != XFER_FP16 && q->dtype != XFER_FP32)
+    return fail(XFER_ERR_INVALID_ARG, w + ": unknown dtype");
+  if (q->rows == 0 || q->batch == 0) return XFER_OK;
+  if (!cache || !q->key || !q->value || !q->lengths || !q->starts || (q->table_width > 0 && !q->table))
+    return fail(XFER_ERR_INVALID_ARG, w + ": NULL buffer with rows to read back");
+  const size_t size = q->dtype == XFER_FP32 ? 4 : 2;
+  if (!aligned(cache, 16) || !aligned(q->key, size) || !aligned(q->value, size) || !aligned(q->table, 4) ||
+      !aligned(q->lengths, 4) || !aligned(q->starts, 4))
+    return fail(XFER_ERR_INVALID_ARG, w + ": the cache must be 16-byte aligned, the others by their type");
+  if (vectors_overlap(q->rows, q->key_row, s.H, q->key_head, s.D) ||
+      vectors_overlap(q->rows, q->value_row, s.H, q->value_head, s.D))
+    return fail(XFER_ERR_INVALID_ARG, w + ": the rows and heads of an output must not overlap");
+  LoadArgs a;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.key = q->key;
+  a.value = q->value;
+  a.table = q->table;
+  a.lengths = q->lengths;
+  a.starts = q->starts;
+  a.key_row = q->key_row;
+  a.key_head = q->key_head;
+  a.value_row = q->value_row;
+  a.value_head = q->value_head;
+  a.table_stride = q->table_stride;
+  a.batch = q->batch;
+  a.rows = q->rows;
+  a.width = q->table_width;
+  a.numbers = uint32_t(q->rows) / kLoadTile + 2u * uint32_t(q->batch);
+  a.s = s;
+  const uint32_t units = 2 * 4 * s.H * (s.D / 8), shares = (units + kLoadThreads - 1) / kLoadThreads;
+  const LoadFn fn = bits == 8 ? pick_load<8>(s.D, q->dtype) : pick_load<4>(s.D, q->dtype);
+  const uint32_t most = uint32_t(kMaxGrid / shares);
+  const hipError_t e = launch(fn, a, dim3(std::min(a.numbers, most), shares), kLoadThreads,
+                              static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, (w + " launch").c_str());
+  return XFER_OK;
+}
+
+}  // namespace
+
+extern "C" int xfer_mxcache_load(const xfer_cache_shape* shape, const void* cache, const xfer_load* args,
+                                 void* stream) {
+  Shape s;
+  const int rc = shape4_of(shape, "xfer_mxcache_load", &s);
+  return rc ? rc : load_call(s, 4, cache, args, stream, "xfer_mxcache_load");
+}
+
+extern "C" int xfer_cache_load(const xfer_cache_shape* shape, const void* cache, const xfer_load* args,
+                               void* stream) {
+  Shape s;
+  const int rc = shape8_of(shape, "xfer_cache_load", &s);
+  return rc ? rc : load_call(s, 8, cache, args, stream, "xfer_cache_load");
+}
+
+extern "C" int xfer_mxcache_attend_workspace(const xfer_cache_shape* shape, const xfer_attend* q,
+                                             size_t* bytes) {
+  Shape s;
+  int rc = shape4_of(shape, "xfer_mxcache_attend_workspace", &s);
+  if (!rc) rc = attend_args(s, q, "xfer_mxcache_attend_workspace");
+  if (rc) return rc;
+  if (!bytes) return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_attend_workspace: NULL bytes");
+  *bytes = attend_work(s, *q, attend4_plan(s, *q)).all();
+  return XFER_OK;
+}
+
+extern "C" int xfer_mxcache_attend(const xfer_cache_shape* shape, const void* cache,
+                                   const xfer_attend* q, void* stream) {
+  Shape s;
+  int rc = shape4_of(shape, "xfer_mxcache_attend", &s);
+  if (!rc) rc = attend_args(s, q, "xfer_mxcache_attend");
+  if (rc) return rc;
+  if (q->rows == 0 || q->batch == 0) return XFER_OK;
+  const auto pick = [&](int dtype, const AttendPlan& p) {
+    const int nr = p.tile / 16;
+    const bool once = p.tiles == 1;
+    return dtype == XFER_BF16 ? pick_attend4<bf16_t>(s.D, nr, once) : pick_attend4<fp16_t>(s.D, nr, once);
+  };
+  return attend_call(s, cache, q, attend4_plan(s, *q), pick, stream, "xfer_mxcache_attend");
+}

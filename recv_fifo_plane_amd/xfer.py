@@ -98,6 +98,13 @@ class xfer_attend(C.Structure):
                 + [("scale", C.c_float), ("max_query", C.c_int), ("max_length", C.c_int)])
 
 
+class xfer_load(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("key", "value", "table", "lengths", "starts")]
+                + [(n, C.c_int64) for n in ("key_row", "key_head", "value_row", "value_head",
+                                            "table_stride")]
+                + [(n, C.c_int) for n in ("batch", "rows", "table_width", "dtype")])
+
+
 class xfer_setup_op(C.Structure):
     _fields_ = [("kind", C.c_int), ("peer", C.c_int), ("channel", C.c_int)]
 
@@ -130,6 +137,15 @@ SIGNATURES = {
     "xfer_cache_attend_workspace": (C.c_int, [C.POINTER(xfer_cache_shape), C.POINTER(xfer_attend),
                                               C.POINTER(C.c_size_t)]),
     "xfer_cache_attend": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, C.POINTER(xfer_attend), _vp]),
+    "xfer_cache_load": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, C.POINTER(xfer_load), _vp]),
+    "xfer_mxcache_block_bytes": (C.c_int, [C.POINTER(xfer_cache_shape), C.POINTER(C.c_size_t)]),
+    "xfer_mxcache_store": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, _vp, C.c_int64, C.c_int64,
+                                     _vp, C.c_int64, C.c_int64, C.c_int, _vp, C.c_int, _vp]),
+    "xfer_mxcache_load": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, C.POINTER(xfer_load), _vp]),
+    "xfer_mxcache_attend_workspace": (C.c_int, [C.POINTER(xfer_cache_shape),
+                                                C.POINTER(xfer_attend), C.POINTER(C.c_size_t)]),
+    "xfer_mxcache_attend": (C.c_int, [C.POINTER(xfer_cache_shape), _vp, C.POINTER(xfer_attend),
+                                      _vp]),
     "xfer_conn_query": (C.c_int, [_vp, C.c_int, C.POINTER(xfer_chan_state)]),
     "xfer_conn_fifo": (C.c_int, [_vp, C.c_int, C.POINTER(_vp), C.POINTER(C.c_size_t)]),
     "xfer_conn_read_fifo": (C.c_int, [_vp, C.c_int, _vp, C.c_size_t]),
