@@ -1014,7 +1014,8 @@ template <typename E, int D, int NR, bool ONCE>
 struct Core {
   typedef E Elem;
   typedef AttendShared<D, NR> Shared;
-  static constexpr int kDim = D, kRows = NR * 16, kResident = attend_resident(D, NR);
+  static constexpr int kDim = D, kRows = NR * 16, kThreads = kAttendWaves * 64;
+  static constexpr int kResident = attend_resident(D, NR);
   static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
                                               uint32_t first, uint32_t c0, uint32_t c1, float* part,
                                               float* stats) {

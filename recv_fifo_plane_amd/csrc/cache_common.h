@@ -4,7 +4,8 @@
 //
 // A form's attention is a core: a type with
 //   Elem, kDim, kRows      the query's type, the head's dims, the rows of a tile
-//   kResident              workgroups a CU is to hold (bounds the registers of a lane)
+//   kThreads, kResident    threads of a workgroup, and how many of them a CU is to hold
+//                          (bounds the registers of a lane)
 //   Shared                 its shared memory
 //   rows(A, sh, b, h, first, c0, c1, part, stats)
 // where rows() computes the rows first .. first + kRows - 1 of request b and
@@ -87,7 +88,7 @@ struct AttendArgs {
   int32_t batch, rows, heads, width;
   uint32_t group;         // query heads of one key/value head
   uint32_t flat;          // workgroups of one key/value head, 0: one per tile of rows
-  uint32_t packed;        // tile numbers of one key/value head, 0: a grid of requests and tiles
+  uint32_t packed;        // tile numbers of one key/value head (flat == 0 and 0: a grid of requests and tiles)
   float scale2;           // scale * log2(e): weights are powers of two
   Shape s;
 };
@@ -183,7 +184,7 @@ __device__ __forceinline__ V fetch(const uint8_t* p) {
 // tokens and are begun first: with 32 heads of 128 over 8, 8 requests of 3000 to
 // 3900 tokens, 700 to 3000 of them new, take 1290 us and not 1390.
 template <class C>
-__global__ void __launch_bounds__(kAttendWaves * 64, C::kResident) attend_kernel(AttendArgs A) {
+__global__ void __launch_bounds__(C::kThreads, C::kResident) attend_kernel(AttendArgs A) {
   __shared__ typename C::Shared sh;
   const uint32_t h = blockIdx.x % A.s.H, b = blockIdx.x / A.s.H;
   const uint32_t tiles = units_of(A, b, C::kRows).tiles;
@@ -216,7 +217,7 @@ __device__ __forceinline__ uint32_t request_of(const AttendArgs& A, uint32_t k, 
 
 // As attend_kernel, a workgroup per number and key/value head.
 template <class C>
-__global__ void __launch_bounds__(kAttendWaves * 64, C::kResident) attend_packed_kernel(AttendArgs A) {
+__global__ void __launch_bounds__(C::kThreads, C::kResident) attend_packed_kernel(AttendArgs A) {
   constexpr uint32_t kRows = C::kRows;
   __shared__ typename C::Shared sh;
   const uint32_t h = blockIdx.x % A.s.H;
@@ -238,10 +239,10 @@ __global__ void __launch_bounds__(kAttendWaves * 64, C::kResident) attend_packed
 // the first and the last, to join_kernel.  Every workgroup sums up the requests'
 // units for itself.
 template <class C>
-__global__ void __launch_bounds__(kAttendWaves * 64, C::kResident) attend_flat_kernel(AttendArgs A) {
-  constexpr uint32_t kThreads = kAttendWaves * 64, kRows = C::kRows;
+__global__ void __launch_bounds__(C::kThreads, C::kResident) attend_flat_kernel(AttendArgs A) {
+  constexpr uint32_t kThreads = C::kThreads, kWaves = kThreads / 64, kRows = C::kRows;
   __shared__ typename C::Shared sh;
-  __shared__ uint64_t s_pre[kThreads], s_wave[kAttendWaves];
+  __shared__ uint64_t s_pre[kThreads], s_wave[kWaves];
   const uint32_t h = blockIdx.x % A.s.H, w = blockIdx.x / A.s.H, tid = threadIdx.x;
   const uint32_t batch = A.batch, seg = (batch + kThreads - 1) / kThreads;
   const uint32_t b0 = min(batch, tid * seg), b1 = min(batch, b0 + seg);
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kAttendWaves * 64, C::kResident) attend_flat_k
   if ((tid & 63u) == 63u) s_wave[tid >> 6] = run;
   __syncthreads();
   uint64_t pre = run - sum, all = 0;
-  for (uint32_t k = 0; k < kAttendWaves; ++k) {
+  for (uint32_t k = 0; k < kWaves; ++k) {
     if (k < (tid >> 6)) pre += s_wave[k];
     all += s_wave[k];
   }
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
 using AttendFn = void (*)(AttendArgs);
 struct AttendKernels {
   AttendFn attend, packed, flat, join;
+  int threads;  // of a workgroup but of join's
 };
 
 
@@ -367,9 +369,9 @@ template <class C, class P, bool SHARED>
 AttendKernels attend_kernels() {
   if constexpr (SHARED)
     return {attend_kernel<C>, attend_packed_kernel<P>, attend_flat_kernel<C>,
-            join_kernel<typename C::Elem, C::kDim, C::kRows>};
+            join_kernel<typename C::Elem, C::kDim, C::kRows>, C::kThreads};
   else
-    return {attend_kernel<C>, attend_packed_kernel<P>, nullptr, nullptr};
+    return {attend_kernel<C>, attend_packed_kernel<P>, nullptr, nullptr, C::kThreads};
 }
 
 // The launch of a call: rows of a workgroup's tile, and how the work is shared.
@@ -507,17 +509,17 @@ int attend_call(const Shape& s, const void* cache, const xfer_attend* q, const A
   const AttendKernels k = pick(q->dtype, p);
   const hipStream_t on = static_cast<hipStream_t>(stream);
   hipError_t e;
-  if (p.packed) {
-    const uint64_t most = kMaxGrid / a.s.H;
-    e = launch(k.packed, a, dim3(uint32_t(std::min<uint64_t>(p.packed, most)) * a.s.H), kAttendWaves * 64, on);
-  } else if (!p.flat) {
-    e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles), kAttendWaves * 64, on);
-  } else {
-    e = launch(k.flat, a, dim3(p.flat * a.s.H), kAttendWaves * 64, on);
+  if (p.flat) {
+    e = launch(k.flat, a, dim3(p.flat * a.s.H), k.threads, on);
     if (e == hipSuccess) {
       const uint32_t rows = uint32_t(kJoinThreads) / (a.s.D / 4);  // of a join workgroup
       e = launch(k.join, a, dim3(p.flat, a.s.H, (uint32_t(p.tile) + rows - 1) / rows), kJoinThreads, on);
     }
+  } else if (p.packed) {
+    const uint64_t most = kMaxGrid * 256 / uint64_t(k.threads) / a.s.H;
+    e = launch(k.packed, a, dim3(uint32_t(std::min<uint64_t>(p.packed, most)) * a.s.H), k.threads, on);
+  } else {
+    e = launch(k.attend, a, dim3(uint32_t(q->batch) * a.s.H, p.tiles), k.threads, on);
   }
   if (e != hipSuccess) return hip_fail(e, (std::string(who) + " launch").c_str());
   return XFER_OK;

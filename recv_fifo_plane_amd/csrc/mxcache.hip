@@ -558,6 +558,16 @@ __device__ __forceinline__ bf16x8 widen4(uint32_t w, float scale) {
   return r;
 }
 
+// The largest of x in the four lanes n, n + 16, n + 32, n + 48.
+__device__ __forceinline__ float max_of_groups(float x) {
+  const uint32_t a = __float_as_uint(x);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const uint32_t b = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // The weights of a chunk's scores s, in units of 1 / mul, as two bfloat16 numbers each:
 // p the rounded ones, p2 the rounded rests.  Maxima m, sums l and accumulators acc go
 // along.  MASK: some row does not see some token of the chunk; limit: the last token
@@ -580,8 +590,7 @@ __device__ __forceinline__ void weights_of(f32x4 (&s)[NR][4], f32x4 (&acc)[NR][D
         s[x][t][r] = v;
         top = fmaxf(top, v);
       }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_of_groups(top);
     // The reference m follows the maximum only when that is 8 above it, so most
     // chunks leave the accumulators alone: weights reach 256 at most, and the
     // same powers of two leave sums and accumulators in the end.
@@ -608,24 +617,32 @@ __device__ __forceinline__ void weights_of(f32x4 (&s)[NR][4], f32x4 (&acc)[NR][D
   }
 }
 
+// The thread's number, of which nothing that follows is worked out before a loop around the
+// caller: registers would have to hold it.
+__device__ __forceinline__ uint32_t thread_here() {
+  uint32_t tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return tid;
+}
+
 // Writes the sixteen rows first .. of a request from what each wave of the workgroup
 // has of them: its sums of weighted values acc, relative to the rows' largest maximum
 // already, and its maxima m and sums l, `stride` from a wave's to the next's.  part
 // null: the rows of out and lse, else their sums to part and stats.
-template <typename E, int D>
-__device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&acc)[kAttendWaves][16][D + 4],
+template <typename E, int D, int WAVES>
+__device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&acc)[WAVES][16][D + 4],
                                            const float* m, const float* l, uint32_t stride,
                                            const RowTile& rt, uint32_t h, uint32_t first, float* part,
                                            float* stats) {
-  for (uint32_t i = threadIdx.x; i < 16 * (D / 4); i += kAttendWaves * 64) {
+  for (uint32_t i = thread_here(); i < 16 * (D / 4); i += WAVES * 64) {
     const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + r;
     const int64_t row = rt.start + ri / A.group;
     if (ri >= rt.rows) continue;
     float top = m[r], sum = 0.0f;
-    for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, m[w * stride + r]);
+    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, m[w * stride + r]);
     const float base = top == -INFINITY ? 0.0f : top;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < kAttendWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       sum += l[w * stride + r] * __builtin_amdgcn_exp2f(m[w * stride + r] - base);
       o += *reinterpret_cast<const f32x4*>(&acc[w][r][d]);
     }
@@ -686,6 +703,7 @@ __device__ __forceinline__ void weigh4(const u32x4 (&w)[D / 32], const u32x4 (&v
           e = mfma(a, p2[x][s], e);
           o = mfma(z, p2[x][s], o);
         }
+        if constexpr (D >= 192) __builtin_amdgcn_sched_barrier(0);
       }
     }
   });
@@ -706,18 +724,18 @@ __device__ __forceinline__ void mask_scales(u32x4& v, int32_t held, uint32_t& na
   }
 }
 
-template <typename E, int D, int NR>
+template <typename E, int D, int NR, int WAVES>
 struct Shared4 {
   static constexpr int kQueries = __is_same(E, fp16_t) ? 2 : 1;  // bfloat16 numbers of one
   union {
     u32x4 q[kQueries][NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
-    float acc[kAttendWaves][16][D + 4];
+    float acc[WAVES][16][D + 4];
   };
-  float m[kAttendWaves][NR * 16], l[kAttendWaves][NR * 16];
+  float m[WAVES][NR * 16], l[WAVES][NR * 16];
 };
 
 constexpr int attend4_resident(int d, int nr) {
-  return nr == 1 ? (d <= 96 ? 3 : d <= 192 ? 2 : 1) : d <= 128 ? 2 : 1;
+  return nr == 1 ? (d <= 96 ? 3 : 2) : d <= 128 ? 2 : 1;
 }
 
 // Attention as over 8-bit codes (cache.hip's kernels have its mathematics: which token
@@ -728,18 +746,19 @@ constexpr int attend4_resident(int d, int nr) {
 // bfloat16, exactly; a float16 query goes in two bfloat16 numbers, exactly, since
 // keys need bfloat16's range; a lane's result tile e of a part holds dims b' n + e, the
 // b' dims that its sixteen-byte pieces have of each token.
-template <typename E, int D, int NR, bool ONCE>
+template <typename E, int D, int NR, bool ONCE, int WAVES = kAttendWaves>
 struct Core4 {
   typedef E Elem;
-  typedef Shared4<E, D, NR> Shared;
-  static constexpr int kDim = D, kRows = NR * 16, kResident = attend4_resident(D, NR);
+  typedef Shared4<E, D, NR, WAVES> Shared;
+  static constexpr int kDim = D, kRows = NR * 16, kThreads = WAVES * 64;
+  static constexpr int kResident = attend4_resident(D, NR);
 
   static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
                                               uint32_t first, uint32_t c0, uint32_t c1, float* part,
                                               float* stats) {
     constexpr int KL = D / 32, DT = D / 16, NQ = Shared::kQueries;
-    const uint32_t lane = threadIdx.x & 63u, n = lane & 15u, g = lane >> 4;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (known to be uniform)
+    const uint32_t tid = thread_here(), lane = tid & 63u, n = lane & 15u, g = lane >> 4;
+    const uint32_t wave = uniform(tid >> 6);
     const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
     const RowTile rt = row_tile(A, b, first, NR * 16);
     c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
@@ -752,12 +771,12 @@ struct Core4 {
     Keys4<D, ONCE> keys;
     Values4<D, ONCE> vals;
     Place at, next;
-    constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
+    constexpr uint32_t kNext = WAVES * kChunk;  // tokens from a wave's chunk to its next
     at.look(A, table, c * kChunk, reach, g, n);
     next.look(A, table, c * kChunk + kNext, reach, g, n);
     __builtin_amdgcn_sched_barrier(0);
 
-    constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
+    constexpr int QL = (KL + WAVES - 1) / WAVES;
     int32_t limit[NR];        // last token that the row sees
     int32_t least = rt.seen;  // the first of them
     u32x4 q[NR][QL];
@@ -772,7 +791,7 @@ struct Core4 {
 #pragma unroll
       for (int k = 0; k < QL; ++k) {
         q[x][k] = u32x4{0u, 0u, 0u, 0u};
-        const uint32_t step = wave + k * kAttendWaves;
+        const uint32_t step = wave + k * WAVES;
         if (there && step < KL) __builtin_memcpy(&q[x][k], p + key4_dim<D>(step, g), 16);
       }
       if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
@@ -785,7 +804,7 @@ struct Core4 {
     for (int x = 0; x < NR; ++x)
 #pragma unroll
       for (int k = 0; k < QL; ++k) {
-        const uint32_t step = wave + k * kAttendWaves;
+        const uint32_t step = wave + k * WAVES;
         if (step >= KL) continue;
         if constexpr (NQ == 2) {
           u32x4 hi, lo;
@@ -838,6 +857,7 @@ struct Core4 {
 #pragma unroll
             for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[i][x], s[x][t]);
         }
+        if constexpr (D >= 192) __builtin_amdgcn_sched_barrier(0);  // (or registers run out)
       }
       __builtin_amdgcn_sched_barrier(0);
       next.settle(A, ahead, seen_all, g);
@@ -855,7 +875,7 @@ struct Core4 {
       at = next;
       next.look(A, table, ahead + kNext, seen_all, g, n);
       vals.load(A, at, ahead, h, g, n);
-      c += kAttendWaves;
+      c += WAVES;
     };
     // Chunks that every row sees whole, up to the first that is not; then the rest.
     const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
@@ -878,12 +898,12 @@ struct Core4 {
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       float top = sh.m[0][x * 16 + n];
-      for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
+      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
       const float f = __builtin_amdgcn_exp2f(m[x] - (top == -INFINITY ? 0.0f : top));
       float nan[part_count(D)] = {};
       if (any_nan) {
 #pragma clang loop unroll(disable)
-        for (uint32_t i = rest; i < c1; i += kAttendWaves)
+        for (uint32_t i = rest; i < c1; i += WAVES)
           seen_nans4<D>(A, table, h, i * kChunk, min(static_cast<int32_t>(i * kChunk) + kChunk - 1, limit[x]), g, nan);
       }
       // result tile e of a part, row 4g + r of it: dim dims / 16 * (4g + r) + e
@@ -896,53 +916,666 @@ struct Core4 {
             sh.acc[wave][n][from + wide * (4 * g + r) + e] = acc[x][from / 16 + e][r] * f + nan[k];
       });
       __syncthreads();
-      write_rows<E, D>(A, sh.acc, &sh.m[0][x * 16], &sh.l[0][x * 16], NR * 16, rt, h, first + x * 16,
+      write_rows<E, D, WAVES>(A, sh.acc, &sh.m[0][x * 16], &sh.l[0][x * 16], NR * 16, rt, h, first + x * 16,
                        part ? part + x * 16 * D : nullptr, stats + x * 32);
       __syncthreads();
     }
   }
 };
 
+// ---------------------------------------------------------- attend, many rows
+// Where a request has many rows, every wave takes 16 NR of them, a tile of rows is
+// four waves', and its keys and values are widened once for all of them: wave t
+// widens tile t of the keys, and half of the dims of half of the tokens' values, and
+// writes the left operands to shared memory, each lane's sixteen bytes where it will
+// read them.
+//
+// Weights multiply the values as float16 numbers where the chunk's scales allow it:
+// code * 2^e is a float16 number, exactly, for e from -23 to 13.  A weight is then off
+// by 2^-12 of itself (half a step of 11 bits), or 2^-32 of the row's largest where it
+// is below float16's normal numbers: maxima lie 7 to 15 powers of two above the reference,
+// so weights reach 2^15.  That is an eighth of a bfloat16 output's rounding.  For
+// float16 outputs a second number takes the rest (2^-22).  Their keys are float16 numbers
+// too under the same condition, and queries stay as they are.  Other chunks take the
+// bfloat16 numbers of few rows' attention.
+constexpr int wide_tiles(int d) { return d <= 128 ? 2 : 1; }    // of 16 rows, of a wave
+constexpr int wide_buffers(int d) { return d <= 128 ? 2 : 1; }  // of widened chunks
+
+
+template <typename E, int D, int NR>
+struct WideShared {
+  static constexpr int kKeys = 4 * (D / 32), kValues = 2 * (D / 16);
+  union {
+    u32x4 tile[wide_buffers(D)][kKeys + kValues][64];
+    Shared4<E, D, 1, kAttendWaves> few;
+  };
+};
+
+// Whether all of a word's four scales lie within 104 .. 135 (2^-23 .. 2^8): 24 is added to each
+// byte, and its upper three bits are 100 then.
+__device__ __forceinline__ bool float16_scales(uint32_t w) {
+  return ((((w & 0x7F7F7F7Fu) + 0x18181818u) ^ (w & 0x80808080u)) & 0xE0E0E0E0u) == 0x80808080u;
+}
+
+__device__ __forceinline__ fp16x2 two_fp16(uint32_t w, int byte, float scale) {
+  switch (byte) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3);
+  }
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t two_of(uint32_t w, int byte, float scale) {
+  if constexpr (HALF)
+    return __builtin_bit_cast(uint32_t, two_fp16(w, byte, scale));
+  else
+    return __builtin_bit_cast(uint32_t, two_bf16(w, byte, scale));
+}
+template <bool HALF>
+__device__ __forceinline__ f32x4 mfma_of(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (HALF)
+    return mfma(__builtin_bit_cast(fp16x8, a), __builtin_bit_cast(fp16x8, b), c);
+  else
+    return mfma(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c);
+}
+
+// The power of two that byte k of w stands for, in one instruction.
+template <int K>
+__device__ __forceinline__ float power_at(uint32_t w) {
+  uint32_t r;
+  if constexpr (K == 0)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(23u), "v"(w));
+  else if constexpr (K == 1)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(23u), "v"(w));
+  else if constexpr (K == 2)
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(23u), "v"(w));
+  else
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(23u), "v"(w));
+  return __uint_as_float(r);
+}
+
+// What a wave widens of a chunk, as loaded, and the scales that decide how.
+template <int D>
+struct WideCodes {
+  static constexpr int kAll = (D / 32 + 3) / 4;  // words of a lane that hold all of a side's scales
+  uint32_t k[D / 32], v[D / 16];
+  uint32_t ks[part_count(D)], vs[part_count(D)][2];
+  uint32_t all[2][kAll];
+
+  // Where a lane loads within a block: chunks begin at multiples of 64 tokens, so it is the same for all.
+  struct From {
+    uint32_t key[part_count(D)], key_scale[part_count(D)], value[part_count(D)], value_scale[part_count(D)], all[kAll];
+    uint32_t side;  // bytes from a head's scales of keys to its values'
+    __device__ __forceinline__ From(const AttendArgs& A, uint32_t h, uint32_t g, uint32_t n, uint32_t wave) {
+      const uint32_t T = A.s.T, tk = 16 * (n >> 2) & (T - 1), tv = 16 * g & (T - 1), s = wave >> 1;
+      const uint32_t tn = tk + 4 * wave + (n & 3u), codes = h * T * D, scales = A.s.H * T * D + 2 * h * (D / 32) * T;
+      side = D / 32 * T;
+      each_part<D>([&](auto part) {
+        constexpr int p = part.value, dims = part_dims(D, p), at = part_at(D, p), b = dims / 32;
+        key[p] = codes + tn * (D / 2) + at / 2 + dims / 8 * g;
+        key_scale[p] = scales + (at / 32 + g * b / 4) * T + tn;
+        // (sixteen tokens of a lane are b pieces of sixteen bytes, 256 bytes apart)
+        value[p] = codes + T * D / 2 + T * at / 2 + tv * b * 16 + n * 16 + (b == 1 ? 8 * s : 128 * b * s);
+        value_scale[p] = scales + side + (at / 32 + n * b / 16) * T + tv + 8 * s;
+      });
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) all[i] = scales + min(4 * i + g, D / 32 - 1u) * T + tk + 4 * (n & 3u);
+    }
+  };
+
+  template <bool QUERIES16>  // (whose keys' scales are asked about too)
+  __device__ __forceinline__ void load(const AttendArgs& A, const Place& at, const From& from) {
+    const uint32_t bytes = static_cast<uint32_t>(A.s.block_bytes);
+    const uint8_t* kb = A.cache + static_cast<uint64_t>(static_cast<uint32_t>(at.line)) * bytes;
+    const uint8_t* vb = A.cache + static_cast<uint64_t>(static_cast<uint32_t>(max(at.mine, 0))) * bytes;
+    each_part<D>([&](auto part) {
+      constexpr int p = part.value, dims = part_dims(D, p), at = part_at(D, p), b = dims / 32;
+      fetch_words<false, b>(kb + from.key[p], &k[at / 32]);
+      ks[p] = kb[from.key_scale[p]];
+      const uint8_t* q = vb + from.value[p];  // (eight tokens of b bytes)
+      if constexpr (b == 4) {
+        fetch_words<false, 4>(q, &v[at / 16]);
+        fetch_words<false, 4>(q + 256, &v[at / 16 + 4]);
+      } else {
+        fetch_words<false, 2 * b>(q, &v[at / 16]);
+      }
+      fetch_words<false, 2>(vb + from.value_scale[p], vs[p]);
+    });
+#pragma unroll
+    for (int i = 0; i < kAll; ++i) {
+      const uint8_t* q = kb + from.all[i];
+      all[1][i] = *reinterpret_cast<const uint32_t*>(q + from.side);
+      if (QUERIES16) all[0][i] = *reinterpret_cast<const uint32_t*>(q);
+    }
+  }
+
+  // Whether all scales of a side of tokens that some row sees are float16's.
+  __device__ __forceinline__ bool float16(int side, uint32_t t0, uint32_t seen, uint32_t n) const {
+    bool ok = true;
+    if (t0 + kChunk <= seen) {
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) ok &= float16_scales(all[side][i]);
+    } else {
+      const int32_t left = static_cast<int32_t>(seen) - static_cast<int32_t>(t0 + 16 * (n >> 2) + 4 * (n & 3u));
+      const uint32_t mask = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) ok &= float16_scales((all[side][i] & mask) | (0x7F7F7F7Fu & ~mask));
+    }
+    return __ballot(ok) == ~0ull;
+  }
+
+  // Replaces, as mask_scales, the scales of values that no row sees (held: tokens from the
+  // lane's sixteen on that some row does), and NaN where HALF has none.
+  template <bool HALF>
+  __device__ __forceinline__ void mask(uint32_t wave, int32_t held, uint32_t& nans) {
+    if (HALF && __ballot(held < 16) == 0) return;
+    const int32_t left = held - 8 * static_cast<int32_t>(wave >> 1);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int more = left - 4 * w;
+      const uint32_t seen = more <= 0 ? 0u : more >= 4 ? ~0u : (1u << (8 * more)) - 1u;
+#pragma unroll
+      for (int p = 0; p < part_count(D); ++p) {
+        uint32_t x = vs[p][w], keep = seen;
+        if constexpr (!HALF) {
+          const uint32_t nan = (((x & 0x7F7F7F7Fu) + 0x01010101u) & x & 0x80808080u & seen) >> 7;
+          nans |= nan;
+          keep &= ~(nan * 0xFFu);
+        }
+        vs[p][w] = (x & keep) | (0x7F7F7F7Fu & ~keep);
+      }
+    }
+  }
+
+  // Writes the operands of the values' dims that the wave's half of each token's bytes holds.
+  template <bool HALF, int SECOND>
+  __device__ __forceinline__ void widen_values(u32x4 (*out)[64], uint32_t lane) const {
+    each_part<D>([&](auto part) {
+      constexpr int p = part.value, dims = part_dims(D, p), at = part_at(D, p), b = dims / 32;
+      constexpr int kBytes = b == 4 ? 2 : 1, kFirst = b == 1 ? 0 : SECOND * kBytes;
+      if constexpr (b == 1 && SECOND) {
+        return;  // (one byte serves both)
+      } else {
+        const float scale[8] = {power_at<0>(vs[p][0]), power_at<1>(vs[p][0]), power_at<2>(vs[p][0]), power_at<3>(vs[p][0]),
+                                power_at<0>(vs[p][1]), power_at<1>(vs[p][1]), power_at<2>(vs[p][1]), power_at<3>(vs[p][1])};
+#pragma unroll
+        for (int j = 0; j < kBytes; ++j) {
+          u32x4 even, odd;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at0 = 2 * i * b + kFirst + j, at1 = at0 + b;
+            const uint32_t c0 = two_of<HALF>(v[at / 16 + at0 / 4], at0 % 4, scale[2 * i]);
+            const uint32_t c1 = two_of<HALF>(v[at / 16 + at1 / 4], at1 % 4, scale[2 * i + 1]);
+            even[i] = __builtin_amdgcn_perm(c1, c0, 0x05040100u);
+            odd[i] = __builtin_amdgcn_perm(c1, c0, 0x07060302u);
+          }
+          out[at / 16 + 2 * (kFirst + j)][lane] = even;
+          out[at / 16 + 2 * (kFirst + j) + 1][lane] = odd;
+        }
+      }
+    });
+  }
+
+  // Writes the operands of the wave's share.
+  template <bool HALFK, bool HALFV>
+  __device__ __forceinline__ void widen(u32x4 (*tile)[64], uint32_t lane, uint32_t wave, int32_t held,
+                                        uint32_t& nans) {
+    constexpr int KL = D / 32, DT = D / 16;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      constexpr int kFirst = part_dims(D, 0) / 32;
+      const float scale = power_of(ks[j < kFirst ? 0 : part_count(D) - 1], 0);
+      u32x4 a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = two_of<HALFK>(k[j], i, scale);
+      tile[wave * KL + j][lane] = a;
+    }
+    mask<HALFV>(wave, held, nans);
+    u32x4(*out)[64] = tile + 4 * KL + (wave >> 1) * DT;
+    if (wave & 1u)
+      widen_values<HALFV, 1>(out, lane);
+    else
+      widen_values<HALFV, 0>(out, lane);
+  }
+};
+
+template <typename W>
+__device__ __forceinline__ uint32_t two_in_word(W a, W b) {
+  typedef W pair __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, pair{a, b});
+}
+
+template <typename E, int D, int NR>
+struct Wide {
+  typedef E Elem;
+  typedef Core4<E, D, 1, false> Few;
+  typedef WideShared<E, D, NR> Shared;
+  static constexpr int kDim = D, kRows = 64 * NR, kThreads = kAttendWaves * 64, kResident = 2;
+  static constexpr bool kHalfQueries = __is_same(E, fp16_t);
+  static constexpr int KL = D / 32, DT = D / 16, NB = wide_buffers(D);
+
+  // Units of work of a tile of `rows` rows that sees `chunks` chunks: a chunk, or four where the
+  // waves of few rows' attention take one each.
+  static __device__ __forceinline__ uint32_t unit(uint32_t rows) { return rows <= 16 ? kAttendWaves : 1; }
+  static __device__ __forceinline__ uint32_t units(uint32_t rows, uint32_t chunks) {
+    return (chunks + unit(rows) - 1) / unit(rows);
+  }
+
+  static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
+                                              uint32_t first, uint32_t u0, uint32_t u1, float* part,
+                                              float* stats) {
+    const uint32_t here = min(rows_of(A, b) - first, static_cast<uint32_t>(kRows));
+    const uint32_t c0 = u0 * unit(here), c1 = u1 == ~0u ? u1 : u1 * unit(here);
+    if (here <= 16)
+      Few::rows(A, sh.few, b, h, first, c0, c1, part, stats);
+    else
+      many(A, sh, b, h, first, c0, c1, part, stats);
+  }
+
+  static __device__ __forceinline__ void many(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
+                                              uint32_t first, uint32_t c0, uint32_t c1, float* part,
+                                              float* stats) {
+    const uint32_t tid = thread_here(), lane = tid & 63u, n = lane & 15u, g = lane >> 4;
+    const uint32_t wave = uniform(tid >> 6);
+    const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
+    const RowTile rt = row_tile(A, b, first, kRows);
+    const uint32_t seen = uniform(static_cast<uint32_t>(rt.seen));
+    c1 = min(c1, (seen + kChunk - 1) / kChunk);
+
+    // the wave's rows
+    const uint32_t mine = first + wave * (16 * NR);
+    int32_t limit[NR];        // last token that the row sees
+    int32_t least = 0x7FFFFFFF, last = -1;  // the first and last of them
+    u32x4 q[NR][KL];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const uint32_t i = mine + x * 16 + n;
+      const int64_t j = i / A.group, row = rt.start + j;
+      const bool there = i < rt.rows;
+      limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
+      const E* p = static_cast<const E*>(A.query) + row * A.query_row +
+                   static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
+#pragma unroll
+      for (int k = 0; k < KL; ++k) {
+        q[x][k] = u32x4{0u, 0u, 0u, 0u};
+        if (there) __builtin_memcpy(&q[x][k], p + key4_dim<D>(k, g), 16);
+      }
+      if (there) least = min(least, limit[x]);
+      last = max(last, limit[x]);
+    }
+    for (int d = 1; d < 16; d <<= 1) {
+      least = min(least, __shfl_xor(least, d));
+      last = max(last, __shfl_xor(last, d));
+    }
+    least = __builtin_amdgcn_readfirstlane(least);
+    last = __builtin_amdgcn_readfirstlane(last);
+
+    float m[NR], l[NR];
+    f32x4 acc[NR][DT];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      m[x] = mine + x * 16 + n < rt.rows ? -INFINITY : 0.0f;  // (rows that are not there need no reference)
+      l[x] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    uint32_t nans = 0;
+
+    if (c0 < c1) {  // (so seen > 0)
+      WideCodes<D> codes;
+      Place at, next, then;  // of the chunk that codes hold, and the two behind it
+      uint32_t c = c0;
+      at.look(A, table, c * kChunk, seen, g, n);
+      next.look(A, table, (c + 1) * kChunk, seen, g, n);
+      at.settle(A, c * kChunk, seen, g);
+      const typename WideCodes<D>::From from(A, h, g, n, wave);
+      codes.template load<kHalfQueries>(A, at, from);
+      auto fits = [&] {  // chunk c is one of float16 numbers
+        return codes.float16(1, c * kChunk, seen, n) && (!kHalfQueries || codes.float16(0, c * kChunk, seen, n));
+      };
+      // The chunks from c on in float16 numbers (HALF), up to one that does not fit, or in
+      // bfloat16: the next chunk's codes are loaded while one is computed, and widened
+      // behind it, into the other buffer where there are two.
+      auto run = [&](auto float16) {
+        constexpr bool HALF = decltype(float16)::value, HALFK = HALF && kHalfQueries;
+        for (;;) {
+          const uint32_t t0 = c * kChunk;
+          const int32_t tg = t0 + 16 * g, bg = at.mine;
+          u32x4(*tile)[64] = sh.tile[NB == 2 ? c & 1u : 0];
+          if constexpr (NB == 1) __syncthreads();
+          uint32_t to = lane;
+          asm volatile("" : "+v"(to));  // (as `own` below)
+          codes.template widen<HALFK, HALF>(tile, to, wave, bg < 0 ? 0 : static_cast<int32_t>(seen) - tg, nans);
+          __syncthreads();
+          next.settle(A, t0 + kChunk, seen, g);
+          if (c + 1 < c1) codes.template load<kHalfQueries>(A, next, from);
+          then.look(A, table, t0 + 2 * kChunk, seen, g, n);
+          __builtin_amdgcn_sched_barrier(0);
+          if (static_cast<int32_t>(t0) <= last) {
+            f32x4 s[NR][4];
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+              for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // Operands are asked for two products' pairs ahead: keys' tiles 2 (i % 2) and + 1 of
+            // step i / 2, then the values' two steps of dims' tile i - 2 KL.
+            u32x4 ops[3][2];
+            uint32_t own = lane;
+            asm volatile("" : "+v"(own));  // (addresses are not to be kept from chunk to chunk)
+            auto ask = [&](int i) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                ops[i % 3][j] = i < 2 * KL ? tile[(2 * (i & 1) + j) * KL + i / 2][own] : tile[4 * KL + j * DT + i - 2 * KL][own];
+            };
+            ask(0);
+            ask(1);
+#pragma unroll
+            for (int i = 0; i < 2 * KL; ++i) {
+              ask(i + 2);
+              __builtin_amdgcn_sched_barrier(0);
+              u32x4 hi[NR], lo[NR];
+#pragma unroll
+              for (int x = 0; x < NR; ++x) {
+                hi[x] = q[x][i / 2];
+                if constexpr (kHalfQueries && !HALFK) {
+                  asm volatile("" : "+v"(hi[x]));  // (not to be kept in two parts from chunk to chunk)
+                  two_parts(hi[x], hi[x], lo[x]);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < NR; ++x) {
+                  f32x4& to = s[x][2 * (i & 1) + j];
+                  if constexpr (kHalfQueries && !HALFK) to = mfma_of<false>(ops[i % 3][j], lo[x], to);
+                  to = mfma_of<HALFK>(ops[i % 3][j], hi[x], to);
+                }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            if (static_cast<int32_t>(t0 + kChunk - 1) > least || __ballot(bg < 0) != 0) {
+#pragma unroll
+              for (int x = 0; x < NR; ++x) {
+                const int32_t sees = bg < 0 ? 0 : limit[x] - tg + 1;  // of this lane's sixteen tokens
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r)
+                    if (4 * t + r >= sees) s[x][t][r] = -INFINITY;
+              }
+            }
+            constexpr int kParts = HALF && !kHalfQueries ? 1 : 2;
+            typedef typename std::conditional<HALF, fp16_t, bf16_t>::type W;
+            u32x4 p[kParts][NR][2];
+            // The reference m follows the row's largest score when a chunk's weights of a lane
+            // add up to more than 2^15, or when there is none yet; they are worked out again then.
+            // (a whole number: what is rescaled by it stays exact)
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+              bool again = __ballot(m[x] == -INFINITY) != 0;
+              for (;;) {
+                if (again) {
+                  float top = -INFINITY;
+#pragma unroll
+                  for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[x][t][r]);
+                  top = max_of_groups(top) * A.scale2;
+                  const bool grows = top > m[x] + 8.0f;
+                  const float was = m[x];
+                  if (grows) m[x] = __builtin_floorf(top) - 7.0f;
+                  const float keep = grows ? __builtin_amdgcn_exp2f(was - m[x]) : 1.0f;
+                  l[x] *= keep;
+#pragma unroll
+                  for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+                }
+                const float base = m[x] == -INFINITY ? 0.0f : -m[x];
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                  for (int r = 0; r < 4; r += 2) {
+                    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r], A.scale2, base));
+                    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r + 1], A.scale2, base));
+                    sum[0] += w0;
+                    sum[1] += w1;
+                    const int i = (t & 1) * 2 + r / 2;
+                    const W f0 = static_cast<W>(w0), f1 = static_cast<W>(w1);
+                    p[0][x][t >> 1][i] = two_in_word(f0, f1);
+                    if constexpr (kParts == 2)
+                      p[kParts - 1][x][t >> 1][i] = two_in_word(static_cast<W>(w0 - static_cast<float>(f0)),
+                                                                static_cast<W>(w1 - static_cast<float>(f1)));
+                  }
+                const float more = sum[0] + sum[1];
+                if (!again && __ballot(more > 32768.0f) != 0) {
+                  again = true;
+                  continue;
+                }
+                l[x] += more;
+                break;
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int e = 0; e < DT; ++e) {
+              if (e + 2 < DT) ask(2 * KL + e + 2);
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                  for (int x = 0; x < NR; ++x)
+                    acc[x][e] = mfma_of<HALF>(ops[(2 * KL + e) % 3][j], p[i][x][j], acc[x][e]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          at = next;
+          next = then;
+          if (++c == c1 || (HALF && !fits())) return;
+        }
+      };
+      if (fits()) run(std::true_type());
+      if (c < c1) run(std::false_type());
+    }
+    // (a wave's own share of the values' NaN tells of them all: their tokens are looked for again)
+    const bool any_nan = __syncthreads_or(nans != 0) != 0;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const uint32_t i = mine + x * 16 + n;
+      float nan[part_count(D)] = {};
+      if (any_nan) seen_nans4<D>(A, table, h, c0 * kChunk, min(static_cast<int32_t>(c1 * kChunk) - 1, limit[x]), g, nan);
+      float sum = l[x] + __shfl_xor(l[x], 16);
+      sum += __shfl_xor(sum, 32);
+      if (i >= rt.rows) continue;
+      const int64_t row = rt.start + i / A.group;
+      const uint32_t head = h * A.group + i % A.group;
+      const float inv = part ? 1.0f : sum != 0.0f ? 1.0f / sum : 0.0f;
+      const uint32_t r0 = wave * (16 * NR) + x * 16 + n;  // in the tile
+      if (g == 0) {
+        if (part) {
+          stats[2 * r0] = m[x];
+          stats[2 * r0 + 1] = sum;
+        } else if (A.lse) {
+          A.lse[row * A.heads + head] = (m[x] + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+        }
+      }
+      each_part<D>([&](auto pt) {
+        constexpr int k = pt.value, wide = part_dims(D, k) / 16, from = part_at(D, k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t d = from + wide * (4 * g + r);
+          float o[wide];
+#pragma unroll
+          for (int e = 0; e < wide; ++e) o[e] = acc[x][from / 16 + e][r] * inv + nan[k];
+          if (part) {
+            __builtin_memcpy(part + r0 * D + d, o, sizeof(o));
+          } else {
+            E v[wide];
+#pragma unroll
+            for (int e = 0; e < wide; ++e) v[e] = static_cast<E>(o[e]);
+            __builtin_memcpy(static_cast<E*>(A.out) + row * A.out_row + head * A.out_head + d, v, sizeof(v));
+          }
+        }
+      });
+    }
+    __syncthreads();
+  }
+};
+
+// The units of tile number k of a core's tiles (0: no tile has it), and which tile that is.
+template <class C>
+struct Numbered {
+  uint32_t b, y, units;
+  __device__ __forceinline__ void look(const AttendArgs& A, uint32_t k) {  // (b set: the request)
+    y = k - first_tile(A, b, C::kRows);
+    const uint32_t rows = rows_of(A, b), first = y * C::kRows;
+    units = 0;
+    if (y >= (rows + C::kRows - 1) / C::kRows) return;
+    const uint32_t here = min(rows - first, static_cast<uint32_t>(C::kRows));
+    const int64_t length = A.lengths[b], held = min<int64_t>(length, static_cast<int64_t>(A.width) * A.s.T);
+    const int64_t ahead = length - (static_cast<int64_t>(A.starts[b + 1]) - A.starts[b]);
+    const int64_t sees = max<int64_t>(1, min<int64_t>(held, ahead + (first + here - 1) / A.group + 1));
+    units = C::units(here, static_cast<uint32_t>((sees + kChunk - 1) / kChunk));
+  }
+  // To number k from one before it.
+  __device__ __forceinline__ void advance(const AttendArgs& A, uint32_t k) {
+    while (b + 1 < static_cast<uint32_t>(A.batch) && first_tile(A, b + 1, C::kRows) <= k) ++b;
+    look(A, k);
+  }
+};
+
+// As attend_flat_kernel, but the line holds what each tile sees, so shares are even for
+// whole prompts too: every workgroup adds up all tiles, a thread its run of numbers.
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kResident) attend_wide_kernel(AttendArgs A) {
+  constexpr uint32_t kThreads = C::kThreads, kRows = C::kRows;
+  __shared__ typename C::Shared sh;
+  __shared__ uint64_t s_pre[kThreads], s_wave[kThreads / 64];
+  const uint32_t h = blockIdx.x % A.s.H, w = blockIdx.x / A.s.H, tid = threadIdx.x;
+  const uint32_t seg = (A.packed + kThreads - 1) / kThreads, k0 = min(A.packed, tid * seg), k1 = min(A.packed, k0 + seg);
+  Numbered<C> t;
+  uint64_t sum = 0;
+  if (k0 < k1) {
+    uint32_t lo = 0, hi = A.batch;  // the last request that begins at or before k0
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (first_tile(A, mid, kRows) <= k0)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    t.b = lo;
+    for (uint32_t k = k0; k < k1; ++k) {
+      t.advance(A, k);
+      sum += t.units;
+    }
+  }
+  uint64_t run = sum;  // inclusive over the wave's lanes
+  for (uint32_t d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up(static_cast<unsigned long long>(run), d);
+    if ((tid & 63u) >= d) run += o;
+  }
+  if ((tid & 63u) == 63u) s_wave[tid >> 6] = run;
+  __syncthreads();
+  uint64_t pre = run - sum, all = 0;
+  for (uint32_t i = 0; i < kThreads / 64; ++i) {
+    if (i < (tid >> 6)) pre += s_wave[i];
+    all += s_wave[i];
+  }
+  s_pre[tid] = pre;
+  __syncthreads();
+  all = uniform(all);
+  const uint64_t flat = min<uint64_t>(A.flat, all);  // (so every share holds a unit)
+  if (h == 0 && tid == 0) A.begun[w].request = -1;
+  if (w >= flat) return;
+  const uint64_t lo = uniform(all * w / flat), hi = uniform(all * (w + 1) / flat);
+  uint32_t from = 0, to = kThreads;  // the last run that begins at or before lo
+  while (to - from > 1) {
+    const uint32_t mid = (from + to) / 2;
+    if (s_pre[mid] <= lo)
+      from = mid;
+    else
+      to = mid;
+  }
+  uint32_t k = uniform(from) * seg;
+  uint64_t u = lo, at = uniform(s_pre[from]);  // the unit to do, the number's first
+  Numbered<C> now;
+  now.b = request_of(A, k, kRows);
+  now.look(A, k);
+  for (;;) {
+    uint32_t units = uniform(now.units);
+    while (at + units <= u && k + 1 < A.packed) {  // (u < all: a number with units follows)
+      at = uniform(at + units);
+      now.advance(A, ++k);
+      now.b = uniform(now.b);
+      units = uniform(now.units);
+    }
+    const uint32_t b = uniform(now.b), y = uniform(now.y);
+    const uint64_t end = uniform(at + units), stop = uniform(min(hi, end));
+    const bool whole = at >= lo && end <= hi;
+    if (end > hi && at >= lo && h == 0 && tid == 0) {
+      uint64_t sum_here = all;
+      asm volatile("" : "+s"(sum_here));  // (nothing for its division is to be kept from before the loop)
+      A.begun[w] = Begun{static_cast<int32_t>(b), y, static_cast<uint32_t>((end * flat - 1) / sum_here), 0};
+    }
+    const uint32_t slot = (blockIdx.x * 2 + (at >= lo ? 1 : 0)) * kRows;
+    C::rows(A, sh, b, h, y * kRows, static_cast<uint32_t>(u - at), static_cast<uint32_t>(stop - at),
+            whole ? nullptr : A.part + static_cast<uint64_t>(slot) * C::kDim, A.stats + slot * 2);
+    u = stop;
+    if (u == hi) return;
+  }
+}
+
+template <class C>
+AttendKernels wide_kernels() {
+  return {attend_kernel<C>, attend_packed_kernel<C>, attend_wide_kernel<C>,
+          join_kernel<typename C::Elem, C::kDim, C::kRows>, C::kThreads};
+}
+
 template <typename E, int D>
-AttendKernels pick_attend4_rows(int nr, bool once) {
-  if (nr == 2) return attend_kernels<Core4<E, D, 2, false>, Core4<E, D, 2, false>, true>();
+AttendKernels pick_attend4_rows(int tile, bool once) {
+  if (tile > 32) return wide_kernels<Wide<E, D, wide_tiles(D)>>();
+  if (tile == 32) return attend_kernels<Core4<E, D, 2, false>, Core4<E, D, 2, false>, true>();
   return once ? attend_kernels<Core4<E, D, 1, true>, Core4<E, D, 1, false>, true>()
               : attend_kernels<Core4<E, D, 1, false>, Core4<E, D, 1, false>, true>();
 }
 
 template <typename E>
-AttendKernels pick_attend4(uint32_t d, int nr, bool once) {
+AttendKernels pick_attend4(uint32_t d, int tile, bool once) {
   switch (d) {
-    case 64: return pick_attend4_rows<E, 64>(nr, once);
-    case 96: return pick_attend4_rows<E, 96>(nr, once);
-    case 128: return pick_attend4_rows<E, 128>(nr, once);
-    case 192: return pick_attend4_rows<E, 192>(nr, once);
-    default: return pick_attend4_rows<E, 256>(nr, once);
+    case 64: return pick_attend4_rows<E, 64>(tile, once);
+    case 96: return pick_attend4_rows<E, 96>(tile, once);
+    case 128: return pick_attend4_rows<E, 128>(tile, once);
+    case 192: return pick_attend4_rows<E, 192>(tile, once);
+    default: return pick_attend4_rows<E, 256>(tile, once);
   }
 }
 
-// The launch of a call, by the rules of 8-bit codes for now.
 AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   AttendPlan p;
   const int64_t group = q.heads / int(s.H);
   int64_t most = q.max_query ? std::min(q.max_query, q.rows) : q.rows;
   if (!q.max_query && q.rows <= q.batch) most = 1;
   const int64_t rows = most * group;
-  const int nr = rows <= 16 ? 1 : 2;
-  p.tile = nr * 16;
+  const int d = int(s.D), nr = rows <= 16 ? 1 : 2;
+  const bool wide = rows > 32;
+  p.tile = wide ? 64 * wide_tiles(d) : nr * 16;
   p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
   const int64_t numbers = int64_t(q.rows) * group / p.tile + q.batch;
-  const int64_t resident = 256 * attend4_resident(int(s.D), nr);
+  const int64_t resident = 256 * (wide ? 2 : attend4_resident(d, nr));
   p.flat = p.packed = 0;
   const bool enough = most > 1 && numbers * s.H > 12 * resident;
-  if (!enough && chunks >= (wgs <= 128 ? 24 : 64))
+  if (!enough && chunks >= (wide ? 8 : wgs <= 128 ? 24 : 64))
     p.flat = uint32_t(std::max<int64_t>(
         1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
-  if (!p.flat && wgs > numbers * s.H + kEmptyWorkgroups) p.packed = uint32_t(numbers);
+  // (a grid of a workgroup of 512 threads for each request and head ends at 2^23 of them)
+  const bool sparse = wgs > numbers * s.H + kEmptyWorkgroups || int64_t(q.batch) * s.H > int64_t(kMaxGrid / 2);
+  if (wide ? p.flat > 0 || sparse : !p.flat && sparse) p.packed = uint32_t(numbers);
   return p;
 }
 
@@ -1081,9 +1714,8 @@ extern "C" int xfer_mxcache_attend(const xfer_cache_shape* shape, const void* ca
   if (rc) return rc;
   if (q->rows == 0 || q->batch == 0) return XFER_OK;
   const auto pick = [&](int dtype, const AttendPlan& p) {
-    const int nr = p.tile / 16;
     const bool once = p.tiles == 1;
-    return dtype == XFER_BF16 ? pick_attend4<bf16_t>(s.D, nr, once) : pick_attend4<fp16_t>(s.D, nr, once);
+    return dtype == XFER_BF16 ? pick_attend4<bf16_t>(s.D, p.tile, once) : pick_attend4<fp16_t>(s.D, p.tile, once);
   };
   return attend_call(s, cache, q, attend4_plan(s, *q), pick, stream, "xfer_mxcache_attend");
 }

@@ -145,14 +145,31 @@ def is_shared(batch, rows, T, H, group, D, dtype, width, max_query=0, max_length
     return n.value > 0
 
 
+def bounds(want, tokens, D, dtype, wide):
+    """How far out and lse may be from R.attend()'s, elementwise.
+
+    Those of two_part_bounds; a bfloat16 query's products are those of D dims, a float16
+    query may go in two bfloat16 numbers, exactly, which makes 2 D products of a
+    score's sum.  wide: a call of many rows, whose weights may multiply the values as
+    float16 numbers.  Theirs are 11 significant bits: one of them is off by 2^-11 of the
+    weight at most, the sum of two (float16 queries) by 2^-22, which two_part_bounds
+    covers.  Below 2^-14 float16's numbers are 2^-24 apart, so what is left of
+    a weight is at least off by 2^-25 there; weights are taken relative to a reference
+    that leaves the largest of a row's at 2^7 or more, so that is 2^-32 of the row's
+    sum of weights, for each of the values that it sees."""
+    out_eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    tol, tol_lse = two_part_bounds(want[:4], tokens, D if dtype == "bf16" else 2 * D, out_eps)
+    if wide:
+        tol = tol + 1.01 * 2.0 ** -32 * want[4] * 1.01
+        if dtype == "bf16":
+            tol = tol + 1.01 * 2.0 ** -11 * want[2] * 1.01
+    return tol, tol_lse
+
+
 def check_attend(lens, rows, T, H, group, D, dtype="bf16", seed=0, width=None, bad_pages=0,
                  nan_tail=True, before=0, behind=0, hints=True, strides=False, scale=None, mag=1.0,
                  edit=None, shared=None):
-    """out and lse against the plain form's.
-
-    The bounds are two_part_bounds': a bfloat16 query's products are those of D
-    dims; a float16 query goes in two bfloat16 numbers, exactly, which makes 2 D
-    products of a score's sum."""
+    """out and lse against the plain form's."""
     rng = np.random.default_rng(seed)
     width = max([-(-max(x, 0) // T) for x in lens] + [0]) + 1 if width is None else width
     blocks = sum(-(-max(x, 0) // T) for x in lens) + 3
@@ -189,8 +206,8 @@ def check_attend(lens, rows, T, H, group, D, dtype="bf16", seed=0, width=None, b
     torch.cuda.synchronize()
     sc = 1 / math.sqrt(D) if scale is None else scale
     want = R.attend(ref, q.double().numpy(), table.tolist(), lens, starts, sc)
-    tol, tol_lse = two_part_bounds(want, max(lens + [1]), D if dtype == "bf16" else 2 * D,
-                                   2.0 ** -8 if dtype == "bf16" else 2.0 ** -11)
+    most = max(rows) if hints else n if n > len(lens) else 1
+    tol, tol_lse = bounds(want, max(lens + [1]), D, dtype, most * group > 32)
     got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
     real = np.zeros(n, bool)
     real[starts[0]:starts[-1]] = True

@@ -141,14 +141,15 @@ def load(cache, table, lengths, starts, rows):
 
 
 def attend(cache, query, table, lengths, starts, scale):
-    """float64 (out, lse, bound of |weights| times |values|, bound of scores) for
-    query rows [rows, heads, D]; rows of no request are NaN."""
+    """float64 (out, lse, bound of |weights| times |values|, bound of scores, sum of the
+    |values| seen) for query rows [rows, heads, D]; rows of no request are NaN."""
     rows, heads, D = query.shape
     group = heads // cache.H
     out = np.full((rows, heads, D), np.nan)
     lse = np.full((rows, heads), np.nan)
     mag = np.zeros((rows, heads, D))
     big = np.zeros((rows, heads))
+    far = np.zeros((rows, heads, D))
     for b, length in enumerate(lengths):
         r0, r1 = starts[b], min(starts[b + 1], rows)
         t = np.arange(max(0, min(length, len(table[b]) * cache.T)))
@@ -171,4 +172,5 @@ def attend(cache, query, table, lengths, starts, scale):
                         lse[n, g] = m + math.log(l) if np.isfinite(l) else np.nan
                         mag[n, g] = (p @ np.abs(v[see])) / l
                         big[n, g] = (np.abs(k[see]) @ np.abs(q)).max() * scale
-    return out, lse, mag, big
+                        far[n, g] = np.abs(v[see]).sum(0)
+    return out, lse, mag, big, far

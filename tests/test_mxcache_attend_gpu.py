@@ -8,9 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import mxcache_ref as R  # noqa: E402
-from mxcache_cases import (check_attend, gpu_cache, ints, is_shared, new_pool, starts_of,  # noqa: E402
+from mxcache_cases import (bounds, check_attend, gpu_cache, ints, is_shared, new_pool, starts_of,  # noqa: E402
                            table_of)
-from attend_bounds import two_part_bounds  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -254,7 +253,7 @@ def test_wrong_hints():
     table = np.arange(240).reshape(2, 120)
     q = torch.randn(93, 4, D, device="cuda").to(torch.bfloat16)
     want = R.attend(ref, q.double().cpu().numpy(), table.tolist(), lens, starts_of(rows), 1 / math.sqrt(D))
-    tol, tol_lse = two_part_bounds(want, 1900, D, 2.0 ** -8)
+    tol, tol_lse = bounds(want, 1900, D, "bf16", True)
     for mq, ml in ((0, 0), (1, 1), (1, 0), (0, 5), (20, 64), (93, 1900), (5000, 1 << 30)):
         got, lse = gpu.attend(q, table_of(table), ints(lens), ints(starts_of(rows)), max_query=mq,
                               max_length=ml, lse=True)
