@@ -572,48 +572,45 @@ __device__ __forceinline__ float max_of_groups(float x) {
 // p the rounded ones, p2 the rounded rests.  Maxima m, sums l and accumulators acc go
 // along.  MASK: some row does not see some token of the chunk; limit: the last token
 // that each row sees; tg: the lane's first of sixteen; bg: their block (below 0: none).
-template <bool MASK, int DT, int NR>
-__device__ __forceinline__ void weights_of(f32x4 (&s)[NR][4], f32x4 (&acc)[NR][DT], float (&m)[NR],
-                                           float (&l)[NR], const int32_t (&limit)[NR], float mul,
-                                           int32_t tg, int32_t bg, bf16x8 (&p)[NR][2],
-                                           bf16x8 (&p2)[NR][2]) {
+template <bool MASK, int DT>
+__device__ __forceinline__ void weights_of(f32x4 (&s)[4], f32x4 (&acc)[DT], float (&m),
+                                           float (&l), const int32_t (&limit), float mul,
+                                           int32_t tg, int32_t bg, bf16x8 (&p)[2],
+                                           bf16x8 (&p2)[2]) {
+  const int32_t seen = bg < 0 ? 0 : limit - tg + 1;  // of this lane's sixteen tokens
+  float top = -INFINITY;
 #pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    const int32_t seen = bg < 0 ? 0 : limit[x] - tg + 1;  // of this lane's sixteen tokens
-    float top = -INFINITY;
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v = s[x][t][r] * mul;
-        if (MASK && 4 * t + r >= seen) v = -INFINITY;
-        s[x][t][r] = v;
-        top = fmaxf(top, v);
-      }
-    top = max_of_groups(top);
-    // The reference m follows the maximum only when that is 8 above it, so most
-    // chunks leave the accumulators alone: weights reach 256 at most, and the
-    // same powers of two leave sums and accumulators in the end.
-    const bool grows = top > m[x] + 8.0f;
-    const float next = grows ? top : m[x], base = next == -INFINITY ? 0.0f : next;
-    const float keep = grows ? __builtin_amdgcn_exp2f(m[x] - base) : 1.0f;
-    m[x] = next;
-    float sum = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float w = __builtin_amdgcn_exp2f(s[x][t][r] - base);
-        sum += w;
-        const bf16_t first = static_cast<bf16_t>(w);
-        p[x][t >> 1][(t & 1) * 4 + r] = first;
-        p2[x][t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
-      }
-    l[x] = l[x] * keep + sum;
-    if (__ballot(grows) != 0) {
-#pragma unroll
-      for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+    for (int r = 0; r < 4; ++r) {
+      float v = s[t][r] * mul;
+      if (MASK && 4 * t + r >= seen) v = -INFINITY;
+      s[t][r] = v;
+      top = fmaxf(top, v);
     }
+  top = max_of_groups(top);
+  // The reference m follows the maximum only when that is 8 above it, so most
+  // chunks leave the accumulators alone: weights reach 256 at most, and the
+  // same powers of two leave sums and accumulators in the end.
+  const bool grows = top > m + 8.0f;
+  const float next = grows ? top : m, base = next == -INFINITY ? 0.0f : next;
+  const float keep = grows ? __builtin_amdgcn_exp2f(m - base) : 1.0f;
+  m = next;
+  float sum = 0.0f;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float w = __builtin_amdgcn_exp2f(s[t][r] - base);
+      sum += w;
+      const bf16_t first = static_cast<bf16_t>(w);
+      p[t >> 1][(t & 1) * 4 + r] = first;
+      p2[t >> 1][(t & 1) * 4 + r] = static_cast<bf16_t>(w - static_cast<float>(first));
+    }
+  l = l * keep + sum;
+  if (__ballot(grows) != 0) {
+#pragma unroll
+    for (int e = 0; e < DT; ++e) acc[e] *= keep;
   }
 }
 
@@ -629,20 +626,20 @@ __device__ __forceinline__ uint32_t thread_here() {
 // has of them: its sums of weighted values acc, relative to the rows' largest maximum
 // already, and its maxima m and sums l, `stride` from a wave's to the next's.  part
 // null: the rows of out and lse, else their sums to part and stats.
-template <typename E, int D, int WAVES>
-__device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&acc)[WAVES][16][D + 4],
+template <typename E, int D>
+__device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&acc)[kAttendWaves][16][D + 4],
                                            const float* m, const float* l, uint32_t stride,
                                            const RowTile& rt, uint32_t h, uint32_t first, float* part,
                                            float* stats) {
-  for (uint32_t i = thread_here(); i < 16 * (D / 4); i += WAVES * 64) {
+  for (uint32_t i = thread_here(); i < 16 * (D / 4); i += kAttendWaves * 64) {
     const uint32_t r = i / (D / 4), d = i % (D / 4) * 4, ri = first + r;
     const int64_t row = rt.start + ri / A.group;
     if (ri >= rt.rows) continue;
     float top = m[r], sum = 0.0f;
-    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, m[w * stride + r]);
+    for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, m[w * stride + r]);
     const float base = top == -INFINITY ? 0.0f : top;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < WAVES; ++w) {
+    for (int w = 0; w < kAttendWaves; ++w) {
       sum += l[w * stride + r] * __builtin_amdgcn_exp2f(m[w * stride + r] - base);
       o += *reinterpret_cast<const f32x4*>(&acc[w][r][d]);
     }
@@ -668,10 +665,10 @@ __device__ __forceinline__ void write_rows(const AttendArgs& A, const float (&ac
 // The product of a chunk's weights p + p2 with the values.  A byte of codes gives two
 // dims of a token, the left operand wants eight tokens of a dim: two bytes of
 // neighbouring tokens, each widened with its own scale, and the halves put together.
-template <int D, int NR>
+template <int D>
 __device__ __forceinline__ void weigh4(const u32x4 (&w)[D / 32], const u32x4 (&vs)[part_count(D)],
-                                       const bf16x8 (&p)[NR][2], const bf16x8 (&p2)[NR][2],
-                                       f32x4 (&acc)[NR][D / 16]) {
+                                       const bf16x8 (&p)[2], const bf16x8 (&p2)[2],
+                                       f32x4 (&acc)[D / 16]) {
   each_part<D>([&](auto part) {
     constexpr int pt = part.value, dims = part_dims(D, pt), from = part_at(D, pt), b = dims / 32;
 #pragma unroll
@@ -694,15 +691,12 @@ __device__ __forceinline__ void weigh4(const u32x4 (&w)[D / 32], const u32x4 (&v
           odd[k] = __builtin_amdgcn_perm(c[1], c[0], 0x07060302u);
         }
         const bf16x8 a = __builtin_bit_cast(bf16x8, even), z = __builtin_bit_cast(bf16x8, odd);
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          f32x4& e = acc[x][from / 16 + 2 * j];
-          f32x4& o = acc[x][from / 16 + 2 * j + 1];
-          e = mfma(a, p[x][s], e);
-          o = mfma(z, p[x][s], o);
-          e = mfma(a, p2[x][s], e);
-          o = mfma(z, p2[x][s], o);
-        }
+        f32x4& e = acc[from / 16 + 2 * j];
+        f32x4& o = acc[from / 16 + 2 * j + 1];
+        e = mfma(a, p[s], e);
+        o = mfma(z, p[s], o);
+        e = mfma(a, p2[s], e);
+        o = mfma(z, p2[s], o);
         if constexpr (D >= 192) __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -724,19 +718,17 @@ __device__ __forceinline__ void mask_scales(u32x4& v, int32_t held, uint32_t& na
   }
 }
 
-template <typename E, int D, int NR, int WAVES>
+template <typename E, int D>
 struct Shared4 {
   static constexpr int kQueries = __is_same(E, fp16_t) ? 2 : 1;  // bfloat16 numbers of one
   union {
-    u32x4 q[kQueries][NR][D / 32][64];  // the rows' queries, in the order of the matrix operand
-    float acc[WAVES][16][D + 4];
+    u32x4 q[kQueries][D / 32][64];  // the rows' queries, in the order of the matrix operand
+    float acc[kAttendWaves][16][D + 4];
   };
-  float m[WAVES][NR * 16], l[WAVES][NR * 16];
+  float m[kAttendWaves][16], l[kAttendWaves][16];
 };
 
-constexpr int attend4_resident(int d, int nr) {
-  return nr == 1 ? (d <= 96 ? 3 : 2) : d <= 128 ? 2 : 1;
-}
+constexpr int attend4_resident(int d) { return d <= 96 ? 3 : 2; }
 
 // Attention as over 8-bit codes (cache.hip's kernels have its mathematics: which token
 // sits where, one running maximum and sum a wave, weights in two bfloat16 numbers):
@@ -746,12 +738,12 @@ constexpr int attend4_resident(int d, int nr) {
 // bfloat16, exactly; a float16 query goes in two bfloat16 numbers, exactly, since
 // keys need bfloat16's range; a lane's result tile e of a part holds dims b' n + e, the
 // b' dims that its sixteen-byte pieces have of each token.
-template <typename E, int D, int NR, bool ONCE, int WAVES = kAttendWaves>
+template <typename E, int D, bool ONCE>
 struct Core4 {
   typedef E Elem;
-  typedef Shared4<E, D, NR, WAVES> Shared;
-  static constexpr int kDim = D, kRows = NR * 16, kThreads = WAVES * 64;
-  static constexpr int kResident = attend4_resident(D, NR);
+  typedef Shared4<E, D> Shared;
+  static constexpr int kDim = D, kRows = 16, kThreads = kAttendWaves * 64;
+  static constexpr int kResident = attend4_resident(D);
 
   static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
                                               uint32_t first, uint32_t c0, uint32_t c1, float* part,
@@ -760,7 +752,7 @@ struct Core4 {
     const uint32_t tid = thread_here(), lane = tid & 63u, n = lane & 15u, g = lane >> 4;
     const uint32_t wave = uniform(tid >> 6);
     const int32_t* table = A.table + static_cast<int64_t>(b) * A.table_stride;
-    const RowTile rt = row_tile(A, b, first, NR * 16);
+    const RowTile rt = row_tile(A, b, first, kRows);
     c1 = min(c1, (static_cast<uint32_t>(rt.seen) + kChunk - 1) / kChunk);
 
     // (waves with no chunk load too, any block: behind a branch around the loads every
@@ -771,63 +763,55 @@ struct Core4 {
     Keys4<D, ONCE> keys;
     Values4<D, ONCE> vals;
     Place at, next;
-    constexpr uint32_t kNext = WAVES * kChunk;  // tokens from a wave's chunk to its next
+    constexpr uint32_t kNext = kAttendWaves * kChunk;  // tokens from a wave's chunk to its next
     at.look(A, table, c * kChunk, reach, g, n);
     next.look(A, table, c * kChunk + kNext, reach, g, n);
     __builtin_amdgcn_sched_barrier(0);
 
-    constexpr int QL = (KL + WAVES - 1) / WAVES;
-    int32_t limit[NR];        // last token that the row sees
+    constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
+    int32_t limit;        // last token that the row sees
     int32_t least = rt.seen;  // the first of them
-    u32x4 q[NR][QL];
+    u32x4 q[QL];
+    const uint32_t i = first + n;
+    const int64_t j = i / A.group, row = rt.start + j;
+    const bool there = i < rt.rows;
+    limit = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
+    const E* p = static_cast<const E*>(A.query) + row * A.query_row +
+                 static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const uint32_t i = first + x * 16 + n;
-      const int64_t j = i / A.group, row = rt.start + j;
-      const bool there = i < rt.rows;
-      limit[x] = there ? static_cast<int32_t>(max<int64_t>(-1, min<int64_t>(rt.seen - 1, rt.ahead + j))) : -1;
-      const E* p = static_cast<const E*>(A.query) + row * A.query_row +
-                   static_cast<int64_t>(h * A.group + i % A.group) * A.query_head;
-#pragma unroll
-      for (int k = 0; k < QL; ++k) {
-        q[x][k] = u32x4{0u, 0u, 0u, 0u};
-        const uint32_t step = wave + k * WAVES;
-        if (there && step < KL) __builtin_memcpy(&q[x][k], p + key4_dim<D>(step, g), 16);
-      }
-      if (there) least = min(least, limit[x]);  // (other rows hold zeros and go nowhere)
+    for (int k = 0; k < QL; ++k) {
+      q[k] = u32x4{0u, 0u, 0u, 0u};
+      const uint32_t step = wave + k * kAttendWaves;
+      if (there && step < KL) __builtin_memcpy(&q[k], p + key4_dim<D>(step, g), 16);
     }
+    if (there) least = min(least, limit);  // (other rows hold zeros and go nowhere)
     at.settle(A, c * kChunk, seen_all, g);
     keys.load(A, at, c * kChunk, h, g, n);
     __builtin_amdgcn_sched_barrier(0);
     vals.load(A, at, c * kChunk, h, g, n);
 #pragma unroll
-    for (int x = 0; x < NR; ++x)
-#pragma unroll
-      for (int k = 0; k < QL; ++k) {
-        const uint32_t step = wave + k * WAVES;
-        if (step >= KL) continue;
-        if constexpr (NQ == 2) {
-          u32x4 hi, lo;
-          two_parts(q[x][k], hi, lo);
-          sh.q[0][x][step][lane] = hi;
-          sh.q[NQ - 1][x][step][lane] = lo;
-        } else {
-          sh.q[0][x][step][lane] = q[x][k];
-        }
+    for (int k = 0; k < QL; ++k) {
+      const uint32_t step = wave + k * kAttendWaves;
+      if (step >= KL) continue;
+      if constexpr (NQ == 2) {
+        u32x4 hi, lo;
+        two_parts(q[k], hi, lo);
+        sh.q[0][step][lane] = hi;
+        sh.q[NQ - 1][step][lane] = lo;
+      } else {
+        sh.q[0][step][lane] = q[k];
       }
+    }
     for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
     least = __builtin_amdgcn_readfirstlane(least);
     __syncthreads();
 
-    float m[NR], l[NR];
-    f32x4 acc[NR][DT];
+    float m, l;
+    f32x4 acc[DT];
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      m[x] = -INFINITY;
-      l[x] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < DT; ++e) acc[x][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int e = 0; e < DT; ++e) acc[e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     // The order of loads is that of the 8-bit codes: the next chunk's keys once this
     // one's scores are done, its values once this one's are used up.
@@ -835,27 +819,23 @@ struct Core4 {
       constexpr bool MASK = decltype(masked)::value;
       const uint32_t t0 = c * kChunk, tg = t0 + 16 * g, ahead = t0 + kNext;
       const int32_t bg = at.mine;
-      f32x4 s[NR][4];
+      f32x4 s[4];
 #pragma unroll
-      for (int x = 0; x < NR; ++x)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) s[x][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int t = 0; t < 4; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < KL; ++k) {
         constexpr int kFirst = part_dims(D, 0) / 32;
         const int pt = k < kFirst ? 0 : part_count(D) - 1;
-        bf16x8 b8[NQ][NR];
+        bf16x8 b8[NQ];
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
-#pragma unroll
-          for (int x = 0; x < NR; ++x) b8[i][x] = __builtin_bit_cast(bf16x8, sh.q[i][x][k][lane]);
+          b8[i] = __builtin_bit_cast(bf16x8, sh.q[i][k][lane]);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const bf16x8 a = widen4(keys.w[t][k], power_of(keys.s[pt][t], n & 3u));
 #pragma unroll
           for (int i = NQ - 1; i >= 0; --i)
-#pragma unroll
-            for (int x = 0; x < NR; ++x) s[x][t] = mfma(a, b8[i][x], s[x][t]);
+            s[t] = mfma(a, b8[i], s[t]);
         }
         if constexpr (D >= 192) __builtin_amdgcn_sched_barrier(0);  // (or registers run out)
       }
@@ -863,19 +843,19 @@ struct Core4 {
       next.settle(A, ahead, seen_all, g);
       keys.load(A, next, ahead, h, g, n);
       __builtin_amdgcn_sched_barrier(0);
-      bf16x8 p[NR][2], p2[NR][2];
-      weights_of<MASK, DT, NR>(s, acc, m, l, limit, A.scale2, tg, bg, p, p2);
+      bf16x8 p[2], p2[2];
+      weights_of<MASK, DT>(s, acc, m, l, limit, A.scale2, tg, bg, p, p2);
       if constexpr (MASK) {
         const int32_t held = bg < 0 ? 0 : static_cast<int32_t>(seen_all) - static_cast<int32_t>(tg);
 #pragma unroll
         for (int k = 0; k < part_count(D); ++k) mask_scales(vals.s[k], held, nans);
       }
-      weigh4<D, NR>(vals.w, vals.s, p, p2, acc);
+      weigh4<D>(vals.w, vals.s, p, p2, acc);
       __builtin_amdgcn_sched_barrier(0);
       at = next;
       next.look(A, table, ahead + kNext, seen_all, g, n);
       vals.load(A, at, ahead, h, g, n);
-      c += WAVES;
+      c += kAttendWaves;
     };
     // Chunks that every row sees whole, up to the first that is not; then the rest.
     const uint32_t whole = min(c1, static_cast<uint32_t>(least + 1) / kChunk);
@@ -885,41 +865,34 @@ struct Core4 {
     const bool any_nan = __ballot(nans != 0) != 0;
 
     // Join the waves.
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      l[x] += __shfl_xor(l[x], 16);
-      l[x] += __shfl_xor(l[x], 32);
-      if (g == 0) {
-        sh.m[wave][x * 16 + n] = m[x];
-        sh.l[wave][x * 16 + n] = l[x];
-      }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+      sh.m[wave][n] = m;
+      sh.l[wave][n] = l;
     }
     __syncthreads();  // (and no wave needs the queries any more)
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      float top = sh.m[0][x * 16 + n];
-      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, sh.m[w][x * 16 + n]);
-      const float f = __builtin_amdgcn_exp2f(m[x] - (top == -INFINITY ? 0.0f : top));
-      float nan[part_count(D)] = {};
-      if (any_nan) {
+    float top = sh.m[0][n];
+    for (int w = 1; w < kAttendWaves; ++w) top = fmaxf(top, sh.m[w][n]);
+    const float f = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.0f : top));
+    float nan[part_count(D)] = {};
+    if (any_nan) {
 #pragma clang loop unroll(disable)
-        for (uint32_t i = rest; i < c1; i += WAVES)
-          seen_nans4<D>(A, table, h, i * kChunk, min(static_cast<int32_t>(i * kChunk) + kChunk - 1, limit[x]), g, nan);
-      }
-      // result tile e of a part, row 4g + r of it: dim dims / 16 * (4g + r) + e
-      each_part<D>([&](auto pt) {
-        constexpr int k = pt.value, wide = part_dims(D, k) / 16, from = part_at(D, k);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int e = 0; e < wide; ++e)
-            sh.acc[wave][n][from + wide * (4 * g + r) + e] = acc[x][from / 16 + e][r] * f + nan[k];
-      });
-      __syncthreads();
-      write_rows<E, D, WAVES>(A, sh.acc, &sh.m[0][x * 16], &sh.l[0][x * 16], NR * 16, rt, h, first + x * 16,
-                       part ? part + x * 16 * D : nullptr, stats + x * 32);
-      __syncthreads();
+      for (uint32_t i = rest; i < c1; i += kAttendWaves)
+        seen_nans4<D>(A, table, h, i * kChunk, min(static_cast<int32_t>(i * kChunk) + kChunk - 1, limit), g, nan);
     }
+    // result tile e of a part, row 4g + r of it: dim dims / 16 * (4g + r) + e
+    each_part<D>([&](auto pt) {
+      constexpr int k = pt.value, wide = part_dims(D, k) / 16, from = part_at(D, k);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < wide; ++e)
+          sh.acc[wave][n][from + wide * (4 * g + r) + e] = acc[from / 16 + e][r] * f + nan[k];
+    });
+    __syncthreads();
+    write_rows<E, D>(A, sh.acc, &sh.m[0][0], &sh.l[0][0], 16, rt, h, first, part, stats);
+    __syncthreads();
   }
 };
 
@@ -930,24 +903,29 @@ struct Core4 {
 // writes the left operands to shared memory, each lane's sixteen bytes where it will
 // read them.
 //
-// Weights multiply the values as float16 numbers where the chunk's scales allow it:
-// code * 2^e is a float16 number, exactly, for e from -23 to 13.  A weight is then off
-// by 2^-12 of itself (half a step of 11 bits), or 2^-32 of the row's largest where it
-// is below float16's normal numbers: maxima lie 7 to 15 powers of two above the reference,
-// so weights reach 2^15.  That is an eighth of a bfloat16 output's rounding.  For
-// float16 outputs a second number takes the rest (2^-22).  Their keys are float16 numbers
-// too under the same condition, and queries stay as they are.  Other chunks take the
-// bfloat16 numbers of few rows' attention.
+// Weights multiply the values as float16 numbers where the chunk's scale bytes lie in
+// 104 .. 135: code * 2^e is a float16 number, exactly, for e from -23 to 8.  A weight
+// is then off by half a step, 2^-11 of itself, or by 2^-25 where it is below float16's
+// normal numbers, 2^-32 of the row's largest: maxima lie 7 to 15 powers of two
+// above the reference, so weights reach 2^15.  That is an eighth of a bfloat16 output's own
+// rounding.  For float16 outputs a second number takes the rest (2^-22).  Their keys are
+// float16 numbers too under the same condition, and queries stay as they are.  Other
+// chunks take the bfloat16 numbers of few rows' attention.
+//
+// What bounds it is instructions: a chunk of 64 tokens and 128 rows of 128 dims takes
+// about 4300 cycles (widening 800, scores 770, weights 1170, products 630, loads and
+// barriers the rest).  8 chunks of prompts over up to 5000 tokens take 76 us, 5 prompts of
+// up to 2900 tokens 125.  Tried and slower: the next chunk widened between this one's products (in
+// the same wave), eight waves in two halves that take turns at widening and multiplying (88 and 235).
 constexpr int wide_tiles(int d) { return d <= 128 ? 2 : 1; }    // of 16 rows, of a wave
 constexpr int wide_buffers(int d) { return d <= 128 ? 2 : 1; }  // of widened chunks
-
 
 template <typename E, int D, int NR>
 struct WideShared {
   static constexpr int kKeys = 4 * (D / 32), kValues = 2 * (D / 16);
   union {
     u32x4 tile[wide_buffers(D)][kKeys + kValues][64];
-    Shared4<E, D, 1, kAttendWaves> few;
+    Shared4<E, D> few;
   };
 };
 
@@ -1149,24 +1127,28 @@ __device__ __forceinline__ uint32_t two_in_word(W a, W b) {
 template <typename E, int D, int NR>
 struct Wide {
   typedef E Elem;
-  typedef Core4<E, D, 1, false> Few;
+  typedef Core4<E, D, false> Few;
   typedef WideShared<E, D, NR> Shared;
   static constexpr int kDim = D, kRows = 64 * NR, kThreads = kAttendWaves * 64, kResident = 2;
   static constexpr bool kHalfQueries = __is_same(E, fp16_t);
   static constexpr int KL = D / 32, DT = D / 16, NB = wide_buffers(D);
 
   // Units of work of a tile of `rows` rows that sees `chunks` chunks: a chunk, or four where the
-  // waves of few rows' attention take one each.
+  // waves of few rows' attention take one each, and two for what a tile takes besides
+  // (its queries, its first loads, its result).  With shares of equal chunks 5 prompts of up
+  // to 2900 tokens took 179 us and with these 150; four units and not two: 153.
+  static constexpr uint32_t kFixed = 2;
   static __device__ __forceinline__ uint32_t unit(uint32_t rows) { return rows <= 16 ? kAttendWaves : 1; }
   static __device__ __forceinline__ uint32_t units(uint32_t rows, uint32_t chunks) {
-    return (chunks + unit(rows) - 1) / unit(rows);
+    return kFixed + (chunks + unit(rows) - 1) / unit(rows);
   }
 
   static __device__ __forceinline__ void rows(const AttendArgs& A, Shared& sh, uint32_t b, uint32_t h,
                                               uint32_t first, uint32_t u0, uint32_t u1, float* part,
                                               float* stats) {
     const uint32_t here = min(rows_of(A, b) - first, static_cast<uint32_t>(kRows));
-    const uint32_t c0 = u0 * unit(here), c1 = u1 == ~0u ? u1 : u1 * unit(here);
+    const uint32_t c0 = (max(u0, kFixed) - kFixed) * unit(here);
+    const uint32_t c1 = u1 == ~0u ? u1 : (max(u1, kFixed) - kFixed) * unit(here);
     if (here <= 16)
       Few::rows(A, sh.few, b, h, first, c0, c1, part, stats);
     else
@@ -1249,7 +1231,7 @@ struct Wide {
           codes.template widen<HALFK, HALF>(tile, to, wave, bg < 0 ? 0 : static_cast<int32_t>(seen) - tg, nans);
           __syncthreads();
           next.settle(A, t0 + kChunk, seen, g);
-          if (c + 1 < c1) codes.template load<kHalfQueries>(A, next, from);
+          codes.template load<kHalfQueries>(A, next, from);
           then.look(A, table, t0 + 2 * kChunk, seen, g, n);
           __builtin_amdgcn_sched_barrier(0);
           if (static_cast<int32_t>(t0) <= last) {
@@ -1535,10 +1517,9 @@ AttendKernels wide_kernels() {
 
 template <typename E, int D>
 AttendKernels pick_attend4_rows(int tile, bool once) {
-  if (tile > 32) return wide_kernels<Wide<E, D, wide_tiles(D)>>();
-  if (tile == 32) return attend_kernels<Core4<E, D, 2, false>, Core4<E, D, 2, false>, true>();
-  return once ? attend_kernels<Core4<E, D, 1, true>, Core4<E, D, 1, false>, true>()
-              : attend_kernels<Core4<E, D, 1, false>, Core4<E, D, 1, false>, true>();
+  if (tile > 16) return wide_kernels<Wide<E, D, wide_tiles(D)>>();
+  return once ? attend_kernels<Core4<E, D, true>, Core4<E, D, false>, true>()
+              : attend_kernels<Core4<E, D, false>, Core4<E, D, false>, true>();
 }
 
 template <typename E>
@@ -1552,29 +1533,43 @@ AttendKernels pick_attend4(uint32_t d, int tile, bool once) {
   }
 }
 
+// Which kernel computes a call's rows, and how it is cut up.  Times are of 32 heads
+// over 8, 128 dims, unless they say otherwise.
 AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   AttendPlan p;
   const int64_t group = q.heads / int(s.H);
   int64_t most = q.max_query ? std::min(q.max_query, q.rows) : q.rows;
   if (!q.max_query && q.rows <= q.batch) most = 1;
   const int64_t rows = most * group;
-  const int d = int(s.D), nr = rows <= 16 ? 1 : 2;
-  const bool wide = rows > 32;
-  p.tile = wide ? 64 * wide_tiles(d) : nr * 16;
-  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
+  const int d = int(s.D);
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
+  // Tiles of 16 rows until there is work for many rows' tiles to fill the device twice
+  // over: 16 requests of 15 rows over 2000 tokens take 23 us so and 39 with many rows'
+  // tiles, 2 of 1000 over 1000 take 58 and 38.  They cost more per row the wider the
+  // heads: 64 requests of 15 rows over 2000 tokens of 256 dims take 125 and 85.  32 rows of a
+  // request stay with them in any case (64 requests of up to 28, 8000 tokens: 57 and 71).
+  const int64_t units = int64_t(q.rows) * group / 16 * s.H * chunks;
+  const bool wide = rows > 32 && units > (d <= 128 ? 57344 : 24576);
+  p.tile = wide ? 64 * wide_tiles(d) : 16;
+  p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
   const int64_t numbers = int64_t(q.rows) * group / p.tile + q.batch;
-  const int64_t resident = 256 * (wide ? 2 : attend4_resident(d, nr));
+  const int64_t resident = 256 * (wide ? 2 : attend4_resident(d));
+  // Equal shares of all work cost a join of the tiles that they cut (25 us where many rows' tiles
+  // are cut), a workgroup per tile leaves the device waiting for the longest tile (1.6 us a chunk).
+  // Many rows: 8 chunks of prompts up to 5000 tokens take 82 us in shares and 135 by
+  // tiles, 2 prompts of 1000 tokens 61 and 38.  Few rows: 64 requests of up to 8000 tokens take
+  // 57 and 76, 48 of up to 3000 (12 heads over 2) 24 and 19.
+  const int64_t share = int64_t(q.rows) * group / p.tile * s.H * chunks / resident;
+  const bool shares = wide ? chunks > share / 2 + 19
+                           : chunks >= (wgs <= 128 ? 24 : 64) && !(most > 1 && numbers * s.H > 12 * resident);
   p.flat = p.packed = 0;
-  const bool enough = most > 1 && numbers * s.H > 12 * resident;
-  if (!enough && chunks >= (wide ? 8 : wgs <= 128 ? 24 : 64))
+  if (shares)
     p.flat = uint32_t(std::max<int64_t>(
         1, std::min<int64_t>(resident / s.H, chunks * q.batch * p.tiles / 8)));
-  // (a grid of a workgroup of 512 threads for each request and head ends at 2^23 of them)
-  const bool sparse = wgs > numbers * s.H + kEmptyWorkgroups || int64_t(q.batch) * s.H > int64_t(kMaxGrid / 2);
+  const bool sparse = wgs > numbers * s.H + kEmptyWorkgroups || int64_t(q.batch) * s.H > int64_t(kMaxGrid);
   if (wide ? p.flat > 0 || sparse : !p.flat && sparse) p.packed = uint32_t(numbers);
   return p;
 }

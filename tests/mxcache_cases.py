@@ -166,10 +166,16 @@ def bounds(want, tokens, D, dtype, wide):
     return tol, tol_lse
 
 
+def many_length(n, H, group, D):
+    """A length from which tiles of many rows compute n rows."""
+    return 64 * ((57344 if D <= 128 else 24576) // (n * group // 16 * H) + 1)
+
+
 def check_attend(lens, rows, T, H, group, D, dtype="bf16", seed=0, width=None, bad_pages=0,
                  nan_tail=True, before=0, behind=0, hints=True, strides=False, scale=None, mag=1.0,
-                 edit=None, shared=None):
-    """out and lse against the plain form's."""
+                 edit=None, shared=None, many=None):
+    """out and lse against the plain form's.  many: the length that the call is told (0: a wide
+    table and no hint), so that tiles of many rows compute it."""
     rng = np.random.default_rng(seed)
     width = max([-(-max(x, 0) // T) for x in lens] + [0]) + 1 if width is None else width
     blocks = sum(-(-max(x, 0) // T) for x in lens) + 3
@@ -200,14 +206,19 @@ def check_attend(lens, rows, T, H, group, D, dtype="bf16", seed=0, width=None, b
         out = torch.full((heads, n, D + 8), 7.0, dtype=q.dtype, device="cuda").transpose(0, 1)[:, :, 8:]
     lse = torch.full((n, heads), 7.0, device="cuda")
     more = dict(max_query=max(rows + [0]), max_length=max(lens + [0, 0])) if hints else {}
+    if many is not None:
+        told = many or many_length(n, H, group, D)
+        width = max(width, -(-told // T))
+        table = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+        if hints:
+            more["max_length"] = told
     if shared is not None:
         assert is_shared(len(lens), n, T, H, group, D, dtype, width, *more.values()) == shared
     gpu.attend(qd, table_of(table), ints(lens), ints(starts), scale=scale, out=out, lse=lse, **more)
     torch.cuda.synchronize()
     sc = 1 / math.sqrt(D) if scale is None else scale
     want = R.attend(ref, q.double().numpy(), table.tolist(), lens, starts, sc)
-    most = max(rows) if hints else n if n > len(lens) else 1
-    tol, tol_lse = bounds(want, max(lens + [1]), D, dtype, most * group > 32)
+    tol, tol_lse = bounds(want, max(lens + [1]), D, dtype, many is not None)
     got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
     real = np.zeros(n, bool)
     real[starts[0]:starts[-1]] = True

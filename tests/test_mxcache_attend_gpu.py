@@ -253,7 +253,7 @@ def test_wrong_hints():
     table = np.arange(240).reshape(2, 120)
     q = torch.randn(93, 4, D, device="cuda").to(torch.bfloat16)
     want = R.attend(ref, q.double().cpu().numpy(), table.tolist(), lens, starts_of(rows), 1 / math.sqrt(D))
-    tol, tol_lse = bounds(want, 1900, D, "bf16", True)
+    tol, tol_lse = bounds(want, 1900, D, "bf16", False)
     for mq, ml in ((0, 0), (1, 1), (1, 0), (0, 5), (20, 64), (93, 1900), (5000, 1 << 30)):
         got, lse = gpu.attend(q, table_of(table), ints(lens), ints(starts_of(rows)), max_query=mq,
                               max_length=ml, lse=True)
