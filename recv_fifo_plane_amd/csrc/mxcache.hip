@@ -196,21 +196,24 @@ __device__ __forceinline__ uint32_t value_unit_at(uint32_t T, uint32_t piece, ui
   return T * at / 2 + t / u * 256 + n * 16 + t % u * b;
 }
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 256, kStoreEach = 2;
 
 // A thread takes eight dims of one head and side of a row: four neighbours have
 // the 32 that share a scale.  The rows' dims are numbered one after the other,
-// keys before values, and a workgroup takes the next EACH * 256 pieces of eight.
-// (the first kernel, simple: figures follow)
-template <typename E, int D, int EACH>
+// keys before values, and a workgroup takes the next kStoreEach * 256 pieces of eight.
+//
+// What bounds it is memory: the rows of 29 prompts, 54 M numbers of 16 bits, are stored in
+// 29.9 us, 4.6 TB/s read and written, where a large copy reaches 4.9.  With one
+// piece a thread it took 34.4 us.
+template <typename E, int D>
 __global__ void __launch_bounds__(kStoreThreads) store4_kernel(Store4Args A) {
   constexpr uint32_t W = D / 8;
   const uint32_t side_pieces = A.s.H * W, row_pieces = 2 * side_pieces;
-  const uint64_t base = static_cast<uint64_t>(blockIdx.x) * (kStoreThreads * EACH);
+  const uint64_t base = static_cast<uint64_t>(blockIdx.x) * (kStoreThreads * kStoreEach);
   const uint64_t row0 = base / row_pieces;
   const uint32_t rest = static_cast<uint32_t>(base - row0 * row_pieces) + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < EACH; ++i) {
+  for (int i = 0; i < kStoreEach; ++i) {
     const uint32_t q = rest + i * kStoreThreads, ahead = q / row_pieces;
     const uint32_t side = q - ahead * row_pieces >= side_pieces ? 1 : 0;
     const uint32_t c = q - ahead * row_pieces - side * side_pieces, h = c / W, piece = c % W;
@@ -248,14 +251,14 @@ __global__ void __launch_bounds__(kStoreThreads) store4_kernel(Store4Args A) {
 
 using Store4Fn = void (*)(Store4Args);
 
-template <typename E, int EACH>
+template <typename E>
 Store4Fn pick_store4(uint32_t d) {
   switch (d) {
-    case 64: return store4_kernel<E, 64, EACH>;
-    case 96: return store4_kernel<E, 96, EACH>;
-    case 128: return store4_kernel<E, 128, EACH>;
-    case 192: return store4_kernel<E, 192, EACH>;
-    default: return store4_kernel<E, 256, EACH>;
+    case 64: return store4_kernel<E, 64>;
+    case 96: return store4_kernel<E, 96>;
+    case 128: return store4_kernel<E, 128>;
+    case 192: return store4_kernel<E, 192>;
+    default: return store4_kernel<E, 256>;
   }
 }
 
@@ -273,7 +276,7 @@ struct LoadArgs {
   Shape s;
 };
 
-constexpr int kLoadThreads = 256;
+constexpr int kLoadThreads = 256, kLoadEach = 2, kLoadShare = kLoadThreads * kLoadEach;
 constexpr int kLoadTile = 16;  // tokens, the first a multiple of it
 
 // Tiles numbered through the packed rows: request b's begin at number first(b) =
@@ -377,8 +380,15 @@ struct Quad<8, D> {
 };
 
 // A workgroup takes a tile of a request's tokens and, of the tile's keys and values,
-// its share: a thread four tokens of eight dims at a time, neighbours the
-// neighbouring dims, so that rows are written in long pieces.
+// its share: a thread twice four tokens of eight dims at a time, neighbours the
+// neighbouring dims, so that rows are written in long pieces.  (A block outside the
+// cache is read as block 0, and its rows are zeros: a branch around the loads would
+// make the second wait for the first.)
+//
+// What bounds it is memory, four fifths of it the rows written: 52 us for 24 prefixes of up to
+// 9001 tokens from 4 bits (5.3 TB/s), 54 us for 17 of up to 12001 from 8 (4.4).  With
+// one load a thread in flight they took 71 and 63 us; one call of 300 tokens then takes 3.9 us
+// and now 4.2.
 template <int BITS, typename E, int D>
 __global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs A) {
   constexpr uint32_t W = D / 8;
@@ -406,20 +416,31 @@ __global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs A) {
     if (static_cast<uint32_t>(block) >= A.s.blocks) block = -1;
     const uint32_t off = static_cast<uint32_t>(t0) & (A.s.T - 1);
     const uint32_t side_pieces = A.s.H * W, all = 2 * 4 * side_pieces;
-    for (uint32_t i = blockIdx.y * kLoadThreads + threadIdx.x; i < all; i += gridDim.y * kLoadThreads) {
-      const uint32_t quad = i / side_pieces & 3u, side = i / side_pieces >> 2, c = i % side_pieces;
-      const uint32_t h = c / W, piece = c % W;
-      Quad<BITS, D> q;
-      if (block >= 0) q.load(A.s, A.cache, static_cast<uint32_t>(block), h, side, piece, off + 4 * quad);
-      E* out = static_cast<E*>(side ? A.value : A.key) + static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
-      const int64_t stride = side ? A.value_row : A.key_row;
+    const uint32_t from = max(block, 0);
+    for (uint32_t i0 = blockIdx.y * kLoadShare + threadIdx.x; i0 < all; i0 += gridDim.y * kLoadShare) {
+      Quad<BITS, D> q[kLoadEach];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t row = start + t0 + 4 * quad + j - ahead;
-        if (row < start || row >= end) continue;
-        E x[8] = {};
-        if (block >= 0) q.rows(j, x);
-        __builtin_memcpy(out + row * stride, x, sizeof(x));
+      for (int z = 0; z < kLoadEach; ++z) {
+        const uint32_t i = min(i0 + z * kLoadThreads, all - 1);
+        const uint32_t quad = i / side_pieces & 3u, side = i / side_pieces >> 2, c = i % side_pieces;
+        q[z].load(A.s, A.cache, from, c / W, side, c % W, off + 4 * quad);
+      }
+#pragma unroll
+      for (int z = 0; z < kLoadEach; ++z) {
+        const uint32_t i = i0 + z * kLoadThreads;
+        if (i >= all) continue;
+        const uint32_t quad = i / side_pieces & 3u, side = i / side_pieces >> 2, c = i % side_pieces;
+        const uint32_t h = c / W, piece = c % W;
+        E* out = static_cast<E*>(side ? A.value : A.key) + static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
+        const int64_t stride = side ? A.value_row : A.key_row;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t row = start + t0 + 4 * quad + j - ahead;
+          if (row < start || row >= end) continue;
+          E x[8] = {};
+          if (block >= 0) q[z].rows(j, x);
+          __builtin_memcpy(out + row * stride, x, sizeof(x));
+        }
       }
     }
   }
@@ -1615,12 +1636,12 @@ extern "C" int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, co
   a.slots = slots;
   a.rows = rows;
   const uint64_t pieces = uint64_t(rows) * a.s.H * 2 * (a.s.D / 8);
-  const uint64_t wgs = (pieces + kStoreThreads - 1) / kStoreThreads;
+  const uint64_t each = kStoreThreads * kStoreEach, wgs = (pieces + each - 1) / each;
   if (wgs > kMaxGrid)
     return fail(XFER_ERR_INVALID_ARG, "xfer_mxcache_store: too many rows times heads for one call");
-  const Store4Fn fn = dtype == XFER_BF16   ? pick_store4<bf16_t, 1>(a.s.D)
-                      : dtype == XFER_FP16 ? pick_store4<fp16_t, 1>(a.s.D)
-                                           : pick_store4<float, 1>(a.s.D);
+  const Store4Fn fn = dtype == XFER_BF16   ? pick_store4<bf16_t>(a.s.D)
+                      : dtype == XFER_FP16 ? pick_store4<fp16_t>(a.s.D)
+                                           : pick_store4<float>(a.s.D);
   const hipError_t e = launch(fn, a, dim3(uint32_t(wgs)), kStoreThreads, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "xfer_mxcache_store launch");
   return XFER_OK;
@@ -1665,7 +1686,7 @@ int load_call(const Shape& s, int bits, const void* cache, const xfer_load* q, v
   a.width = q->table_width;
   a.numbers = uint32_t(q->rows) / kLoadTile + 2u * uint32_t(q->batch);
   a.s = s;
-  const uint32_t units = 2 * 4 * s.H * (s.D / 8), shares = (units + kLoadThreads - 1) / kLoadThreads;
+  const uint32_t units = 2 * 4 * s.H * (s.D / 8), shares = (units + kLoadShare - 1) / kLoadShare;
   const LoadFn fn = bits == 8 ? pick_load<8>(s.D, q->dtype) : pick_load<4>(s.D, q->dtype);
   const uint32_t most = uint32_t(kMaxGrid / shares);
   const hipError_t e = launch(fn, a, dim3(std::min(a.numbers, most), shares), kLoadThreads,
