@@ -4,7 +4,7 @@ A connection moves a device buffer A into a device buffer B through a ring of
 FIFO slots per channel (SIMPLE copy, LL 8-byte flagged lines, or zero-copy
 through a ptrExchange word), with both endpoints running as concurrent
 workgroup sets in one kernel launch.  A paged cache of keys and values in 8
-bits (cache.py) has blocks that a connection moves as they are, with the
+or 4 bits (cache.py) has blocks that a connection moves as they are, with the
 operators that fill and read it.  The compute path is libxfer.so (HIP
 kernels + C++ runtime, C ABI in include/xfer.h); this package only binds it.
 """

@@ -301,8 +301,8 @@ class PagedCache:
         v, v_row, v_head = _rows(value, "store: value", (dtype,), self.device, rows, self.kv_heads,
                                  self.head_dim)
         at = _list(slots, "store: slots", rows, self.device)
-        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].store), self._ref, self._base, k, k_row, k_head,
-              v, v_row, v_head, kinds[dtype], at, rows)
+        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].store), self._ref,
+              self._base, k, k_row, k_head, v, v_row, v_head, kinds[dtype], at, rows)
 
     def load(self, table, lengths, starts, rows: int, dtype=None, out=None, stream=None):
         """Keys and values of the cache's tokens as packed rows [rows, kv_heads,
@@ -346,7 +346,8 @@ class PagedCache:
         v, v_row, v_head = _rows(value, "load: out value", (key.dtype,), self.device, *shape)
         a = X.xfer_load(k, v, at_table, at_lengths, at_starts, k_row, k_head, v_row, v_head, stride,
                         batch, rows, width, kinds[key.dtype])
-        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].load), self._ref, self._base, C.byref(a))
+        _call(self.device, stream, getattr(X.lib(), self._NAMES[self.bits].load), self._ref,
+              self._base, C.byref(a))
         return key, value
 
     def attend(self, query, table, lengths, starts, scale=None, out=None, lse=False, max_query=0,

@@ -106,8 +106,10 @@ __device__ __forceinline__ void eight_of(uint32_t w, float scale, E (&out)[8]) {
 
 // Byte j of the four words, as word j.
 __device__ __forceinline__ void transpose(const uint32_t (&w)[4], uint32_t (&out)[4]) {
-  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
-  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);
+  const uint32_t b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
   out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
   out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
   out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
@@ -242,7 +244,8 @@ __global__ void __launch_bounds__(kStoreThreads) store4_kernel(Store4Args A) {
         *reinterpret_cast<uint16_t*>(v + value_unit_at<D>(A.s.T, piece, 1, t)) = static_cast<uint16_t>(codes >> 16);
       } else {
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) v[value_unit_at<D>(A.s.T, piece, k, t)] = static_cast<uint8_t>(codes >> (8 * k));
+        for (uint32_t k = 0; k < 4; ++k)
+          v[value_unit_at<D>(A.s.T, piece, k, t)] = static_cast<uint8_t>(codes >> (8 * k));
       }
     }
     if (piece % 4 == 0) A.cache[scales4_at(A.s, block, h, side, piece / 4) + t] = static_cast<uint8_t>(e);
@@ -316,7 +319,8 @@ struct Quad<4, D> {
     } else {
       uint32_t x[4];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint32_t*>(v + value_unit_at<D>(S.T, piece, j, t));
+      for (uint32_t j = 0; j < 4; ++j)
+        x[j] = *reinterpret_cast<const uint32_t*>(v + value_unit_at<D>(S.T, piece, j, t));
       transpose(x, w);
     }
   }
@@ -346,7 +350,8 @@ struct Quad<8, D> {
     }
     uint32_t x[2][4], y[4];
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) x[k / 4][k % 4] = *reinterpret_cast<const uint32_t*>(p + (8 * piece + k) * S.T + t);
+    for (uint32_t k = 0; k < 8; ++k)
+      x[k / 4][k % 4] = *reinterpret_cast<const uint32_t*>(p + (8 * piece + k) * S.T + t);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       transpose(x[i], y);
@@ -431,7 +436,8 @@ __global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs A) {
         if (i >= all) continue;
         const uint32_t quad = i / side_pieces & 3u, side = i / side_pieces >> 2, c = i % side_pieces;
         const uint32_t h = c / W, piece = c % W;
-        E* out = static_cast<E*>(side ? A.value : A.key) + static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
+        E* out = static_cast<E*>(side ? A.value : A.key) +
+                 static_cast<int64_t>(h) * (side ? A.value_head : A.key_head) + 8 * piece;
         const int64_t stride = side ? A.value_row : A.key_row;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -706,7 +712,8 @@ __device__ __forceinline__ void weigh4(const u32x4 (&w)[D / 32], const u32x4 (&v
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int byte = (8 * s + 2 * k + i) * b + j;
-            c[i] = __builtin_bit_cast(uint32_t, two_bf16(w[from / 32 + byte / 16][byte / 4 % 4], byte % 4, scale[2 * k + i]));
+            c[i] = __builtin_bit_cast(
+                uint32_t, two_bf16(w[from / 32 + byte / 16][byte / 4 % 4], byte % 4, scale[2 * k + i]));
           }
           even[k] = __builtin_amdgcn_perm(c[1], c[0], 0x05040100u);
           odd[k] = __builtin_amdgcn_perm(c[1], c[0], 0x07060302u);
@@ -790,7 +797,7 @@ struct Core4 {
     __builtin_amdgcn_sched_barrier(0);
 
     constexpr int QL = (KL + kAttendWaves - 1) / kAttendWaves;
-    int32_t limit;        // last token that the row sees
+    int32_t limit;            // last token that the row sees
     int32_t least = rt.seen;  // the first of them
     u32x4 q[QL];
     const uint32_t i = first + n;
@@ -984,13 +991,21 @@ template <int K>
 __device__ __forceinline__ float power_at(uint32_t w) {
   uint32_t r;
   if constexpr (K == 0)
-    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(23u), "v"(w));
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0"
+        : "=v"(r)
+        : "v"(23u), "v"(w));
   else if constexpr (K == 1)
-    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(23u), "v"(w));
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1"
+        : "=v"(r)
+        : "v"(23u), "v"(w));
   else if constexpr (K == 2)
-    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(23u), "v"(w));
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2"
+        : "=v"(r)
+        : "v"(23u), "v"(w));
   else
-    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(23u), "v"(w));
+    asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3"
+        : "=v"(r)
+        : "v"(23u), "v"(w));
   return __uint_as_float(r);
 }
 
@@ -1004,7 +1019,8 @@ struct WideCodes {
 
   // Where a lane loads within a block: chunks begin at multiples of 64 tokens, so it is the same for all.
   struct From {
-    uint32_t key[part_count(D)], key_scale[part_count(D)], value[part_count(D)], value_scale[part_count(D)], all[kAll];
+    uint32_t key[part_count(D)], key_scale[part_count(D)], value[part_count(D)];
+    uint32_t value_scale[part_count(D)], all[kAll];
     uint32_t side;  // bytes from a head's scales of keys to its values'
     __device__ __forceinline__ From(const AttendArgs& A, uint32_t h, uint32_t g, uint32_t n, uint32_t wave) {
       const uint32_t T = A.s.T, tk = 16 * (n >> 2) & (T - 1), tv = 16 * g & (T - 1), s = wave >> 1;
@@ -1096,8 +1112,10 @@ struct WideCodes {
       if constexpr (b == 1 && SECOND) {
         return;  // (one byte serves both)
       } else {
-        const float scale[8] = {power_at<0>(vs[p][0]), power_at<1>(vs[p][0]), power_at<2>(vs[p][0]), power_at<3>(vs[p][0]),
-                                power_at<0>(vs[p][1]), power_at<1>(vs[p][1]), power_at<2>(vs[p][1]), power_at<3>(vs[p][1])};
+        const float scale[8] = {power_at<0>(vs[p][0]), power_at<1>(vs[p][0]), power_at<2>(vs[p][0]),
+                                power_at<3>(vs[p][0]),
+                                power_at<0>(vs[p][1]), power_at<1>(vs[p][1]), power_at<2>(vs[p][1]),
+                                power_at<3>(vs[p][1])};
 #pragma unroll
         for (int j = 0; j < kBytes; ++j) {
           u32x4 even, odd;
@@ -1269,7 +1287,8 @@ struct Wide {
             auto ask = [&](int i) {
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                ops[i % 3][j] = i < 2 * KL ? tile[(2 * (i & 1) + j) * KL + i / 2][own] : tile[4 * KL + j * DT + i - 2 * KL][own];
+                ops[i % 3][j] = i < 2 * KL ? tile[(2 * (i & 1) + j) * KL + i / 2][own]
+                                           : tile[4 * KL + j * DT + i - 2 * KL][own];
             };
             ask(0);
             ask(1);
@@ -1387,7 +1406,8 @@ struct Wide {
     for (int x = 0; x < NR; ++x) {
       const uint32_t i = mine + x * 16 + n;
       float nan[part_count(D)] = {};
-      if (any_nan) seen_nans4<D>(A, table, h, c0 * kChunk, min(static_cast<int32_t>(c1 * kChunk) - 1, limit[x]), g, nan);
+      if (any_nan)
+        seen_nans4<D>(A, table, h, c0 * kChunk, min(static_cast<int32_t>(c1 * kChunk) - 1, limit[x]), g, nan);
       float sum = l[x] + __shfl_xor(l[x], 16);
       sum += __shfl_xor(sum, 32);
       if (i >= rt.rows) continue;
@@ -1456,7 +1476,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kResident) attend_wide_kernel(
   __shared__ typename C::Shared sh;
   __shared__ uint64_t s_pre[kThreads], s_wave[kThreads / 64];
   const uint32_t h = blockIdx.x % A.s.H, w = blockIdx.x / A.s.H, tid = threadIdx.x;
-  const uint32_t seg = (A.packed + kThreads - 1) / kThreads, k0 = min(A.packed, tid * seg), k1 = min(A.packed, k0 + seg);
+  const uint32_t seg = (A.packed + kThreads - 1) / kThreads;
+  const uint32_t k0 = min(A.packed, tid * seg), k1 = min(A.packed, k0 + seg);
   Numbered<C> t;
   uint64_t sum = 0;
   if (k0 < k1) {
