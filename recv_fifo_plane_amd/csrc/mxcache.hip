@@ -1343,9 +1343,15 @@ struct Wide {
             // The reference m follows the row's largest score when a chunk's weights of a lane
             // add up to more than 2^15, or when there is none yet; they are worked out again then.
             // (a whole number: what is rescaled by it stays exact)
+            //
+            // A score times scale2 is not rounded before m is taken from it, but the maximum that m
+            // follows is; where floats lie so far apart that this shows (2^20: 2^-5 at most), all
+            // are rounded first, or a weight could be any power of two.
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
-              bool again = __ballot(m[x] == -INFINITY) != 0;
+              constexpr float kFar = 1048576.0f;
+              bool again = __ballot(!(fabsf(m[x]) < kFar)) != 0;
+              float mul = A.scale2;
               for (;;) {
                 if (again) {
                   float top = -INFINITY;
@@ -1361,6 +1367,11 @@ struct Wide {
                   l[x] *= keep;
 #pragma unroll
                   for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
+                  if (__ballot(!(fabsf(m[x]) < kFar)) != 0) {
+                    mul = 1.0f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) s[x][t] *= A.scale2;
+                  }
                 }
                 const float base = m[x] == -INFINITY ? 0.0f : -m[x];
                 float sum[2] = {0.0f, 0.0f};
@@ -1368,8 +1379,8 @@ struct Wide {
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                   for (int r = 0; r < 4; r += 2) {
-                    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r], A.scale2, base));
-                    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r + 1], A.scale2, base));
+                    const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r], mul, base));
+                    const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][r + 1], mul, base));
                     sum[0] += w0;
                     sum[1] += w1;
                     const int i = (t & 1) * 2 + r / 2;
