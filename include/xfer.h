@@ -524,13 +524,12 @@ int xfer_cache_load(const xfer_cache_shape* shape, const void* cache, const xfer
  * slots of a call must differ (-1 and others outside the cache apart).  Numbers
  * are rounded to nearest even, and to 6 * 2^125 where they are beyond it.
  * xfer_mxcache_load: as xfer_cache_load.
- * xfer_mxcache_attend: as xfer_cache_attend, but for two things.  Where a call is large
- * enough for tiles of 64 or 128 rows, the weights are rounded to one float16 number for
- * bfloat16 queries (off by 2^-11 of the weight at most, and 2^-32 of the row's largest)
- * and to two for float16 ones (2^-22), in each run of 64 tokens whose scale bytes lie in
- * 104 .. 135.  And what has to fit a float is the products of a query and a key,
- * scores, and up to 2^15 times the values of the tokens that a row sees (values times
- * tokens below 2^112). */
+ * xfer_mxcache_attend: as xfer_cache_attend, but what has to fit a float is the products
+ * of a query and a key, scores, and up to 256 times the values of the tokens that a row
+ * sees (values times tokens below 2^119).  For float16 queries in a call that is large enough
+ * for tiles of 64 or 128 rows it is 2^15 times the values (below 2^112), and in
+ * runs of 64 tokens whose scale bytes lie in 104 .. 135 a weight is the sum of two float16
+ * numbers (off by 2^-22 of it at most, and 2^-32 of the row's largest). */
 int xfer_mxcache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
 int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, const void* key, int64_t key_row,
                        int64_t key_head, const void* value, int64_t value_row, int64_t value_head,

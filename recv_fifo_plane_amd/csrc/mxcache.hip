@@ -942,14 +942,19 @@ struct Core4 {
 // writes the left operands to shared memory, each lane's sixteen bytes where it will
 // read them.
 //
-// Weights multiply the values as float16 numbers where the chunk's scale bytes lie in
-// 104 .. 135: code * 2^e is a float16 number, exactly, for e from -23 to 8.  A weight
-// is then off by half a step, 2^-11 of itself, or by 2^-25 where it is below float16's
-// normal numbers, 2^-32 of the row's largest: maxima lie 7 to 15 powers of two
-// above the reference, so weights reach 2^15.  That is an eighth of a bfloat16 output's own
-// rounding.  For float16 outputs a second number takes the rest (2^-22).  Their keys are
-// float16 numbers too under the same condition, and queries stay as they are.  Other
-// chunks take the bfloat16 numbers of few rows' attention.
+// Weights of bfloat16 queries are held as those of few rows' attention: two bfloat16 numbers
+// (off by 2^-16), relative to a reference that they are 256 times at most.
+//
+// Those of float16 queries, and keys and values, are float16 numbers where the chunk's scale
+// bytes lie in 104 .. 135: code * 2^e is one, exactly, for e from -23 to 8, and queries stay as
+// they are.  A rounded weight is then off by half a step, 2^-11 of itself, or by 2^-25
+// where it is below float16's normal numbers, 2^-32 of the row's largest: maxima
+// lie 7 to 15 powers of two above the reference, so weights reach 2^15.  A second number takes the
+// rest (2^-22).  Other chunks take bfloat16 numbers.
+//
+// Tried: one float16 number for bfloat16 queries.  Chunks take 82 us so and 96 with two numbers,
+// which cost as much in either type; but where values cancel the output is off by far more than
+// its own rounding, and whether a row is would depend on the call around it.
 //
 // What bounds it is instructions: a chunk of 64 tokens and 128 rows of 128 dims takes
 // about 4300 cycles (widening 800, scores 770, weights 1170, products 630, loads and
@@ -1068,26 +1073,24 @@ struct WideCodes {
       }
       fetch_words<false, 2>(vb + from.value_scale[p], vs[p]);
     });
+    if constexpr (QUERIES16) {
 #pragma unroll
-    for (int i = 0; i < kAll; ++i) {
-      const uint8_t* q = kb + from.all[i];
-      all[1][i] = *reinterpret_cast<const uint32_t*>(q + from.side);
-      if (QUERIES16) all[0][i] = *reinterpret_cast<const uint32_t*>(q);
+      for (int i = 0; i < kAll; ++i)
+#pragma unroll
+        for (int side = 0; side < 2; ++side)
+          all[side][i] = *reinterpret_cast<const uint32_t*>(kb + from.all[i] + side * from.side);
     }
   }
 
-  // Whether all scales of a side of tokens that some row sees are float16's.
-  __device__ __forceinline__ bool float16(int side, uint32_t t0, uint32_t seen, uint32_t n) const {
+  // Whether all scales of tokens that some row sees are float16's.
+  __device__ __forceinline__ bool float16(uint32_t t0, uint32_t seen, uint32_t n) const {
     bool ok = true;
-    if (t0 + kChunk <= seen) {
+    const int32_t left = static_cast<int32_t>(seen) - static_cast<int32_t>(t0 + 16 * (n >> 2) + 4 * (n & 3u));
+    const uint32_t mask = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
 #pragma unroll
-      for (int i = 0; i < kAll; ++i) ok &= float16_scales(all[side][i]);
-    } else {
-      const int32_t left = static_cast<int32_t>(seen) - static_cast<int32_t>(t0 + 16 * (n >> 2) + 4 * (n & 3u));
-      const uint32_t mask = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    for (int side = 0; side < 2; ++side)
 #pragma unroll
       for (int i = 0; i < kAll; ++i) ok &= float16_scales((all[side][i] & mask) | (0x7F7F7F7Fu & ~mask));
-    }
     return __ballot(ok) == ~0ull;
   }
 
@@ -1181,6 +1184,10 @@ struct Wide {
   typedef WideShared<E, D, NR> Shared;
   static constexpr int kDim = D, kRows = 64 * NR, kThreads = kAttendWaves * 64, kResident = 2;
   static constexpr bool kHalfQueries = __is_same(E, fp16_t);
+  // What a lane's weights of a chunk may add up to before the reference follows the row's largest, how many
+  // powers of two above the reference that must be then, and how many it is afterwards.
+  static constexpr float kMost = kHalfQueries ? 32768.0f : 256.0f, kGrows = kHalfQueries ? 8.0f : 4.0f;
+  static constexpr float kAbove = kHalfQueries ? 7.0f : 0.0f;
   static constexpr int KL = D / 32, DT = D / 16, NB = wide_buffers(D);
 
   // Units of work of a tile of `rows` rows that sees `chunks` chunks: a chunk, or four where the
@@ -1264,7 +1271,7 @@ struct Wide {
       const typename WideCodes<D>::From from(A, h, g, n, wave);
       codes.template load<kHalfQueries>(A, at, from);
       auto fits = [&] {  // chunk c is one of float16 numbers
-        return codes.float16(1, c * kChunk, seen, n) && (!kHalfQueries || codes.float16(0, c * kChunk, seen, n));
+        return kHalfQueries && codes.float16(c * kChunk, seen, n);
       };
       // The chunks from c on in float16 numbers (HALF), up to one that does not fit, or in
       // bfloat16: the next chunk's codes are loaded while one is computed, and widened
@@ -1337,11 +1344,10 @@ struct Wide {
                     if (4 * t + r >= sees) s[x][t][r] = -INFINITY;
               }
             }
-            constexpr int kParts = HALF && !kHalfQueries ? 1 : 2;
             typedef typename std::conditional<HALF, fp16_t, bf16_t>::type W;
-            u32x4 p[kParts][NR][2];
+            u32x4 p[2][NR][2];  // the rounded weights, and the rounded rests
             // The reference m follows the row's largest score when a chunk's weights of a lane
-            // add up to more than 2^15, or when there is none yet; they are worked out again then.
+            // add up to more than kMost, or when there is none yet; they are worked out again then.
             // (a whole number: what is rescaled by it stays exact)
             //
             // A score times scale2 is not rounded before m is taken from it, but the maximum that m
@@ -1360,9 +1366,9 @@ struct Wide {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) top = fmaxf(top, s[x][t][r]);
                   top = max_of_groups(top) * A.scale2;
-                  const bool grows = top > m[x] + 8.0f;
+                  const bool grows = top > m[x] + kGrows;
                   const float was = m[x];
-                  if (grows) m[x] = __builtin_floorf(top) - 7.0f;
+                  if (grows) m[x] = __builtin_floorf(top) - kAbove;
                   const float keep = grows ? __builtin_amdgcn_exp2f(was - m[x]) : 1.0f;
                   l[x] *= keep;
 #pragma unroll
@@ -1386,12 +1392,11 @@ struct Wide {
                     const int i = (t & 1) * 2 + r / 2;
                     const W f0 = static_cast<W>(w0), f1 = static_cast<W>(w1);
                     p[0][x][t >> 1][i] = two_in_word(f0, f1);
-                    if constexpr (kParts == 2)
-                      p[kParts - 1][x][t >> 1][i] = two_in_word(static_cast<W>(w0 - static_cast<float>(f0)),
-                                                                static_cast<W>(w1 - static_cast<float>(f1)));
+                    p[1][x][t >> 1][i] = two_in_word(static_cast<W>(w0 - static_cast<float>(f0)),
+                                                     static_cast<W>(w1 - static_cast<float>(f1)));
                   }
                 const float more = sum[0] + sum[1];
-                if (!again && __ballot(more > 32768.0f) != 0) {
+                if (!again && __ballot(more > kMost) != 0) {
                   again = true;
                   continue;
                 }
@@ -1407,7 +1412,7 @@ struct Wide {
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int i = 0; i < kParts; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                   for (int x = 0; x < NR; ++x)
                     acc[x][e] = mfma_of<HALF>(ops[(2 * KL + e) % 3][j], p[i][x][j], acc[x][e]);
@@ -1419,7 +1424,9 @@ struct Wide {
           if (++c == c1 || (HALF && !fits())) return;
         }
       };
-      if (fits()) run(std::true_type());
+      if constexpr (kHalfQueries) {
+        if (fits()) run(std::true_type());
+      }
       if (c < c1) run(std::false_type());
     }
     // (a wave's own share of the values' NaN tells of them all: their tokens are looked for again)
