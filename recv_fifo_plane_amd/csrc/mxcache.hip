@@ -950,7 +950,11 @@ struct Core4 {
 // they are.  A rounded weight is then off by half a step, 2^-11 of itself, or by 2^-25
 // where it is below float16's normal numbers, 2^-32 of the row's largest: maxima
 // lie 7 to 15 powers of two above the reference, so weights reach 2^15.  A second number takes the
-// rest (2^-22).  Other chunks take bfloat16 numbers.
+// rest (2^-22).  Other chunks take bfloat16 numbers, in a pass of their own behind the first: a
+// store of zeros has a scale byte of 9, and with one such token in each request 5 prompts take
+// 144 us; 246 where all behind it went on in bfloat16 numbers, 132 without it.  If no chunk is of float16
+// numbers the first pass is in vain (270 and not 248).  (In one pass registers spill: the accumulators
+// are held twice where two loops may each follow the other.)
 //
 // Tried: one float16 number for bfloat16 queries.  Chunks take 82 us so and 96 with two numbers,
 // which cost as much in either type; but where values cancel the output is off by far more than
@@ -1149,7 +1153,7 @@ struct WideCodes {
   }
 
   // Writes the operands of the wave's share.
-  template <bool HALFK, bool HALFV>
+  template <bool HALF>
   __device__ __forceinline__ void widen(u32x4 (*tile)[64], uint32_t lane, uint32_t wave, int32_t held,
                                         uint32_t& nans) {
     constexpr int KL = D / 32, DT = D / 16;
@@ -1159,15 +1163,15 @@ struct WideCodes {
       const float scale = power_of(ks[j < kFirst ? 0 : part_count(D) - 1], 0);
       u32x4 a;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = two_of<HALFK>(k[j], i, scale);
+      for (int i = 0; i < 4; ++i) a[i] = two_of<HALF>(k[j], i, scale);
       tile[wave * KL + j][lane] = a;
     }
-    mask<HALFV>(wave, held, nans);
+    mask<HALF>(wave, held, nans);
     u32x4(*out)[64] = tile + 4 * KL + (wave >> 1) * DT;
     if (wave & 1u)
-      widen_values<HALFV, 1>(out, lane);
+      widen_values<HALF, 1>(out, lane);
     else
-      widen_values<HALFV, 0>(out, lane);
+      widen_values<HALF, 0>(out, lane);
   }
 };
 
@@ -1262,36 +1266,40 @@ struct Wide {
     uint32_t nans = 0;
 
     if (c0 < c1) {  // (so seen > 0)
-      WideCodes<D> codes;
-      Place at, next, then;  // of the chunk that codes hold, and the two behind it
-      uint32_t c = c0;
-      at.look(A, table, c * kChunk, seen, g, n);
-      next.look(A, table, (c + 1) * kChunk, seen, g, n);
-      at.settle(A, c * kChunk, seen, g);
       const typename WideCodes<D>::From from(A, h, g, n, wave);
-      codes.template load<kHalfQueries>(A, at, from);
-      auto fits = [&] {  // chunk c is one of float16 numbers
-        return kHalfQueries && codes.float16(c * kChunk, seen, n);
-      };
-      // The chunks from c on in float16 numbers (HALF), up to one that does not fit, or in
-      // bfloat16: the next chunk's codes are loaded while one is computed, and widened
-      // behind it, into the other buffer where there are two.
-      auto run = [&](auto float16) {
-        constexpr bool HALF = decltype(float16)::value, HALFK = HALF && kHalfQueries;
-        for (;;) {
+      uint32_t odd0 = ~0u, odd1 = 0, turn = 0;  // chunks that are not of float16 numbers lie in odd0 .. odd1 - 1
+      // The chunks c .. end - 1 that are of float16 numbers (HALF), or those that are not: the next
+      // chunk's codes are loaded while one is computed, and widened behind it, into the other
+      // buffer where there are two.
+      auto run = [&](auto float16, uint32_t c, uint32_t end) {
+        constexpr bool HALF = decltype(float16)::value;
+        WideCodes<D> codes;
+        Place at, next, then;  // of the chunk that codes hold, and the two behind it
+        at.look(A, table, c * kChunk, seen, g, n);
+        next.look(A, table, (c + 1) * kChunk, seen, g, n);
+        at.settle(A, c * kChunk, seen, g);
+        codes.template load<kHalfQueries>(A, at, from);
+        for (; c < end; ++c) {
           const uint32_t t0 = c * kChunk;
           const int32_t tg = t0 + 16 * g, bg = at.mine;
-          u32x4(*tile)[64] = sh.tile[NB == 2 ? c & 1u : 0];
-          if constexpr (NB == 1) __syncthreads();
-          uint32_t to = lane;
-          asm volatile("" : "+v"(to));  // (as `own` below)
-          codes.template widen<HALFK, HALF>(tile, to, wave, bg < 0 ? 0 : static_cast<int32_t>(seen) - tg, nans);
-          __syncthreads();
+          u32x4(*tile)[64] = sh.tile[NB == 2 ? turn & 1u : 0];
+          const bool here = !kHalfQueries || codes.float16(t0, seen, n) == HALF;  // (the same for all waves)
+          if (here) {
+            if constexpr (NB == 1) __syncthreads();
+            uint32_t to = lane;
+            asm volatile("" : "+v"(to));  // (as `own` below)
+            codes.template widen<HALF>(tile, to, wave, bg < 0 ? 0 : static_cast<int32_t>(seen) - tg, nans);
+            __syncthreads();
+            ++turn;
+          } else if (HALF) {
+            odd0 = min(odd0, c);
+            odd1 = c + 1;
+          }
           next.settle(A, t0 + kChunk, seen, g);
           codes.template load<kHalfQueries>(A, next, from);
           then.look(A, table, t0 + 2 * kChunk, seen, g, n);
           __builtin_amdgcn_sched_barrier(0);
-          if (static_cast<int32_t>(t0) <= last) {
+          if (here && static_cast<int32_t>(t0) <= last) {
             f32x4 s[NR][4];
 #pragma unroll
             for (int x = 0; x < NR; ++x)
@@ -1318,7 +1326,7 @@ struct Wide {
 #pragma unroll
               for (int x = 0; x < NR; ++x) {
                 hi[x] = q[x][i / 2];
-                if constexpr (kHalfQueries && !HALFK) {
+                if constexpr (kHalfQueries && !HALF) {
                   asm volatile("" : "+v"(hi[x]));  // (not to be kept in two parts from chunk to chunk)
                   two_parts(hi[x], hi[x], lo[x]);
                 }
@@ -1328,8 +1336,8 @@ struct Wide {
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
                   f32x4& to = s[x][2 * (i & 1) + j];
-                  if constexpr (kHalfQueries && !HALFK) to = mfma_of<false>(ops[i % 3][j], lo[x], to);
-                  to = mfma_of<HALFK>(ops[i % 3][j], hi[x], to);
+                  if constexpr (kHalfQueries && !HALF) to = mfma_of<false>(ops[i % 3][j], lo[x], to);
+                  to = mfma_of<HALF>(ops[i % 3][j], hi[x], to);
                 }
               __builtin_amdgcn_sched_barrier(0);
             }
@@ -1421,13 +1429,14 @@ struct Wide {
           }
           at = next;
           next = then;
-          if (++c == c1 || (HALF && !fits())) return;
         }
       };
       if constexpr (kHalfQueries) {
-        if (fits()) run(std::true_type());
+        run(std::true_type(), c0, c1);
+        if (odd0 < odd1) run(std::false_type(), odd0, odd1);
+      } else {
+        run(std::false_type(), c0, c1);
       }
-      if (c < c1) run(std::false_type());
     }
     // (a wave's own share of the values' NaN tells of them all: their tokens are looked for again)
     const bool any_nan = __syncthreads_or(nans != 0) != 0;
