@@ -975,6 +975,7 @@ struct WideShared {
     u32x4 tile[wide_buffers(D)][kKeys + kValues][64];
     Shared4<E, D> few;
   };
+  uint32_t nans[kAttendWaves];  // whether a wave met a value that is not a number
 };
 
 // Whether all of a word's four scales lie within 104 .. 135 (2^-23 .. 2^8): 24 is added to each
@@ -1086,11 +1087,13 @@ struct WideCodes {
     }
   }
 
-  // Whether all scales of tokens that some row sees are float16's.
-  __device__ __forceinline__ bool float16(uint32_t t0, uint32_t seen, uint32_t n) const {
+  // Whether all scales of tokens that some row sees are float16's.  mine: the block of the lane's sixteen
+  // tokens from 16 g on (below 0: none, and no row sees them; what was loaded in their place is of block 0).
+  __device__ __forceinline__ bool float16(uint32_t t0, uint32_t seen, uint32_t n, int32_t mine) const {
     bool ok = true;
     const int32_t left = static_cast<int32_t>(seen) - static_cast<int32_t>(t0 + 16 * (n >> 2) + 4 * (n & 3u));
-    const uint32_t mask = left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+    const bool none = (__ballot(mine < 0) >> (16 * (n >> 2)) & 1) != 0;
+    const uint32_t mask = none || left <= 0 ? 0u : left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
 #pragma unroll
     for (int side = 0; side < 2; ++side)
 #pragma unroll
@@ -1283,7 +1286,7 @@ struct Wide {
           const uint32_t t0 = c * kChunk;
           const int32_t tg = t0 + 16 * g, bg = at.mine;
           u32x4(*tile)[64] = sh.tile[NB == 2 ? turn & 1u : 0];
-          const bool here = !kHalfQueries || codes.float16(t0, seen, n) == HALF;  // (the same for all waves)
+          const bool here = !kHalfQueries || codes.float16(t0, seen, n, bg) == HALF;  // (the same for all waves)
           if (here) {
             if constexpr (NB == 1) __syncthreads();
             uint32_t to = lane;
@@ -1439,7 +1442,11 @@ struct Wide {
       }
     }
     // (a wave's own share of the values' NaN tells of them all: their tokens are looked for again)
-    const bool any_nan = __syncthreads_or(nans != 0) != 0;
+    const bool some = __ballot(nans != 0) != 0;
+    if (lane == 0) sh.nans[wave] = some;
+    __syncthreads();
+    bool any_nan = false;
+    for (int w = 0; w < kAttendWaves; ++w) any_nan |= sh.nans[w] != 0;
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const uint32_t i = mine + x * 16 + n;
