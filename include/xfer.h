@@ -483,7 +483,8 @@ int xfer_cache_attend(const xfer_cache_shape* shape, const void* cache, const xf
  * of no request are left as they were.  The rows and heads of an output must not
  * overlap, nor an output anything else of the call.
  * Errors: INVALID_ARG (sizes outside their domains: batch below 2^27; NULL or
- * misaligned buffers, strides that let an output's rows or heads overlap), HIP. */
+ * misaligned buffers, strides that let an output's rows or heads overlap, outputs
+ * of the same strides that overlap one another), HIP. */
 typedef struct {
   void* key;   /* [rows][H][D] of dtype */
   void* value; /* [rows][H][D] of dtype */

@@ -312,8 +312,8 @@ class PagedCache:
         which those rows are the last, as in attend: a plan's starts give the
         tokens that it added, sums of the lengths whole contexts.  table: int32
         [batch, width].  out: (key, value) to write into (any strides of rows and
-        heads), else new tensors.  Tokens that the table lacks give 0; rows of no
-        request are left as they were (without `out`: undefined)."""
+        heads, but no memory in common), else new tensors.  Tokens that the table
+        lacks give 0; rows of no request are left as they were (without `out`: undefined)."""
         kinds = _kinds()
         rows = int(rows)
         if rows < 0:

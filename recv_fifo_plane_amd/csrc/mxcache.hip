@@ -1716,6 +1716,27 @@ extern "C" int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, co
 
 namespace {
 
+// Whether the vectors of `inner` elements, n0 times n1 of them with strides s0 and s1, of two places share
+// elements; the second's are `apart` elements behind the first's.  A vector of one is x + r s0 behind one
+// of the other for an r between -n0 and n0, x = apart + h s1 for an h between -n1 and n1: it
+// is asked of every h whether the r's that come nearest to x + r s0 = 0 are near enough.
+bool places_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner, int64_t apart) {
+  typedef __int128 wide;
+  if (n1 > n0) {
+    std::swap(n0, n1);
+    std::swap(s0, s1);
+  }
+  for (int64_t h = 1 - n1; h < n1; ++h) {
+    const wide x = wide(apart) + wide(h) * s1;
+    const wide near = s0 ? -x / s0 : 0;
+    for (wide r = near - 1; r <= near + 1; ++r) {
+      const wide at = std::min<wide>(std::max<wide>(r, 1 - n0), n0 - 1), off = x + at * s0;
+      if (off < inner && -off < inner) return true;
+    }
+  }
+  return false;
+}
+
 int load_call(const Shape& s, int bits, const void* cache, const xfer_load* q, void* stream, const char* who) {
   const std::string w(who);
   if (!q) return fail(XFER_ERR_INVALID_ARG, w + ": NULL arguments");
@@ -1736,6 +1757,11 @@ int load_call(const Shape& s, int bits, const void* cache, const xfer_load* q, v
   if (vectors_overlap(q->rows, q->key_row, s.H, q->key_head, s.D) ||
       vectors_overlap(q->rows, q->value_row, s.H, q->value_head, s.D))
     return fail(XFER_ERR_INVALID_ARG, w + ": the rows and heads of an output must not overlap");
+  if ((q->rows == 1 || q->key_row == q->value_row) && (s.H == 1 || q->key_head == q->value_head) &&
+      places_overlap(q->rows, q->key_row, s.H, q->key_head, s.D,
+                     (int64_t(reinterpret_cast<uintptr_t>(q->value)) - int64_t(reinterpret_cast<uintptr_t>(q->key))) /
+                         int64_t(size)))
+    return fail(XFER_ERR_INVALID_ARG, w + ": the key's and the value's output must not overlap");
   LoadArgs a;
   a.cache = static_cast<const uint8_t*>(cache);
   a.key = q->key;
