@@ -325,12 +325,12 @@ class PagedCache:
         at_starts = _list(starts, "load: starts", batch + 1, self.device)
         at_table, stride, width = _table(table, "load: table", batch, self.device)
         shape = (rows, self.kv_heads, self.head_dim)
+        if dtype is not None and dtype not in kinds:
+            raise TypeError("load: unsupported dtype %s" % (dtype,))
         if out is None:
             if dtype is None:
                 import torch
                 dtype = torch.bfloat16
-            if dtype not in kinds:
-                raise TypeError("load: unsupported dtype %s" % (dtype,))
             side = None if stream is None else _side(stream, self.device)
             out = tuple(self.buffer.new_empty(shape, dtype=dtype) if side is None
                         else _empty(self.buffer, shape, dtype, side) for _ in range(2))
