@@ -1722,6 +1722,8 @@ namespace {
 // is asked of every h whether the r's that come nearest to x + r s0 = 0 are near enough.
 bool places_overlap(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner, int64_t apart) {
   typedef __int128 wide;
+  const wide reach = (n0 - 1) * (s0 < 0 ? -wide(s0) : wide(s0)) + (n1 - 1) * (s1 < 0 ? -wide(s1) : wide(s1)) + inner;
+  if (apart >= reach || -wide(apart) >= reach) return false;  // (separate tensors, mostly)
   if (n1 > n0) {
     std::swap(n0, n1);
     std::swap(s0, s1);
