@@ -29,13 +29,6 @@ __device__ __forceinline__ uint64_t scales_at(const Shape& s, uint32_t block, ui
   return block * s.block_bytes + 2ull * s.H * s.T * s.D + 8u * h;
 }
 
-int shape8_of(const xfer_cache_shape* g, const char* who, Shape* out) {
-  const int rc = shape_of(g, who, out);
-  if (rc) return rc;
-  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
-  return XFER_OK;
-}
-
 // -------------------------------------------------------------------- plan
 struct PlanArgs {
   const int32_t* cached;
@@ -595,6 +588,7 @@ __device__ __forceinline__ void widen(uint32_t lo, uint32_t hi, float scale, fp1
   r = fp16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// The dims of lane group g in step k of 32: sixteen-byte loads of the keys
 // serve two steps where D allows.
 template <int D>
 __device__ __forceinline__ uint32_t key_dim(uint32_t k, uint32_t g) {

@@ -170,7 +170,7 @@ struct Place {
   }
 };
 
-// The dims of lane group g in step k of 32: sixteen-byte loads of the keys
+// A load of the cache.  ONCE: no other workgroup reads the same bytes, so the caches need not keep them.
 template <bool ONCE, typename V>
 __device__ __forceinline__ V fetch(const uint8_t* p) {
   if constexpr (ONCE)
@@ -178,7 +178,6 @@ __device__ __forceinline__ V fetch(const uint8_t* p) {
   else
     return *reinterpret_cast<const V*>(p);
 }
-
 
 // One workgroup per tile of rows and key/value head.  The last tiles see most
 // tokens and are begun first: with 32 heads of 128 over 8, 8 requests of 3000 to
@@ -363,7 +362,6 @@ struct AttendKernels {
   int threads;  // of a workgroup but of join's
 };
 
-
 // The kernels of a core; P: the core of the tiles that are numbered.
 template <class C, class P, bool SHARED>
 AttendKernels attend_kernels() {
@@ -423,6 +421,14 @@ int shape_of(const xfer_cache_shape* g, const char* who, Shape* out) {
   return XFER_OK;
 }
 
+// The shape of a cache of 8 bits: codes, and a float pair of scales for each head.
+int shape8_of(const xfer_cache_shape* g, const char* who, Shape* out) {
+  const int rc = shape_of(g, who, out);
+  if (rc) return rc;
+  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
+  return XFER_OK;
+}
+
 // Whether vectors of `inner` elements, n0 times n1 of them with strides s0 and s1,
 // may share elements: they do not where the vectors of one dimension follow one
 // another and those of the other lie behind them all.
@@ -461,8 +467,8 @@ int attend_args(const Shape& s, const xfer_attend* q, const char* who) {
   return XFER_OK;
 }
 
-// A call of attention: its checks, its workspace, its launches.  plan: the launch's
-// shape; once: no other workgroup reads the same tokens; kernels(dtype, plan).
+// A call of attention: its checks, its workspace, its launches.  p: the launch's shape;
+// pick(dtype, p): its kernels.
 template <typename Pick>
 int attend_call(const Shape& s, const void* cache, const xfer_attend* q, const AttendPlan& p, Pick pick,
                 void* stream, const char* who) {

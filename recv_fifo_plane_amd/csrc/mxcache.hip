@@ -10,9 +10,9 @@
 // storing one never touches another's, whatever the order of the rows, and
 // nothing is rounded twice.
 //
-// Keys lie as [T][D / 2], dim 2j in the lower half of byte j: sixteen bytes are 32
-// dims of a token, which is what a lane of the matrix instruction's left operand takes
-// of a head of 128, with one scale.  Values lie in parts of 128, 64 or 32 dims as
+// Keys lie as [T][D / 2], dim 2j in the lower half of byte j: sixteen bytes are 32 dims
+// of a token, a quarter of a head of 128, which a lane loads at once and widens with one scale for
+// four products of 32 dims.  Values lie in parts of 128, 64 or 32 dims as
 // D is made of (96 = 64 + 32, 192 = 128 + 64): a sixteenth of the part's dims, b = 4,
 // 2 or 1 bytes, of u = 16 / b tokens together, [T / u][16][u][b].  A lane then loads
 // sixteen tokens of its dims in pieces of sixteen bytes, and one scale serves all
@@ -52,13 +52,6 @@ int shape4_of(const xfer_cache_shape* g, const char* who, Shape* out) {
   if (rc) return rc;
   const uint64_t codes = uint64_t(out->H) * out->T * out->D;
   out->block_bytes = codes + ((codes / 16 + 127) & ~127ull);
-  return XFER_OK;
-}
-
-int shape8_of(const xfer_cache_shape* g, const char* who, Shape* out) {
-  const int rc = shape_of(g, who, out);
-  if (rc) return rc;
-  out->block_bytes = 2ull * out->H * out->T * out->D + ((8ull * out->H + 127) & ~127ull);
   return XFER_OK;
 }
 
@@ -1632,23 +1625,27 @@ AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   const int64_t width = int64_t(q.table_width) * s.T;
   const int64_t tokens = q.max_length ? std::min<int64_t>(q.max_length, width) : width;
   const int64_t chunks = std::max<int64_t>(1, (tokens + kChunk - 1) / kChunk);
-  // Tiles of 16 rows until there is work for many rows' tiles to fill the device twice
-  // over: 16 requests of 15 rows over 2000 tokens take 23 us so and 39 with many rows'
-  // tiles, 2 of 1000 over 1000 take 58 and 38.  They cost more per row the wider the
+  // Tiles of 16 rows until there is work for many rows' tiles, two of whose workgroups a CU
+  // holds: 14 chunks of 128 rows for each of 512 workgroups, or 12 of 64 rows of wide heads (units are
+  // chunks of 16 rows).  16 requests of 15 rows over 2000 tokens take 23 us so and 39 with many
+  // rows' tiles, 2 of 1000 over 1000 take 58 and 38.  They cost more per row the wider the
   // heads: 64 requests of 15 rows over 2000 tokens of 256 dims take 125 and 85.  32 rows of a
   // request stay with them in any case (64 requests of up to 28, 8000 tokens: 57 and 71).
   const int64_t units = int64_t(q.rows) * group / 16 * s.H * chunks;
-  const bool wide = rows > 32 && units > (d <= 128 ? 57344 : 24576);
+  const bool wide = rows > 32 && units > 512 * (d <= 128 ? 14 * 8 : 12 * 4);
   p.tile = wide ? 64 * wide_tiles(d) : 16;
   p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;
   const int64_t numbers = int64_t(q.rows) * group / p.tile + q.batch;
   const int64_t resident = 256 * (wide ? 2 : attend4_resident(d));
-  // Equal shares of all work cost a join of the tiles that they cut (25 us where many rows' tiles
-  // are cut), a workgroup per tile leaves the device waiting for the longest tile (1.6 us a chunk).
-  // Many rows: 8 chunks of prompts up to 5000 tokens take 82 us in shares and 135 by
-  // tiles, 2 prompts of 1000 tokens 61 and 38.  Few rows: 64 requests of up to 8000 tokens take
-  // 57 and 76, 48 of up to 3000 (12 heads over 2) 24 and 19.
+  // Equal shares of all work cost a join of the tiles that they cut, a workgroup per tile leaves the device
+  // waiting for the longest tile.  Many rows: that one takes `chunks` (1.6 us each), while a
+  // share of equal ones takes half of its part of all chunks, as tiles of a prompt see half of
+  // its tokens, and 19 chunks' time (30 us) for the join and what its tiles begin with: 8 chunks of
+  // prompts up to 5000 tokens take 82 us in shares and 135 by tiles, 2 prompts of 1000 tokens 61 and
+  // 38.  Few rows: a join takes as long as 24 chunks in four waves, or 64 where 128 workgroups or more
+  // overlap the longest, and is not worth it where each place of the device has 12 tiles to even out: 64
+  // requests of up to 8000 tokens take 57 and 76, 48 of up to 3000 (12 heads over 2) 24 and 19.
   const int64_t share = int64_t(q.rows) * group / p.tile * s.H * chunks / resident;
   const bool shares = wide ? chunks > share / 2 + 19
                            : chunks >= (wgs <= 128 ? 24 : 64) && !(most > 1 && numbers * s.H > 12 * resident);
