@@ -1628,11 +1628,12 @@ AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   // Tiles of 16 rows until there is work for many rows' tiles, two of whose workgroups a CU
   // holds: 14 chunks of 128 rows for each of 512 workgroups, or 12 of 64 rows of wide heads (units are
   // chunks of 16 rows).  16 requests of 15 rows over 2000 tokens take 23 us so and 39 with many
-  // rows' tiles, 2 of 1000 over 1000 take 58 and 38.  They cost more per row the wider the
-  // heads: 64 requests of 15 rows over 2000 tokens of 256 dims take 125 and 85.  32 rows of a
-  // request stay with them in any case (64 requests of up to 28, 8000 tokens: 57 and 71).
+  // rows' tiles, 2 of 1000 over 1000 take 57 and 43.  They cost more per row the wider the
+  // heads.  A request that fills half of one of those tiles or less stays with them in any case: 64
+  // requests over 500 to 8000 tokens take 57 and 71 with 28 rows of 128 dims, 126 and 144 with 60, 173
+  // and 150 with 80; with 60 rows of 256 dims 234 and 186.
   const int64_t units = int64_t(q.rows) * group / 16 * s.H * chunks;
-  const bool wide = rows > 32 && units > 512 * (d <= 128 ? 14 * 8 : 12 * 4);
+  const bool wide = rows > 32 * wide_tiles(d) && units > 512 * (d <= 128 ? 14 * 8 : 12 * 4);
   p.tile = wide ? 64 * wide_tiles(d) : 16;
   p.tiles = uint32_t(std::min<int64_t>(65535, (rows + p.tile - 1) / p.tile));
   const int64_t wgs = int64_t(q.batch) * s.H * p.tiles;

@@ -65,3 +65,12 @@ def test_few_rows(dtype, kernels):
     assert are(kernels[0], ("attend_kernel", "5Core4")), kernels[0]
     assert are(kernels[1], ("attend_flat_kernel", "5Core4"), ("join_kernel", None)), kernels[1]
     assert are(kernels[2], ("attend_packed_kernel", "5Core4")), kernels[2]
+
+
+@pytest.mark.parametrize("D", DIMS)
+def test_requests_of_half_a_tile(D, kernels):
+    """However long, 64 rows of a request (32 of wide heads) are few; one more are many."""
+    most = 64 if D <= 128 else 32
+    for rows in (most, most + 1):
+        check_attend([300], [rows], 16, 2, 1, D, seed=D, many=0)
+    assert "5Core4" in kernels[0][0] and "4Wide" in kernels[1][0], kernels
