@@ -530,7 +530,8 @@ int xfer_cache_load(const xfer_cache_shape* shape, const void* cache, const xfer
  * sees (values times tokens below 2^119).  For float16 queries in a call that is large enough
  * for tiles of 64 or 128 rows it is 2^15 times the values (below 2^112), and in
  * runs of 64 tokens whose scale bytes lie in 104 .. 135 a weight is the sum of two float16
- * numbers (off by 2^-22 of it at most, and 2^-32 of the row's largest). */
+ * numbers (off by 2^-22 of it at most, and 2^-32 of the row's largest).  A value that is not
+ * finite costs rows that see it time as well: they look for such tokens one by one. */
 int xfer_mxcache_block_bytes(const xfer_cache_shape* shape, size_t* bytes);
 int xfer_mxcache_store(const xfer_cache_shape* shape, void* cache, const void* key, int64_t key_row,
                        int64_t key_head, const void* value, int64_t value_row, int64_t value_head,

@@ -303,7 +303,8 @@ constexpr int kJoinThreads = 256;
 // that of the tile which share w begins and later ones go on with, D / 4
 // threads for a row, the shares in order, so the result does not depend on
 // when they were done.  Bound by latency: 4.6 us behind 64 requests' decode
-// step, 9.4 where 2 long ones are spread over 512 workgroups, 6.8 for chunks.
+// step, 9.4 where 2 long ones are spread over 512 workgroups, 6.8 for chunks in tiles of 32
+// rows, 15 in tiles of 128.
 template <typename E, int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs A) {
   constexpr uint32_t kWide = D / 4, kGroups = kJoinThreads / kWide, kRows = ROWS;

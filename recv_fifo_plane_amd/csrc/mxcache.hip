@@ -199,9 +199,10 @@ constexpr int kStoreThreads = 256, kStoreEach = 2, kStoreRows = 16;
 // fills whole lines; a workgroup takes the next kStoreEach * 256 pieces of eight.
 //
 // What bounds it is memory: the rows of 29 prompts, 54 M numbers of 16 bits, are stored in
-// 22.7 us, 6.0 TB/s read and written (a large copy of new data reaches 5.3).  Row by row it
-// took 29.9 (values of four tokens share a line, scales of 64: 63 MB written for
-// 29), with one piece a thread 3 more.
+// 23 us where they lie in the Infinity Cache (5.9 TB/s read and written).  New data, stored and
+// read back by load_kernel, take 55 us for 272 MB, 5.0 TB/s (a large copy: 5.3).  Row by row the store
+// alone took 30 (values of four tokens share a line, scales of 64: 63 MB written for
+// 29), with one piece a thread both 54 and not 50 on data near at hand.
 template <typename E, int D>
 __global__ void __launch_bounds__(kStoreThreads) store4_kernel(Store4Args A) {
   constexpr uint32_t W = D / 8, kSide = kStoreRows * W;  // pieces of a row, of a tile's head and side
@@ -394,10 +395,10 @@ struct Quad<8, D> {
 // cache is read as block 0, and its rows are zeros: a branch around the loads would
 // make the second wait for the first.)
 //
-// What bounds it is memory, four fifths of it the rows written: 52 us for 24 prefixes of up to
-// 9001 tokens from 4 bits (5.3 TB/s), 54 us for 17 of up to 12001 from 8 (4.4).  With
-// one load a thread in flight they took 71 and 63 us; one call of 300 tokens then takes 3.9 us
-// and now 4.2.
+// What bounds it is memory, four fifths of it the rows written: 24 prefixes of up to 9001 tokens
+// from 4 bits, 300 MB, take 61 us (4.9 TB/s) of new data and 52 (5.7) of data in the Infinity
+// Cache, 17 of up to 12001 from 8, 255 MB, 73 (3.5) and 53 (4.8).  With one load a thread in
+// flight the latter take 20 and 9 us more.
 template <int BITS, typename E, int D>
 __global__ void __launch_bounds__(kLoadThreads) load_kernel(LoadArgs A) {
   constexpr uint32_t W = D / 8;
@@ -949,14 +950,14 @@ struct Core4 {
 // numbers the first pass is in vain (270 and not 248).  (In one pass registers spill: the accumulators
 // are held twice where two loops may each follow the other.)
 //
-// Tried: one float16 number for bfloat16 queries.  Chunks take 82 us so and 96 with two numbers,
+// Tried: one float16 number for bfloat16 queries.  Chunks take 76 us so and 87 with two numbers,
 // which cost as much in either type; but where values cancel the output is off by far more than
 // its own rounding, and whether a row is would depend on the call around it.
 //
-// What bounds it is instructions: a chunk of 64 tokens and 128 rows of 128 dims takes
-// about 4300 cycles (widening 800, scores 770, weights 1170, products 630, loads and
-// barriers the rest).  8 chunks of prompts over up to 5000 tokens take 76 us, 5 prompts of
-// up to 2900 tokens 125.  Tried and slower: the next chunk widened between this one's products (in
+// What bounds it is instructions: with one number a weight a chunk of 64 tokens and 128 rows of 128
+// dims took about 4300 cycles (widening 800, scores 770, weights 1170, products 630, loads and
+// barriers the rest); the second number's products are 630 more.  8 chunks of prompts over up to
+// 5000 tokens take 86 us, 5 prompts of up to 2900 tokens 123.  Tried and slower: the next chunk widened between this one's products (in
 // the same wave), eight waves in two halves that take turns at widening and multiplying (88 and 235).
 constexpr int wide_tiles(int d) { return d <= 128 ? 2 : 1; }    // of 16 rows, of a wave
 constexpr int wide_buffers(int d) { return d <= 128 ? 2 : 1; }  // of widened chunks
@@ -1193,7 +1194,7 @@ struct Wide {
   // Units of work of a tile of `rows` rows that sees `chunks` chunks: a chunk, or four where the
   // waves of few rows' attention take one each, and two for what a tile takes besides
   // (its queries, its first loads, its result).  With shares of equal chunks 5 prompts of up
-  // to 2900 tokens took 179 us and with these 150; four units and not two: 153.
+  // to 2900 tokens take 178 us in shares and with these 150; four units and not two: 153.
   static constexpr uint32_t kFixed = 2;
   static __device__ __forceinline__ uint32_t unit(uint32_t rows) { return rows <= 16 ? kAttendWaves : 1; }
   static __device__ __forceinline__ uint32_t units(uint32_t rows, uint32_t chunks) {
@@ -1643,8 +1644,8 @@ AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   // waiting for the longest tile.  Many rows: that one takes `chunks` (1.6 us each), while a
   // share of equal ones takes half of its part of all chunks, as tiles of a prompt see half of
   // its tokens, and 19 chunks' time (30 us) for the join and what its tiles begin with: 8 chunks of
-  // prompts up to 5000 tokens take 82 us in shares and 135 by tiles, 2 prompts of 1000 tokens 61 and
-  // 38.  Few rows: a join takes as long as 24 chunks in four waves, or 64 where 128 workgroups or more
+  // prompts up to 5000 tokens take 96 us in shares and 165 by tiles, 5 prompts up to 2900 tokens 150 and
+  // 127, 2 of 1000 tokens 66 and 43.  Few rows: a join takes as long as 24 chunks in four waves, or 64 where 128 workgroups or more
   // overlap the longest, and is not worth it where each place of the device has 12 tiles to even out: 64
   // requests of up to 8000 tokens take 57 and 76, 48 of up to 3000 (12 heads over 2) 24 and 19.
   const int64_t share = int64_t(q.rows) * group / p.tile * s.H * chunks / resident;
