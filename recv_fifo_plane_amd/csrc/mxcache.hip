@@ -946,9 +946,9 @@ struct Core4 {
 // lie 7 to 15 powers of two above the reference, so weights reach 2^15.  A second number takes the
 // rest (2^-22).  Other chunks take bfloat16 numbers, in a pass of their own behind the first: a
 // store of zeros has a scale byte of 9, and with one such token in each request 5 prompts take
-// 144 us; 246 where all behind it went on in bfloat16 numbers, 132 without it.  If no chunk is of float16
-// numbers the first pass is in vain (270 and not 248).  (In one pass registers spill: the accumulators
-// are held twice where two loops may each follow the other.)
+// 144 us; 246 where all behind it went on in bfloat16 numbers, 132 without it.  If no chunk is of
+// float16 numbers the first pass is in vain (270 and not 248).  (In one pass registers spill: the
+// accumulators are held twice where two loops may each follow the other.)
 //
 // Tried: one float16 number for bfloat16 queries.  Chunks take 76 us so and 87 with two numbers,
 // which cost as much in either type; but where values cancel the output is off by far more than
@@ -957,8 +957,9 @@ struct Core4 {
 // What bounds it is instructions: with one number a weight a chunk of 64 tokens and 128 rows of 128
 // dims took about 4300 cycles (widening 800, scores 770, weights 1170, products 630, loads and
 // barriers the rest); the second number's products are 630 more.  8 chunks of prompts over up to
-// 5000 tokens take 86 us, 5 prompts of up to 2900 tokens 123.  Tried and slower: the next chunk widened between this one's products (in
-// the same wave), eight waves in two halves that take turns at widening and multiplying (88 and 235).
+// 5000 tokens take 86 us, 5 prompts of up to 2900 tokens 123.  Tried and slower: the next chunk
+// widened between this one's products (in the same wave), eight waves in two halves that take turns
+// at widening and multiplying (88 and 235 us, where four took 81 and 179).
 constexpr int wide_tiles(int d) { return d <= 128 ? 2 : 1; }    // of 16 rows, of a wave
 constexpr int wide_buffers(int d) { return d <= 128 ? 2 : 1; }  // of widened chunks
 
@@ -1378,7 +1379,7 @@ struct Wide {
                   l[x] *= keep;
 #pragma unroll
                   for (int e = 0; e < DT; ++e) acc[x][e] *= keep;
-                  if (__ballot(!(fabsf(m[x]) < kFar)) != 0) {
+                  if (__ballot(fabsf(m[x]) >= kFar && m[x] != -INFINITY) != 0) {
                     mul = 1.0f;
 #pragma unroll
                     for (int t = 0; t < 4; ++t) s[x][t] *= A.scale2;
@@ -1644,10 +1645,11 @@ AttendPlan attend4_plan(const Shape& s, const xfer_attend& q) {
   // waiting for the longest tile.  Many rows: that one takes `chunks` (1.6 us each), while a
   // share of equal ones takes half of its part of all chunks, as tiles of a prompt see half of
   // its tokens, and 19 chunks' time (30 us) for the join and what its tiles begin with: 8 chunks of
-  // prompts up to 5000 tokens take 96 us in shares and 165 by tiles, 5 prompts up to 2900 tokens 150 and
-  // 127, 2 of 1000 tokens 66 and 43.  Few rows: a join takes as long as 24 chunks in four waves, or 64 where 128 workgroups or more
-  // overlap the longest, and is not worth it where each place of the device has 12 tiles to even out: 64
-  // requests of up to 8000 tokens take 57 and 76, 48 of up to 3000 (12 heads over 2) 24 and 19.
+  // prompts up to 5000 tokens take 96 us in shares and 165 by tiles, 5 prompts up to 2900 tokens 150
+  // and 127, 2 of 1000 tokens 66 and 43.  Few rows: a join takes as long as 24 chunks in four waves, or
+  // 64 where 128 workgroups or more overlap the longest, and is not worth it where each place of the
+  // device has 12 tiles to even out: 64 requests of up to 8000 tokens take 57 and 76, 48 of up to 3000
+  // (12 heads over 2) 24 and 19.
   const int64_t share = int64_t(q.rows) * group / p.tile * s.H * chunks / resident;
   const bool shares = wide ? chunks > share / 2 + 19
                            : chunks >= (wgs <= 128 ? 24 : 64) && !(most > 1 && numbers * s.H > 12 * resident);
